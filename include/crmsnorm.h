@@ -93,11 +93,18 @@ enum {
     CRMSN_OP_ADA_STYLE = 4,
     CRMSN_OP_GATED_ADA_FP8 = 5,
     CRMSN_OP_SILU = 6,
-    CRMSN_OP_LAYERNORM = 7
+    CRMSN_OP_LAYERNORM = 7,
+    CRMSN_OP_QK_ROPE = 8            /* the query / key functions: H is the head size */
 };
+/* Index types (positions, cache slots). */
+enum { CRMSN_I32 = 0, CRMSN_I64 = 1 };
+/* Element types of a key / value cache. */
+enum { CRMSN_CACHE_BF16 = 0, CRMSN_CACHE_E4M3 = 1, CRMSN_CACHE_E5M2 = 2 };
 
 /* Largest supported hidden size. */
 #define CRMSN_MAX_H 16384
+/* Largest supported head size of the query / key functions. */
+#define CRMSN_MAX_HEAD_DIM 512
 
 /*
  * rmsnorm_fwd -- [API] rmsnorm, gemma_rmsnorm, fused_add_rmsnorm,
@@ -349,6 +356,147 @@ crmsn_status layernorm_quant(void *out, int64_t ldo, int fp8_kind,
                              const float *scale, float eps,
                              int64_t T, int64_t H, float *mean, float *rstd,
                              cudaStream_t stream);
+
+/*
+ * ---- Queries and keys: rotary positions, per-head norms, cache ----
+ *
+ * Shared by the functions below ([API] fused_qk_rmsnorm_rope; [GUIDE] 5.2
+ * names the fusion; the formulas are stated here in full):
+ *   - Heads are BF16 [T, H, D] with a contiguous D, a token stride ld* and a
+ *     head stride hs* in ELEMENTS: slices of a packed projection, heads
+ *     beside an output gate (hs = 2 D), or [H, T, D] storage (ld = D,
+ *     hs = T*D).  Two heads of one tensor must not overlap: hs >= D, ld >= D
+ *     and ld >= (H-1)*hs + D or hs >= (T-1)*ld + D, else CRMSN_ERR_SHAPE.
+ *     D is even and at most CRMSN_MAX_HEAD_DIM.  k may be NULL with Hk = 0
+ *     (queries alone).
+ *   - wq, wk: [D], BF16 or FP32 (w_dtype) with weight_bias as in rmsnorm_fwd;
+ *     both NULL: no norm (the rotation alone; eps and weight_bias unused).
+ *   - cos_sin: FP32 [cs_rows, >= R] with row stride ldcs: R/2 cosines, then
+ *     R/2 sines, as rope_cos_sin writes them.  Token t uses row t % cs_rows;
+ *     T must be a multiple of cs_rows (a batch of sequences with the same
+ *     positions gives cs_rows = one sequence).  R is even, 0 <= R <= D;
+ *     R = 0: no rotation (cos_sin may be NULL).
+ *   - Column j turns the pair (j, j + R/2) (interleaved = 0) or
+ *     (2j, 2j + 1) (interleaved = 1); elements R .. D-1 are not rotated.
+ *   - FP32 throughout, one rounding to the output format.
+ *   - Fast form: D a multiple of 8, R of 16, BF16 bases, strides and cache
+ *     16-byte aligned (FP8 cache: 8-byte), FP32 weights and cos_sin rows
+ *     16-byte.  Anything else that is aligned to its own elements runs an
+ *     element-wise form with the same results up to the order of the sums.
+ */
+
+/*
+ * rope_cos_sin -- the cosines and sines of rotary positions on 1..4 axes
+ * (text; time, height and width of images and video), once for every layer.
+ *
+ *   cos_sin[t, j]       = f32(scaling * cos(p * inv_freq[j]))
+ *   cos_sin[t, R/2 + j] = f32(scaling * sin(p * inv_freq[j]))
+ *   p = positions[axis(j), t],  0 <= j < R/2
+ *
+ * positions: [n_axes, T] of I32 or I64 (pos_dtype) with axis stride ldp;
+ * negative positions are valid.  inv_freq: FP32 [R/2] on the device;
+ * |inv_freq| < 2^40 (columns beyond that, infinite or NaN give NaN).  The
+ * product p * inv_freq is reduced modulo 2 pi exactly (64-bit fractions of a
+ * turn): the angle is off by less than 2^-61 |p|, whatever inv_freq is.
+ * sections: HOST array of n_axes column counts >= 0 with sum R/2, or NULL
+ * with n_axes = 1.  interleaved_axes = 0: the columns of axis 0 come first,
+ * then those of axis 1, ...; interleaved_axes = 1: column j belongs to axis
+ * j % n_axes while that axis has columns left (j < n_axes * sections[axis]),
+ * else to axis 0 (CRMSN_ERR_SHAPE when an axis then has another count).
+ * T == 0 returns CRMSN_OK without a launch.
+ */
+crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp,
+                          int n_axes, const int32_t *sections,
+                          int interleaved_axes, const float *inv_freq,
+                          float scaling, int64_t T, int64_t R, float *cos_sin,
+                          int64_t ldcs, cudaStream_t stream);
+
+/*
+ * qk_rmsnorm_rope_fwd -- per row x of q (weight wq) and of k (weight wk):
+ *
+ *   n = (x * rstd) * w_eff,  rstd = 1 / sqrt(mean(x^2) + eps)
+ *   y_a = bf16(n_a * c - n_b * s),  y_b = bf16(n_b * c + n_a * s)
+ *
+ * on the rotated pairs (a, b), y = bf16(n) elsewhere.  In place: q_out == q
+ * and k_out == k (same pointer and strides) are allowed.
+ */
+crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_t Hq,
+                                 const void *k, int64_t ldk, int64_t hsk, int64_t Hk,
+                                 const void *wq, const void *wk, int w_dtype,
+                                 float weight_bias, float eps,
+                                 const float *cos_sin, int64_t ldcs, int64_t cs_rows,
+                                 int64_t R, int interleaved, int64_t T, int64_t D,
+                                 void *q_out, int64_t ldqo, int64_t hsqo,
+                                 void *k_out, int64_t ldko, int64_t hsko,
+                                 cudaStream_t stream);
+
+/*
+ * qk_rmsnorm_rope_bwd -- the gradient of qk_rmsnorm_rope_fwd: gq, gk are the
+ * gradients of q_out, k_out; q, k the forward's inputs (nothing else is kept
+ * from it: rstd is computed again).  With u = the transposed rotation of g:
+ *
+ *   dx = bf16(rstd * (u * w_eff - xhat * mean(u * w_eff * xhat))),  xhat = x * rstd
+ *   dw[j] = sum over the tensor's rows of u * xhat       (FP32, overwritten)
+ *
+ * Without weights dx = bf16(u); q, k, dwq, dwk and the workspace may then be
+ * NULL.  dw is added in a fixed order that depends on the sizes and the SM
+ * count alone (no atomics).  In place: dq == gq, dk == gk are allowed.
+ * workspace: at least qk_rmsnorm_rope_bwd_workspace_bytes(D, device) bytes,
+ * 256-byte aligned, any content; scratch that a later call on the same
+ * stream may use again (two calls that may run at the same time need two).
+ * T == 0 writes dwq = dwk = 0 and launches no kernel.
+ */
+crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq,
+                                 const void *gk, int64_t ldgk, int64_t hsgk,
+                                 const void *q, int64_t ldq, int64_t hsq, int64_t Hq,
+                                 const void *k, int64_t ldk, int64_t hsk, int64_t Hk,
+                                 const void *wq, const void *wk, int w_dtype,
+                                 float weight_bias, float eps,
+                                 const float *cos_sin, int64_t ldcs, int64_t cs_rows,
+                                 int64_t R, int interleaved, int64_t T, int64_t D,
+                                 void *dq, int64_t lddq, int64_t hsdq,
+                                 void *dk, int64_t lddk, int64_t hsdk,
+                                 float *dwq, float *dwk,
+                                 void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/* Bytes of workspace for head size D on `device`; 0 for an invalid D or device. */
+size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device);
+
+/*
+ * qk_rmsnorm_rope_append -- the serving form: q_out as in
+ * qk_rmsnorm_rope_fwd, and for the keys and values of token t
+ *
+ *   k_cache[slot] = the normed and rotated key,  v_cache[slot] = the value
+ *   (BF16, or fp8(x * (1 / scale)), rounded to nearest even and saturating)
+ *
+ * slot = slots[t] (I32 or I64): page slot / page_size, row slot % page_size.
+ * A token whose slot is negative or >= num_pages * page_size (padding) writes
+ * nothing to the cache; its q_out is still written.  Nothing but the slots
+ * named is written.  Slots must differ: if two tokens name one slot, each of
+ * its elements holds the value of either.  Caches: [num_pages, page_size, Hk,
+ * D] elements of cache_kind with page, slot and head strides (k: kps, kss,
+ * khs) in elements and contiguous D -- [num_pages, Hk, page_size, D] storage
+ * is kss = D, khs = page_size * D.  k_scale, v_scale: device FP32 [1] > 0,
+ * FP8 caches only (else NULL).  q may be NULL with Hq = 0 (the cache alone).
+ * In place: q_out == q is allowed.  An overlap of an output with another
+ * tensor returns CRMSN_ERR_ALIAS (k_cache and v_cache may interleave in one
+ * buffer).  num_pages * page_size < 2^31.
+ */
+crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int64_t Hq,
+                                    const void *k, int64_t ldk, int64_t hsk,
+                                    const void *v, int64_t ldv, int64_t hsv, int64_t Hk,
+                                    const void *wq, const void *wk, int w_dtype,
+                                    float weight_bias, float eps,
+                                    const float *cos_sin, int64_t ldcs, int64_t cs_rows,
+                                    int64_t R, int interleaved, int64_t T, int64_t D,
+                                    void *q_out, int64_t ldqo, int64_t hsqo,
+                                    void *k_cache, int64_t kps, int64_t kss, int64_t khs,
+                                    void *v_cache, int64_t vps, int64_t vss, int64_t vhs,
+                                    int cache_kind, int64_t num_pages, int64_t page_size,
+                                    const void *slots, int slot_dtype,
+                                    const float *k_scale, const float *v_scale,
+                                    cudaStream_t stream);
 
 /*
  * crmsn_debug_status -- no counterpart on the pages: the bounds guard of the

@@ -8,6 +8,7 @@ call does, and raises when the library has not been built.
 from .binding import (  # noqa: F401
     CrmsnError,
     ada_rms_norm_style,
+    as_heads,
     as_rows,
     fused_add_rmsnorm_fp8_block_quant,
     fused_add_rmsnorm_quant,
@@ -15,6 +16,10 @@ from .binding import (  # noqa: F401
     gate_residual_ada_norm_fp8,
     layernorm,
     layernorm_quant,
+    qk_rmsnorm_rope_append,
+    qk_rmsnorm_rope_bwd,
+    qk_rmsnorm_rope_bwd_workspace_bytes,
+    qk_rmsnorm_rope_fwd,
     rmsnorm_bwd,
     rmsnorm_bwd_noalloc,
     rmsnorm_bwd_workspace,
@@ -22,5 +27,11 @@ from .binding import (  # noqa: F401
     rmsnorm_fwd,
     rmsnorm_quant,
     rmsnorm_supports,
+    rope_cos_sin,
 )
-from .autograd import RMSNormFunction, rmsnorm  # noqa: F401,E402
+from .autograd import (  # noqa: F401,E402
+    QKRMSNormRopeFunction,
+    RMSNormFunction,
+    qk_rmsnorm_rope,
+    rmsnorm,
+)

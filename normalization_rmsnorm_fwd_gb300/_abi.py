@@ -34,6 +34,16 @@ SIGNATURES = {
     "fused_rmsnorm_silu": (_ST, [_P, _I, _INT, _P, _I, _P, _INT, _F, _P, _F, _I, _I, _P, _P]),
     "layernorm": (_ST, [_P, _I, _P, _I, _P, _P, _F, _I, _I, _P, _P, _P]),
     "layernorm_quant": (_ST, [_P, _I, _INT, _P, _I, _P, _P, _P, _F, _I, _I, _P, _P, _P]),
+    "rope_cos_sin": (_ST, [_P, _INT, _I, _INT, _P, _INT, _P, _F, _I, _I, _P, _I, _P]),
+    "qk_rmsnorm_rope_fwd": (_ST, [_P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _INT, _F, _F, _P, _I, _I, _I,
+                                  _INT, _I, _I, _P, _I, _I, _P, _I, _I, _P]),
+    "qk_rmsnorm_rope_bwd": (_ST, [_P, _I, _I, _P, _I, _I, _P, _I, _I, _I, _P, _I, _I, _I, _P, _P, _INT,
+                                  _F, _F, _P, _I, _I, _I, _INT, _I, _I, _P, _I, _I, _P, _I, _I, _P, _P,
+                                  _P, ctypes.c_size_t, _P]),
+    "qk_rmsnorm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _INT]),
+    "qk_rmsnorm_rope_append": (_ST, [_P, _I, _I, _I, _P, _I, _I, _P, _I, _I, _I, _P, _P, _INT, _F, _F,
+                                     _P, _I, _I, _I, _INT, _I, _I, _P, _I, _I, _P, _I, _I, _I, _P, _I,
+                                     _I, _I, _INT, _I, _I, _P, _INT, _P, _P, _P]),
     "crmsn_debug_status": (_ST, [ctypes.POINTER(ctypes.c_uint64)]),
 }
 
@@ -47,8 +57,12 @@ OK = 0
 BF16, F32 = 0, 1
 E4M3, E5M2 = 0, 1
 OP_FWD, OP_BWD, OP_QUANT, OP_BLOCK_QUANT, OP_ADA_STYLE, OP_GATED_ADA_FP8, OP_SILU, OP_LAYERNORM = range(8)
+OP_QK_ROPE = 8
+I32, I64 = 0, 1
+CACHE_BF16, CACHE_E4M3, CACHE_E5M2 = 0, 1, 2
 OUT_BF16, OUT_E4M3 = 0, 1
 MAX_H = 16384
+MAX_HEAD_DIM = 512
 
 _lock = threading.Lock()
 _lib = None

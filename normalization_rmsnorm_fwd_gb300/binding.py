@@ -1,5 +1,9 @@
 """PyTorch-facing binding of the C ABI: argument marshalling only.
 
+Heads (the query / key functions) are ``[..., heads, D]`` with a contiguous D,
+one stride between heads and one between tokens: slices of a packed
+projection, heads beside a gate, ``[heads, T, D]`` storage transposed.
+
 Each function has the name of the C entry point it calls, takes CUDA tensors,
 turns them into pointers, row counts and row strides, allocates outputs the
 caller did not pass (``torch.empty``), and enqueues the call on the current
@@ -393,6 +397,290 @@ def rmsnorm_bwd_noalloc(g, x, w, rstd, weight_bias: float = 0.0, g_residual=None
                                         H, _ptr(dx), lddx, _ptr(dw), _stream(x))
     check("rmsnorm_bwd_noalloc", st)
     return dx, dw
+
+
+# ------------------------------------------------- queries, keys and cache --
+
+_INDEX = {torch.int32: _abi.I32, torch.int64: _abi.I64}
+_CACHE = {torch.bfloat16: _abi.CACHE_BF16, torch.float8_e4m3fn: _abi.CACHE_E4M3,
+          torch.float8_e5m2: _abi.CACHE_E5M2}
+
+
+def as_heads(t: torch.Tensor, name: str = "q") -> tuple[int, int, int, int, int]:
+    """(tokens, heads, D, token stride, head stride in elements) of a
+    [..., heads, D] tensor whose leading dimensions collapse into tokens."""
+    shape, st = t.shape, t.stride()
+    nd = len(shape)
+    if nd < 3:
+        raise ValueError(f"{name}: needs [tokens, heads, D]")
+    H, D = shape[-2:]
+    if D > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: D must be contiguous")
+    if nd == 3:
+        return shape[0], H, D, st[0], st[1]
+    for i in range(nd - 3):
+        if shape[i] > 1 and st[i] != st[i + 1] * shape[i + 1]:
+            raise ValueError(f"{name}: leading dimensions must be contiguous with one another "
+                             "(stride(i) == stride(i+1) * size(i+1)) to collapse into tokens")
+    return math.prod(shape[:-2]), H, D, st[-3], st[-2]
+
+
+def _head_tensor(t, name, like, shape):
+    """as_heads of a BF16 tensor of `like`'s device and the given shape."""
+    if t.dtype is not torch.bfloat16 or t.device != like.device:
+        raise TypeError(f"{name} must be bfloat16 on {like.device}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    return as_heads(t, name)
+
+
+def _head_weights(wq, wk, D, device, has_k):
+    """w_dtype of the two weights (0 when there are none)."""
+    if wq is None and wk is None:
+        return 0
+    if wq is None or (has_k and wk is None):
+        raise ValueError("wq and wk: both or neither")
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if w is not None and (w.device != device or w.dim() != 1 or w.shape[0] != D or (D > 1 and w.stride(0) != 1)):
+            raise ValueError(f"{name} must be a contiguous [{D}] tensor on {device}")
+    if wk is not None and wk.dtype != wq.dtype:
+        raise TypeError("wq and wk must have the same dtype")
+    if wq.dtype is torch.bfloat16:
+        return BF16
+    if wq.dtype is torch.float32:
+        return F32
+    raise TypeError(f"wq and wk must be bfloat16 or float32, got {wq.dtype}")
+
+
+def _rotation(cos_sin, device):
+    """(pointer, row stride, rows, R) of the cosines and sines; None: none."""
+    if cos_sin is None:
+        return None, 0, 1, 0
+    if cos_sin.dtype is not torch.float32 or cos_sin.device != device:
+        raise TypeError(f"cos_sin must be float32 on {device}, got {cos_sin.dtype} on {cos_sin.device}")
+    rows, R, ld = as_rows(cos_sin, "cos_sin")
+    return cos_sin.data_ptr(), ld, rows, R
+
+
+def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = False,
+                 scaling: float = 1.0, out=None):
+    """Cosines and sines of rotary positions, FP32 [..., R] (R/2 cosines, then
+    R/2 sines) with R = 2 * inv_freq.numel(): positions is [...] (int32 or
+    int64), or [axes, ...] when `sections` (the columns of each axis) names
+    more than one axis.  One call serves every layer.  Returns out."""
+    _need_cuda(positions, "positions")
+    device = positions.device
+    kind = _INDEX.get(positions.dtype)
+    if kind is None:
+        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+    if inv_freq.dtype is not torch.float32 or inv_freq.device != device:
+        raise TypeError(f"inv_freq must be float32 on {device}")
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous 1-D tensor")
+    R = 2 * inv_freq.shape[0]
+    axes = 1 if sections is None else len(sections)
+    if axes < 1:
+        raise ValueError("sections must name at least one axis")
+    shape, ldp = positions.shape, 0
+    if axes > 1:
+        if positions.dim() < 2 or shape[0] != axes:
+            raise ValueError(f"positions must be [{axes}, ...]")
+        shape, ldp = shape[1:], positions.stride(0)
+        if not positions[0].is_contiguous():
+            raise ValueError("positions: each axis must be contiguous")
+    elif not positions.is_contiguous():
+        raise ValueError("positions must be contiguous")
+    if out is None:
+        out = torch.empty(*shape, R, dtype=torch.float32, device=device)
+    elif out.dtype is not torch.float32 or out.device != device or out.shape != (*shape, R):
+        raise TypeError(f"out must be float32 {(*shape, R)} on {device}")
+    T = math.prod(shape)
+    ldo = as_rows(out, "out")[2]
+    parts = None if sections is None else (_abi.ctypes.c_int32 * axes)(*sections)
+    with _on_device(positions):
+        st = _lib().rope_cos_sin(positions.data_ptr(), kind, ldp, axes, parts, int(interleaved_axes),
+                                 inv_freq.data_ptr(), float(scaling), T, R, out.data_ptr(), ldo,
+                                 _stream(positions))
+    if st:
+        check("rope_cos_sin", st)
+    return out
+
+
+def _kv_shape(q, k):
+    """The shape of k: q's with k's own heads."""
+    if k.dim() != q.dim() or k.dim() < 3:
+        raise ValueError("k must have q's dimensions")
+    return (*q.shape[:-2], k.shape[-2], q.shape[-1])
+
+
+def qk_rmsnorm_rope_fwd(q, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: float = 0.0,
+                        interleaved: bool = False, q_out=None, k_out=None):
+    """Per-head RMSNorm of q [..., Hq, D] (weight wq) and k [..., Hk, D] (wk)
+    and the rotation by cos_sin, one rounding to BF16.  k None: queries alone;
+    wq = wk = None: no norm; cos_sin None: no rotation.  cos_sin [P, R] serves
+    token t with row t % P.  q_out may be q, k_out may be k.  Returns
+    (q_out, k_out)."""
+    _need_cuda(q, "q")
+    device = q.device
+    T, Hq, D, ldq, hsq = _head_tensor(q, "q", q, q.shape)
+    Hk = ldk = hsk = ldko = hsko = 0
+    kp = kop = None
+    if k is not None:
+        _, Hk, _, ldk, hsk = _head_tensor(k, "k", q, _kv_shape(q, k))
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=device)
+        _, _, _, ldko, hsko = _head_tensor(k_out, "k_out", q, k.shape)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    kind = _head_weights(wq, wk, D, device, k is not None)
+    cs, ldcs, rows, R = _rotation(cos_sin, device)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+    _, _, _, ldqo, hsqo = _head_tensor(q_out, "q_out", q, q.shape)
+    with _on_device(q):
+        st = _lib().qk_rmsnorm_rope_fwd(q.data_ptr(), ldq, hsq, Hq, kp, ldk, hsk, Hk, _ptr(wq),
+                                        _ptr(wk) if k is not None else None, kind, weight_bias, eps, cs, ldcs, rows, R,
+                                        interleaved, T, D, q_out.data_ptr(), ldqo, hsqo, kop, ldko, hsko,
+                                        _stream(q))
+    if st:
+        check("qk_rmsnorm_rope_fwd", st)
+    return q_out, k_out
+
+
+def qk_rmsnorm_rope_bwd_workspace_bytes(D: int, device=None) -> int:
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    n = _lib().qk_rmsnorm_rope_bwd_workspace_bytes(int(D), idx)
+    if n == 0:
+        raise CrmsnError("qk_rmsnorm_rope_bwd_workspace_bytes", 3, "invalid head size or device")
+    return n
+
+
+def _dw_tensor(dw, name, D, device):
+    if dw is None:
+        return torch.empty(D, dtype=torch.float32, device=device)
+    if dw.dtype is not torch.float32 or dw.device != device or dw.shape != (D,) or not dw.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [{D}] tensor on {device}")
+    return dw
+
+
+def qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: float = 0.0,
+                        interleaved: bool = False, dq=None, dk=None, dwq=None, dwk=None, workspace=None):
+    """Gradients of qk_rmsnorm_rope_fwd from gq, gk (of its outputs) and its
+    inputs q, k: dq, dk (BF16) and the FP32 dwq, dwk, added in a fixed order.
+    Without weights q and k may be None and dwq, dwk are None.  Returns
+    (dq, dk, dwq, dwk)."""
+    _need_cuda(gq, "gq")
+    device = gq.device
+    norm = wq is not None or wk is not None
+    T, Hq, D, ldgq, hsgq = _head_tensor(gq, "gq", gq, gq.shape)
+    kind = _head_weights(wq, wk, D, device, gk is not None)
+    ldq = hsq = Hk = ldgk = hsgk = ldk = hsk = lddk = hsdk = 0
+    qp = kp = gkp = dkp = dwqp = dwkp = wsp = wkp = None
+    wsn = 0
+    if dq is None:
+        dq = torch.empty(gq.shape, dtype=torch.bfloat16, device=device)
+    _, _, _, lddq, hsdq = _head_tensor(dq, "dq", gq, gq.shape)
+    if gk is not None:
+        _, Hk, _, ldgk, hsgk = _head_tensor(gk, "gk", gq, _kv_shape(gq, gk))
+        if dk is None:
+            dk = torch.empty(gk.shape, dtype=torch.bfloat16, device=device)
+        _, _, _, lddk, hsdk = _head_tensor(dk, "dk", gq, gk.shape)
+        gkp, dkp = gk.data_ptr(), dk.data_ptr()
+    elif dk is not None or dwk is not None:
+        raise ValueError("dk or dwk without gk")
+    if norm:
+        if q is None or (gk is not None and k is None):
+            raise ValueError("q and k are needed with weights")
+        _, _, _, ldq, hsq = _head_tensor(q, "q", gq, gq.shape)
+        qp = q.data_ptr()
+        dwq = _dw_tensor(dwq, "dwq", D, device)
+        dwqp = dwq.data_ptr()
+        if gk is not None:
+            _, _, _, ldk, hsk = _head_tensor(k, "k", gq, gk.shape)
+            dwk = _dw_tensor(dwk, "dwk", D, device)
+            kp, dwkp, wkp = k.data_ptr(), dwk.data_ptr(), wk.data_ptr()
+        if workspace is None:
+            workspace = torch.empty(qk_rmsnorm_rope_bwd_workspace_bytes(D, device), dtype=torch.uint8, device=device)
+        elif workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {device}")
+        wsp, wsn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif dwq is not None or dwk is not None:
+        raise ValueError("dwq or dwk without weights")
+    cs, ldcs, rows, R = _rotation(cos_sin, device)
+    with _on_device(gq):
+        st = _lib().qk_rmsnorm_rope_bwd(gq.data_ptr(), ldgq, hsgq, gkp, ldgk, hsgk, qp, ldq, hsq, Hq, kp, ldk,
+                                        hsk, Hk, _ptr(wq), wkp, kind, weight_bias, eps, cs, ldcs, rows, R,
+                                        interleaved, T, D, dq.data_ptr(), lddq, hsdq, dkp, lddk, hsdk, dwqp,
+                                        dwkp, wsp, wsn, _stream(gq))
+    if st:
+        check("qk_rmsnorm_rope_bwd", st)
+    return dq, dk, dwq, dwk
+
+
+def _cache_scale(scale, name, fp8, device):
+    if not fp8:
+        if scale is not None:
+            raise ValueError(f"{name} without an FP8 cache")
+        return None
+    if not isinstance(scale, torch.Tensor) or scale.dtype is not torch.float32 or scale.device != device \
+            or scale.numel() != 1:
+        raise TypeError(f"{name} must be a float32 tensor of one value on {device}")
+    return scale.data_ptr()
+
+
+def qk_rmsnorm_rope_append(q, k, v, wq, wk, cos_sin, k_cache, v_cache, slots, eps: float = 1e-6,
+                           weight_bias: float = 0.0, interleaved: bool = False, k_scale=None, v_scale=None,
+                           q_out=None):
+    """qk_rmsnorm_rope_fwd with the keys, and the values v, written to a paged
+    cache: k_cache, v_cache are [pages, page_size, Hk, D] views (any strides
+    with a contiguous D, e.g. a transposed [pages, Hk, page_size, D]) in BF16
+    or FP8 (x / scale, k_scale and v_scale being float32 tensors of one
+    value).  Token t goes to slot slots[t] = page * page_size + row (int32 or
+    int64); a negative or too large slot writes nothing.  Slots must differ.
+    q None: the cache alone.  Returns q_out."""
+    _need_cuda(k, "k")
+    device = k.device
+    T, Hk, D, ldk, hsk = _head_tensor(k, "k", k, k.shape)
+    _, _, _, ldv, hsv = _head_tensor(v, "v", k, k.shape)
+    Hq = ldq = hsq = ldqo = hsqo = 0
+    qp = qop = None
+    if q is not None:
+        _, Hq, _, ldq, hsq = _head_tensor(q, "q", k, _kv_shape(k, q))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+        _, _, _, ldqo, hsqo = _head_tensor(q_out, "q_out", k, q.shape)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    kind = _head_weights(wk if q is None else wq, wk, D, device, True)
+    cs, ldcs, rows, R = _rotation(cos_sin, device)
+    ck = _CACHE.get(k_cache.dtype)
+    if ck is None or v_cache.dtype != k_cache.dtype or k_cache.device != device or v_cache.device != device:
+        raise TypeError(f"k_cache and v_cache must be bfloat16, float8_e4m3fn or float8_e5m2, both, on {device}")
+    shape = k_cache.shape
+    if len(shape) != 4 or shape != v_cache.shape or shape[2] != Hk or shape[3] != D:
+        raise ValueError(f"k_cache and v_cache must be [pages, page_size, {Hk}, {D}]")
+    kst, vst = k_cache.stride(), v_cache.stride()
+    if D > 1 and (kst[3] != 1 or vst[3] != 1):
+        raise ValueError("k_cache and v_cache: D must be contiguous")
+    sk = _INDEX.get(slots.dtype)
+    if sk is None or slots.device != device:
+        raise TypeError(f"slots must be int32 or int64 on {device}, got {slots.dtype} on {slots.device}")
+    if slots.numel() != T or not slots.is_contiguous():
+        raise ValueError("slots must be contiguous with one slot per token")
+    fp8 = ck != _abi.CACHE_BF16
+    ks, vs = _cache_scale(k_scale, "k_scale", fp8, device), _cache_scale(v_scale, "v_scale", fp8, device)
+    with _on_device(k):
+        st = _lib().qk_rmsnorm_rope_append(qp, ldq, hsq, Hq, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, Hk,
+                                           _ptr(wq) if q is not None else None, _ptr(wk), kind, weight_bias, eps, cs, ldcs, rows, R,
+                                           interleaved, T, D, qop, ldqo, hsqo, k_cache.data_ptr(), kst[0],
+                                           kst[1], kst[2], v_cache.data_ptr(), vst[0], vst[1], vst[2], ck,
+                                           shape[0], shape[1], slots.data_ptr(), sk, ks, vs, _stream(k))
+    if st:
+        check("qk_rmsnorm_rope_append", st)
+    return q_out
 
 
 def rmsnorm_supports(H: int, w_dtype: int = BF16, op: int = _abi.OP_FWD) -> int:

@@ -19,7 +19,9 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 
-int sm_count(int dev)
+}  // namespace
+
+int crmsn::sm_count(int dev)
 {
     if (dev < 0 || dev >= kMaxDevices) return 0;
     int n = g_sm_count[dev].load(std::memory_order_relaxed);
@@ -31,6 +33,8 @@ int sm_count(int dev)
     g_sm_count[dev].store(n, std::memory_order_relaxed);
     return n;
 }
+
+namespace {
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -249,7 +253,9 @@ constexpr int kDebugDevices = 64;
 std::mutex g_debug_mutex;
 unsigned long long *g_debug_word_ptr[kDebugDevices];
 
-unsigned long long *debug_word()
+}  // namespace
+
+unsigned long long *crmsn::debug_word()
 {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDebugDevices) {
@@ -267,6 +273,8 @@ unsigned long long *debug_word()
     }
     return g_debug_word_ptr[dev];
 }
+
+namespace {
 
 template <int N>
 DebugRanges debug_ranges(const Tensor (&ts)[N])
@@ -365,6 +373,9 @@ crmsn_status rmsnorm_supports(int64_t H, int w_dtype, int op)
         case CRMSN_OP_LAYERNORM:
             if (w_dtype != CRMSN_F32) return CRMSN_ERR_DTYPE;
             return check_h(H);
+        case CRMSN_OP_QK_ROPE:
+            if (H < 1) return CRMSN_ERR_SHAPE;
+            return (H > CRMSN_MAX_HEAD_DIM || (H & 1)) ? CRMSN_ERR_UNSUPPORTED_H : CRMSN_OK;
         case CRMSN_OP_ADA_STYLE:
         case CRMSN_OP_GATED_ADA_FP8:
             if (w_dtype != CRMSN_BF16) return CRMSN_ERR_DTYPE;

@@ -183,6 +183,13 @@ cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t sm
     return e;
 }
 
+// SMs of a device (0: unknown), kept after the first query (api.cu).
+int sm_count(int dev);
+#ifdef CRMSN_DEBUG
+// The debug build's violation word on the current device (api.cu).
+unsigned long long *debug_word();
+#endif
+
 cudaError_t launch_fwd_y(const FwdParams &p, int in, int wk, const Layout &L, cudaStream_t s);
 cudaError_t launch_fwd_q(const FwdParams &p, int in, int wk, int fp8k, const Layout &L, cudaStream_t s);
 cudaError_t launch_fwd_block(const FwdParams &p, const Layout &L, cudaStream_t s);
