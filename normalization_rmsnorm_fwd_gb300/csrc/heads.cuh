@@ -1,12 +1,20 @@
 // heads.cuh -- device helpers of the query / key kernels.
 //
 // A head is a row of D elements.  In the 16-byte form a row belongs to
-// 2^lg lanes, each holding two pieces of 8 elements: a lane of the rotated
-// part (the first R/16 lanes) holds [8l, 8l+8) and [R/2 + 8l, R/2 + 8l + 8),
-// so that both members of every pair are in one lane whichever pairing is
-// used; a lane behind them holds 16 consecutive elements of the rest.  The
-// rotation then needs no exchange between lanes, and a warp's loads of one
-// piece cover whole 32-byte sectors.
+// n = ceil(D / 16) lanes, each holding two pieces of 8 elements: a lane of the
+// rotated part (the first R/16 lanes) holds [8l, 8l+8) and [R/2 + 8l,
+// R/2 + 8l + 8), so that both members of every pair are in one lane whichever
+// pairing is used; a lane behind them holds 16 consecutive elements of the
+// rest.  The rotation then needs no exchange between lanes, and a warp's loads
+// of one piece cover whole 32-byte sectors.  A warp works on 32 / n rows at a
+// time.
+//
+// Rows of one tensor are numbered t H + h.  A warp walks through its rows by
+// running offsets (no division or product per row), and its rows stream
+// through a ring of shared-memory slots filled with cp.async: every thread
+// copies exactly the pieces that it will itself use, kStages - 1 steps ahead,
+// and waits only on its own copies, so that the loads in flight cost no
+// registers and no barrier.
 #pragma once
 
 #include "common.cuh"
@@ -14,14 +22,23 @@
 
 namespace crmsn {
 
+#ifdef CRMSN_DEBUG
+constexpr unsigned DBG_ASYNC_COPY_KIND = DBG_ASYNC_COPY;
+#else
+constexpr unsigned DBG_ASYNC_COPY_KIND = 0;
+#endif
+
 struct Pieces {
     int a, b;        // first element of the two pieces
     bool va, vb;     // piece inside the row
     bool rot;        // rotated pieces
 };
 
+// WHOLE: every lane is rotated (D = R = 16 N).
+template <int N, bool WHOLE>
 __device__ __forceinline__ Pieces lane_pieces(int l, int R, int D)
 {
+    if constexpr (WHOLE) return {8 * l, 8 * l + 8 * N, true, true, true};
     Pieces s;
     s.rot = l < R / 16;
     if (s.rot) {
@@ -34,6 +51,7 @@ __device__ __forceinline__ Pieces lane_pieces(int l, int R, int D)
         s.va = s.a < D;
         s.vb = s.b < D;
     }
+    if (N > 0) s.va = s.vb = true;
     return s;
 }
 
@@ -84,10 +102,17 @@ __device__ __forceinline__ void rotate(F2 (&a)[4], F2 (&b)[4], const Turn &t)
             a[i] = f2_fma(a[i], f2(ca), pa);
             b[i] = f2_fma(b[i], f2(cb), pb);
         } else {
-            const F2 s = t.s[i], n = f2(-f2_lo(s), -f2_hi(s)), c = t.c[i];
-            const F2 x = f2_fma(a[i], c, f2_mul(b[i], INV ? s : n));
-            b[i] = f2_fma(b[i], c, f2_mul(a[i], INV ? n : s));
-            a[i] = x;
+            // The product that is taken off is negated in a scalar FMA
+            // (a packed one has no negated operand).
+            const F2 s = t.s[i], c = t.c[i], as = f2_mul(a[i], s), bs = f2_mul(b[i], s);
+            const F2 x = a[i], y = b[i];
+            if constexpr (INV) {
+                a[i] = f2_fma(x, c, bs);
+                b[i] = f2(__fmaf_rn(f2_lo(y), f2_lo(c), -f2_lo(as)), __fmaf_rn(f2_hi(y), f2_hi(c), -f2_hi(as)));
+            } else {
+                a[i] = f2(__fmaf_rn(f2_lo(x), f2_lo(c), -f2_lo(bs)), __fmaf_rn(f2_hi(x), f2_hi(c), -f2_hi(bs)));
+                b[i] = f2_fma(y, c, as);
+            }
         }
     }
 }
@@ -108,11 +133,124 @@ __device__ __forceinline__ void ld_weight8(F2 (&f)[4], const void *w, int w32, f
     for (int j = 0; j < 4; ++j) f[j] = f2_add(f[j], f2(bias));
 }
 
-// Sum over the 2^lg lanes of a row.
-__device__ __forceinline__ float row_lanes_sum(float v, int lg)
+// The lanes of a warp: n to a row; lanes past the last whole row are idle
+// (their group is >= rows).  N > 0: n is known, a power of two, and D = 16 N.
+template <int N>
+struct Lanes {
+    int n, l, grp;   // lanes of a row; lane in its row, row in the step
+    __device__ __forceinline__ explicit Lanes(int n_) : n(N > 0 ? N : n_)
+    {
+        const int lane = threadIdx.x & 31;
+        grp = lane / n;
+        l = lane - grp * n;
+    }
+    __device__ __forceinline__ int rows() const { return 32 / n; }
+    // Sums over the lanes of a row, the same bits in all of them.
+    template <int K>
+    __device__ __forceinline__ void sum(float (&v)[K]) const
+    {
+        if (N > 0 || (n & (n - 1)) == 0) {
+#pragma unroll
+            for (int o = N > 0 ? N / 2 : 16; o > 0; o >>= 1) {
+                if (N == 0 && o >= n) continue;
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            }
+            return;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            if (o >= n) continue;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float w = __shfl_down_sync(0xffffffffu, v[k], o);
+                if (l + o < n) v[k] += w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], grp * n);
+    }
+};
+__device__ __forceinline__ float warp_sum(float v)
 {
-    for (int o = 1 << lg >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// A running position in [T, H, D].
+template <typename E>
+struct Walk {
+    E *p;
+    int h;
+    // True when the step passes the end of a token's heads.
+    __device__ __forceinline__ bool step(const Stride &s, int dh, int H)
+    {
+        p += s.step;
+        h += dh;
+        const bool over = h >= H;
+        if (over) {
+            h -= H;
+            p += s.wrap;
+        }
+        return over;
+    }
+};
+
+// A lane's first row in a share, and how many it has.
+struct LaneRows {
+    int64_t t;       // token
+    int h, mine;     // head; rows of this lane
+    int most;        // of any lane of the warp
+    __device__ __forceinline__ LaneRows(const Share &s, int H, int warp, int grp, int rows_per_step)
+    {
+        const int64_t r0 = (int64_t)warp * s.run * rows_per_step + grp, rest = s.rows - r0;
+        mine = 0;
+        t = h = 0;
+        if (grp < rows_per_step && rest > 0) {
+            const int64_t runs = (rest - 1) / s.inc, last = rest - runs * s.inc;
+            const int64_t in_last = (last + rows_per_step - 1) / rows_per_step;
+            mine = (int)runs * s.run + (int)(in_last < s.run ? in_last : s.run);
+            t = r0 / H;
+            h = (int)(r0 - t * H);
+        }
+        most = __reduce_max_sync(0xffffffffu, mine);
+    }
+};
+
+__device__ __forceinline__ void cp_async16(void *smem, const void *g)
+{
+    if (!dbg_shared(smem, 16)) return;
+    if (!dbg_global(g, 16, false, DBG_ASYNC_COPY_KIND)) {
+        *static_cast<uint4 *>(smem) = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                 :: "r"((unsigned)__cvta_generic_to_shared(smem)), "l"(g) : "memory");
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait()
+{
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+// The CTA's dynamic shared memory.
+extern __shared__ __align__(16) unsigned char heads_smem[];
+__device__ __forceinline__ BVec<8> ld_slot(const uint4 *s)
+{
+    const uint4 q = dbg_shared(s, 16) ? *s : make_uint4(0, 0, 0, 0);
+    BVec<8> v;
+    v.w[0] = q.x;
+    v.w[1] = q.y;
+    v.w[2] = q.z;
+    v.w[3] = q.w;
+    return v;
+}
+__device__ __forceinline__ void st_f2x4(uint16_t *y, const F2 (&a)[4])
+{
+    BVec<8> v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = bf16_f2(a[i]);
+    if (dbg_global(y, 16, true)) *reinterpret_cast<uint4 *>(y) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
 }
 
 // One element at a time (any alignment a BF16 or FP8 tensor can have).

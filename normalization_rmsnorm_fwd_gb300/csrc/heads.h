@@ -20,6 +20,27 @@ struct CacheView {
     int64_t ps, ss, hs;
 };
 
+// How a tensor's position moves with a step: `step` elements, and `wrap` more
+// where the step passes a token's last head.
+struct Stride {
+    int64_t step, wrap;
+};
+
+// The share of one tensor in a launch.  Warp w of it takes rows
+// w run rps + i rps (i < run; rps rows at once), then the same `inc` rows on,
+// and so forth: neighbouring warps read neighbouring memory at any time.
+struct Share {
+    int blocks;                  // CTAs
+    int run;                     // steps of a run: kRun or 1
+    int64_t rows;                // T * heads
+    int64_t inc;                 // rows from a run to the warp's next
+    // Inside a run [0] and to the next run [1]: tokens (dtc: modulo the rows
+    // of cos_sin) and heads of a step, and the tensors' strides.
+    int dt[2], dtc[2], dh[2];
+    Stride in[2], in2[2], out[2];
+};
+constexpr int kRun = 2;
+
 struct QkParams {
     HeadView in[3];              // q, k, v (v only for the append)
     HeadView out[2];             // q_out, k_out (k_out only without a cache)
@@ -40,8 +61,8 @@ struct QkParams {
     int page_size;
     // launch
     int heads;                   // rows per token: Hq + Hk (+ Hk)
-    int lg;                      // log2 of the lanes of a row
-    int chunks, steps;           // tasks per token, steps per task
+    int lanes;                   // lanes of a row
+    Share share[3];
 #ifdef CRMSN_DEBUG
     DebugRanges dbg;
 #endif
@@ -57,10 +78,9 @@ struct QkBwdParams {
     int cs_rows, R, pairs;
     int T, D;
     float *dw[2];
-    float *part;                 // [nblk[0] + nblk[1]][D] partial dw rows
-    int nblk[2];                 // CTAs of q and of k
-    int lg;
-    int chunks[2], steps[2];
+    float *part;                 // [CTAs of q, then of k][D] partial dw rows
+    int lanes;
+    Share share[2];
 #ifdef CRMSN_DEBUG
     DebugRanges dbg;
 #endif
@@ -85,6 +105,13 @@ struct RopeParams {
 
 // Most CTAs per SM of the backward (its workspace holds one row for each).
 constexpr int kQkBwdCtasPerSm = 4;
+
+// Deals `ctas` CTAs of `warps` warps out to n tensors of heads[i] heads
+// (heads_fwd.cu): each gets its share of the rows, at least one CTA and no more
+// than its rows fill; runs: runs of kRun steps where there are enough.
+void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_per_step, int warps, int ctas,
+          bool runs);
+void set_strides(Stride (&d)[2], const Share &s, int H, int64_t ld, int64_t hs);
 
 // norm: with weights; fast: the 16-byte form (D a multiple of 8, R of 16,
 // aligned tensors).

@@ -10,13 +10,15 @@
 // CTA, and a second kernel adds the partial rows in a fixed order: the bits
 // depend on the sizes and the number of SMs alone.  Each CTA works on q or on
 // k, so that a lane keeps one weight and one set of sums.
+#include <type_traits>
+
 #include "heads.cuh"
 
 namespace crmsn {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kStages = 2 * kRun;
 constexpr int kFold = 16;    // rows added plainly before they join the compensated sum
 
 // A compensated sum as one value; an infinite or NaN sum has no low part.
@@ -33,138 +35,199 @@ __device__ __forceinline__ void store_partial(const float *hi, const float *lo, 
     }
 }
 
-template <bool NORM, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) k_qk_bwd(const QkBwdParams p)
+// Shared memory of a CTA: the ring of g and x pieces and, per thread, the
+// compensated sums of its 16 columns, 4 to a 16-byte word.
+struct BwdShared {
+    uint4 ring[kStages][4][kThreads];
+    float4 hi[4][kThreads], lo[4][kThreads];
+};
+struct BwdSharedPlain {
+    uint4 ring[kStages][2][kThreads];
+};
+
+// The lane and the place among its 16 values of column j.
+__device__ __forceinline__ void column_place(int j, int R, int &l, int &i)
+{
+    if (j < R) {
+        const bool second = j >= R / 2;
+        const int k = second ? j - R / 2 : j;
+        l = k >> 3;
+        i = (k & 7) + (second ? 8 : 0);
+    } else {
+        l = R / 16 + ((j - R) >> 4);
+        i = (j - R) & 15;
+    }
+}
+
+// Four values (two packed pairs) join a compensated sum in shared memory.
+__device__ __forceinline__ void fold4(float4 &hi, float4 &lo, F2 a, F2 b)
+{
+    if (!dbg_shared(&hi, 16) || !dbg_shared(&lo, 16)) return;
+    float4 h = hi, l = lo;
+    float e;
+    two_sum(h.x, f2_lo(a), h.x, e);
+    l.x = __fadd_rn(l.x, e);
+    two_sum(h.y, f2_hi(a), h.y, e);
+    l.y = __fadd_rn(l.y, e);
+    two_sum(h.z, f2_lo(b), h.z, e);
+    l.z = __fadd_rn(l.z, e);
+    two_sum(h.w, f2_hi(b), h.w, e);
+    l.w = __fadd_rn(l.w, e);
+    hi = h;
+    lo = l;
+}
+
+template <int N, bool WHOLE, bool NORM, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, kQkBwdCtasPerSm) k_qk_bwd(const QkBwdParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     CRMSN_DEBUG_ENTER(p.dbg);
-    __shared__ float sums[NORM ? 2 * kWarps * CRMSN_MAX_HEAD_DIM : 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lg = p.lg, l = lane & ((1 << lg) - 1), grp = lane >> lg, rpw = 32 >> lg;
-    const Pieces pc = lane_pieces(l, p.R, p.D);
-    const int which = (int)blockIdx.x < p.nblk[0] ? 0 : 1;
-    const HeadView G = p.g[which], X = p.x[which], Y = p.dx[which];
-    const int block = (int)blockIdx.x - (which ? p.nblk[0] : 0);
-    const int chunks = p.chunks[which], steps = p.steps[which];
-    F2 wa[4], wb[4];
-    F2 ba[4], bb[4], ha[4], hb[4], la[4], lb[4];     // block sums, and the pairs they join
+    using Shared = typename std::conditional<NORM, BwdShared, BwdSharedPlain>::type;
+    Shared &sm = *reinterpret_cast<Shared *>(heads_smem);
+    const int which = (int)blockIdx.x < p.share[0].blocks ? 0 : 1;
+    const int block = (int)blockIdx.x - (which ? p.share[0].blocks : 0);
+    const Lanes<N> L(p.lanes);
+    const Pieces pc = lane_pieces<N, WHOLE>(L.l, p.R, p.D);
+    const int H = p.g[which].H, tid = threadIdx.x, delta = pc.b - pc.a, P = p.cs_rows;
+    const Share &sh = p.share[which];
+    const LaneRows mine(sh, H, block * kWarps + (tid >> 5), L.grp, L.rows());
+    const int64_t t = mine.t;
+    // x moves with g: its own strides, g's heads.
+    Walk<const uint16_t> g = {p.g[which].p + t * p.g[which].ld + mine.h * p.g[which].hs + pc.a, mine.h};
+    Walk<uint16_t> out = {const_cast<uint16_t *>(p.dx[which].p) + t * p.dx[which].ld + mine.h * p.dx[which].hs + pc.a,
+                          mine.h};
+    const uint16_t *x = NORM ? p.x[which].p + t * p.x[which].ld + mine.h * p.x[which].hs + pc.a : nullptr;
+    int to_issue = mine.mine;
+    auto issue = [&](int stage) {
+        if (to_issue > 0) {
+            if (pc.va) cp_async16(&sm.ring[stage][0][tid], g.p);
+            if (pc.vb) cp_async16(&sm.ring[stage][1][tid], g.p + delta);
+            if constexpr (NORM) {
+                if (pc.va) cp_async16(&sm.ring[stage][2][tid], x);
+                if (pc.vb) cp_async16(&sm.ring[stage][3][tid], x + delta);
+            }
+        }
+        --to_issue;
+        const int e = stage % kRun == kRun - 1;
+        const bool over = g.step(sh.in[e], sh.dh[e], H);
+        if constexpr (NORM) {
+            x += sh.in2[e].step;
+            if (over) x += sh.in2[e].wrap;
+        }
+    };
+    // A piece that the row has not stays zero.
+    if (N == 0 && !(pc.va && pc.vb))
+        for (int i = 0; i < kStages; ++i)
+            for (int k = 0; k < (NORM ? 4 : 2); ++k) sm.ring[i][k][tid] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) issue(i);
+    ring_commit();
+
+    F2 wa[4], wb[4], ba[4], bb[4];                   // weights, sums of the last rows
     int filled = 0;
     if constexpr (NORM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            wa[i] = wb[i] = ba[i] = bb[i] = ha[i] = hb[i] = la[i] = lb[i] = f2(0.f);
+        for (int i = 0; i < 4; ++i) {
+            wa[i] = wb[i] = ba[i] = bb[i] = f2(0.f);
+            sm.hi[i][tid] = sm.lo[i][tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         if (pc.va) ld_weight8(wa, p.w[which], p.w32, p.bias, pc.a);
         if (pc.vb) ld_weight8(wb, p.w[which], p.w32, p.bias, pc.b);
     }
     auto fold = [&] {
+        if constexpr (NORM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float s0, e0, s1, e1;
-            two_sum(f2_lo(ha[i]), f2_lo(ba[i]), s0, e0);
-            two_sum(f2_hi(ha[i]), f2_hi(ba[i]), s1, e1);
-            ha[i] = f2(s0, s1);
-            la[i] = f2_add(la[i], f2(e0, e1));
-            two_sum(f2_lo(hb[i]), f2_lo(bb[i]), s0, e0);
-            two_sum(f2_hi(hb[i]), f2_hi(bb[i]), s1, e1);
-            hb[i] = f2(s0, s1);
-            lb[i] = f2_add(lb[i], f2(e0, e1));
-            ba[i] = bb[i] = f2(0.f);
+            for (int i = 0; i < 2; ++i) {
+                fold4(sm.hi[i][tid], sm.lo[i][tid], ba[2 * i], ba[2 * i + 1]);
+                fold4(sm.hi[2 + i][tid], sm.lo[2 + i][tid], bb[2 * i], bb[2 * i + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ba[i] = bb[i] = f2(0.f);
         }
         filled = 0;
     };
-    const uint32_t tasks = (uint32_t)p.T * (uint32_t)chunks;
-    const uint32_t nwarps = (uint32_t)p.nblk[which] * kWarps;
-    for (uint32_t task = (uint32_t)block * kWarps + warp; task < tasks; task += nwarps) {
-        const int t = (int)(task / (uint32_t)chunks), chunk = (int)(task - (uint32_t)t * (uint32_t)chunks);
-        Turn turn;
-        if (pc.rot) ld_turn<PAIRS>(turn, p.cs + (int64_t)(t % p.cs_rows) * p.ldcs, l, p.R);
-        const int h1 = min(X.H, (chunk + 1) * steps * rpw);
-        for (int h0 = chunk * steps * rpw; h0 < h1; h0 += rpw) {
-            const int h = h0 + grp;
-            const bool on = h < h1;
-            BVec<8> xa{}, xb{}, ga{}, gb{};
-            if (on) {
-                const uint16_t *g = G.p + (int64_t)t * G.ld + (int64_t)h * G.hs;
-                if (pc.va) ga = ld_stream<8>(g + pc.a);
-                if (pc.vb) gb = ld_stream<8>(g + pc.b);
-                if constexpr (NORM) {
-                    const uint16_t *x = X.p + (int64_t)t * X.ld + (int64_t)h * X.hs;
-                    if (pc.va) xa = ld_stream<8>(x + pc.a);
-                    if (pc.vb) xb = ld_stream<8>(x + pc.b);
-                }
-            }
-            F2 a[4], b[4];
+    int tc = (int)(t % P);
+    Turn turn;
+    if (pc.rot && mine.mine > 0) ld_turn<PAIRS>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R);
+    for (int i0 = 0; i0 < mine.most; i0 += kStages) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = f2_bf16(ga.w[i]);
-                b[i] = f2_bf16(gb.w[i]);
-            }
-            if (pc.rot) rotate<PAIRS, true>(a, b, turn);
-            if constexpr (NORM) {
-                float s0 = 0.f, s1 = 0.f;
-                F2 m2 = f2(0.f);
+      for (int stage = 0; stage < kStages; ++stage) {
+        const int i = i0 + stage;
+        if (i >= mine.most) break;
+        if (stage % kRun == 0) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sq_acc_bf16x2(xa.w[i], s0, s1);
-                    sq_acc_bf16x2(xb.w[i], s0, s1);
-                    m2 = f2_fma(f2_mul(a[i], wa[i]), f2_bf16(xa.w[i]), m2);
-                    m2 = f2_fma(f2_mul(b[i], wb[i]), f2_bf16(xb.w[i]), m2);
-                }
-                const float ss = row_lanes_sum(s0 + s1, lg);
-                const float m = row_lanes_sum(f2_lo(m2) + f2_hi(m2), lg);
-                const float rstd = __frsqrt_rn(__fadd_rn(__fmul_rn(ss, p.inv_d), p.eps));
-                const float along = __fmul_rn(__fmul_rn(m, p.inv_d), rstd);
-                const F2 r2 = f2(on ? rstd : 0.f), n2 = f2(-along);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const F2 ya = f2_mul(f2_bf16(xa.w[i]), r2), yb = f2_mul(f2_bf16(xb.w[i]), r2);
-                    const F2 ua = a[i], ub = b[i];
-                    a[i] = f2_mul(r2, f2_fma(ya, n2, f2_mul(ua, wa[i])));
-                    b[i] = f2_mul(r2, f2_fma(yb, n2, f2_mul(ub, wb[i])));
-                    ba[i] = f2_fma(ua, ya, ba[i]);
-                    bb[i] = f2_fma(ub, yb, bb[i]);
-                }
-                if (++filled == kFold) fold();
-            }
-            uint16_t *y = const_cast<uint16_t *>(Y.p) + (int64_t)t * Y.ld + (int64_t)h * Y.hs;
-            BVec<8> v;
-            if (on && pc.va) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v.w[i] = bf16_f2(a[i]);
-                st_stream<8>(y + pc.a, v);
-            }
-            if (on && pc.vb) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v.w[i] = bf16_f2(b[i]);
-                st_stream<8>(y + pc.b, v);
-            }
+            for (int k = 0; k < kRun; ++k) issue((stage + kRun + k) % kStages);
+            ring_commit();
+            ring_wait<1>();
         }
+        const bool on = i < mine.mine;
+        const BVec<8> ga = ld_slot(&sm.ring[stage][0][tid]);
+        const BVec<8> gb = ld_slot(&sm.ring[stage][1][tid]);
+        F2 a[4], b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a[k] = f2_bf16(ga.w[k]);
+            b[k] = f2_bf16(gb.w[k]);
+        }
+        if (pc.rot) rotate<PAIRS, true>(a, b, turn);
+        if constexpr (NORM) {
+            const BVec<8> xa = ld_slot(&sm.ring[stage][2][tid]);
+            const BVec<8> xb = ld_slot(&sm.ring[stage][3][tid]);
+            F2 va[4], vb[4], ss = f2(0.f), m2 = f2(0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                va[k] = f2_bf16(xa.w[k]);
+                vb[k] = f2_bf16(xb.w[k]);
+                ss = f2_fma(va[k], va[k], ss);
+                ss = f2_fma(vb[k], vb[k], ss);
+                m2 = f2_fma(f2_mul(a[k], wa[k]), va[k], m2);
+                m2 = f2_fma(f2_mul(b[k], wb[k]), vb[k], m2);
+            }
+            float sum[2] = {f2_lo(ss) + f2_hi(ss), f2_lo(m2) + f2_hi(m2)};
+            L.sum(sum);
+            const float rstd = __frsqrt_rn(__fmaf_rn(sum[0], p.inv_d, p.eps));
+            const F2 r2 = f2(on ? rstd : 0.f), n2 = f2(-__fmul_rn(__fmul_rn(sum[1], p.inv_d), rstd));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                va[k] = f2_mul(va[k], r2);
+                vb[k] = f2_mul(vb[k], r2);
+                if (on) {
+                    ba[k] = f2_fma(a[k], va[k], ba[k]);
+                    bb[k] = f2_fma(b[k], vb[k], bb[k]);
+                }
+                a[k] = f2_mul(r2, f2_fma(va[k], n2, f2_mul(a[k], wa[k])));
+                b[k] = f2_mul(r2, f2_fma(vb[k], n2, f2_mul(b[k], wb[k])));
+            }
+            if (++filled == kFold) fold();
+        }
+        if (on && pc.va) st_f2x4(out.p, a);
+        if (on && pc.vb) st_f2x4(out.p + delta, b);
+        const int e = stage % kRun == kRun - 1;
+        const bool over = out.step(sh.out[e], sh.dh[e], H);
+        tc += sh.dtc[e] + over;
+        if (tc >= P) tc -= P;
+        if ((over || sh.dt[e] > 0) && i + 1 < mine.mine && pc.rot) ld_turn<PAIRS>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R);
+      }
     }
     if constexpr (NORM) {
         fold();
-        // The row groups of the warp hold the same columns.
-        float *hi = sums + warp * p.D, *lo = sums + (kWarps + warp) * p.D;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float h0 = i & 1 ? f2_hi(ha[i / 2]) : f2_lo(ha[i / 2]), l0 = i & 1 ? f2_hi(la[i / 2]) : f2_lo(la[i / 2]);
-            float h1 = i & 1 ? f2_hi(hb[i / 2]) : f2_lo(hb[i / 2]), l1 = i & 1 ? f2_hi(lb[i / 2]) : f2_lo(lb[i / 2]);
-            for (int o = 1 << lg; o < 32; o <<= 1) {
-                const float ch = __shfl_xor_sync(0xffffffffu, h0, o), cl = __shfl_xor_sync(0xffffffffu, l0, o);
-                const float dh = __shfl_xor_sync(0xffffffffu, h1, o), dl = __shfl_xor_sync(0xffffffffu, l1, o);
-                pair_acc(h0, l0, ch, cl);
-                pair_acc(h1, l1, dh, dl);
-            }
-            if (grp == 0 && pc.va) {
-                hi[pc.a + i] = h0;
-                lo[pc.a + i] = l0;
-            }
-            if (grp == 0 && pc.vb) {
-                hi[pc.b + i] = h1;
-                lo[pc.b + i] = l1;
-            }
+        // One partial row per CTA: each column over the warps and their row
+        // groups, in order.
+        __syncthreads();
+        for (int j = tid; j < p.D; j += kThreads) {
+            int l, i;
+            column_place(j, p.R, l, i);
+            const float *hi = reinterpret_cast<const float *>(sm.hi[i >> 2]) + (i & 3);
+            const float *lo = reinterpret_cast<const float *>(sm.lo[i >> 2]) + (i & 3);
+            float h = 0.f, e = 0.f;
+            for (int w = 0; w < kWarps; ++w)
+                for (int r = 0; r < L.rows(); ++r) {
+                    const int k = 4 * (32 * w + r * L.n + l);
+                    if (dbg_shared(hi + k, 4) && dbg_shared(lo + k, 4)) pair_acc(h, e, hi[k], lo[k]);
+                }
+            st_f32(p.part + (int64_t)blockIdx.x * p.D + j, joined(h, e));
         }
-        store_partial(sums, sums + kWarps * p.D, p.D, p.part);
     }
 }
 
@@ -177,13 +240,13 @@ __global__ void __launch_bounds__(kThreads) k_qk_bwd_any(const QkBwdParams p, bo
     constexpr int kUnits = CRMSN_MAX_HEAD_DIM / 64;
     __shared__ float sums[2 * kWarps * CRMSN_MAX_HEAD_DIM];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = p.D / 2;
-    const int which = (int)blockIdx.x < p.nblk[0] ? 0 : 1;
+    const int which = (int)blockIdx.x < p.share[0].blocks ? 0 : 1;
     const HeadView G = p.g[which], X = p.x[which], Y = p.dx[which];
     float h[kUnits][2], lo[kUnits][2];
 #pragma unroll
     for (int k = 0; k < kUnits; ++k) h[k][0] = h[k][1] = lo[k][0] = lo[k][1] = 0.f;
-    const int64_t rows = (int64_t)p.T * X.H, nwarps = (int64_t)p.nblk[which] * kWarps;
-    const int block = (int)blockIdx.x - (which ? p.nblk[0] : 0);
+    const int64_t rows = (int64_t)p.T * X.H, nwarps = (int64_t)p.share[which].blocks * kWarps;
+    const int block = (int)blockIdx.x - (which ? p.share[0].blocks : 0);
     for (int64_t r = (int64_t)block * kWarps + warp; r < rows; r += nwarps) {
         const int t = (int)(r / X.H), head = (int)(r - (int64_t)t * X.H);
         const uint16_t *g = G.p + (int64_t)t * G.ld + (int64_t)head * G.hs;
@@ -218,8 +281,8 @@ __global__ void __launch_bounds__(kThreads) k_qk_bwd_any(const QkBwdParams p, bo
         }
         float rstd = 1.f, along = 0.f;
         if (norm) {
-            rstd = __frsqrt_rn(__fadd_rn(__fmul_rn(row_lanes_sum(ss, 5), p.inv_d), p.eps));
-            along = __fmul_rn(__fmul_rn(row_lanes_sum(m, 5), p.inv_d), rstd);
+            rstd = __frsqrt_rn(__fadd_rn(__fmul_rn(warp_sum(ss), p.inv_d), p.eps));
+            along = __fmul_rn(__fmul_rn(warp_sum(m), p.inv_d), rstd);
         }
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
@@ -271,8 +334,8 @@ __global__ void __launch_bounds__(32 * kReduceWarps) k_qk_dw_reduce(const QkBwdP
     CRMSN_DEBUG_ENTER(p.dbg);
     __shared__ float sh[2][kReduceWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y;
-    const int col = blockIdx.x * 32 + lane, n = p.nblk[which];
-    const float *part = p.part + (which ? (int64_t)p.nblk[0] * p.D : 0) + col;
+    const int col = blockIdx.x * 32 + lane, n = p.share[which].blocks;
+    const float *part = p.part + (which ? (int64_t)p.share[0].blocks * p.D : 0) + col;
     const int c0 = (int)((int64_t)warp * n / kReduceWarps), c1 = (int)((int64_t)(warp + 1) * n / kReduceWarps);
     float h = 0.f, l = 0.f;
     if (col < p.D) {
@@ -305,43 +368,46 @@ __global__ void __launch_bounds__(32 * kReduceWarps) k_qk_dw_reduce(const QkBwdP
     if ((lane & 15) == 0 && out < p.D) st_f32(p.dw[which] + out, joined(a, b));
 }
 
+template <int N, bool WHOLE, bool NORM, bool PAIRS>
+cudaError_t go(const QkBwdParams &p, dim3 grid, cudaStream_t s)
+{
+    constexpr size_t smem = NORM ? sizeof(BwdShared) : sizeof(BwdSharedPlain);
+    static std::atomic<int> opted[kOptInDevices];
+    if (cudaError_t e = opt_in_smem(k_qk_bwd<N, WHOLE, NORM, PAIRS>, smem, opted)) return e;
+    return launch_pdl(k_qk_bwd<N, WHOLE, NORM, PAIRS>, grid, dim3(kThreads), smem, s, p);
+}
+
+template <int N, bool WHOLE>
+cudaError_t go(const QkBwdParams &p, bool norm, dim3 grid, cudaStream_t s)
+{
+    if (norm) return p.pairs ? go<N, WHOLE, true, true>(p, grid, s) : go<N, WHOLE, true, false>(p, grid, s);
+    return p.pairs ? go<N, WHOLE, false, true>(p, grid, s) : go<N, WHOLE, false, false>(p, grid, s);
+}
+
 }  // namespace
 
 cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, bool fast, int sms, cudaStream_t s)
 {
-    p.lg = 0;
-    while ((16 << p.lg) < p.D) ++p.lg;
-    const int rpw = fast ? 32 >> p.lg : 1, all = p.x[0].H + p.x[1].H;
-    const int most = sms * kQkBwdCtasPerSm;
+    p.lanes = (p.D + 15) / 16;
+    const int heads[2] = {p.g[0].H, p.g[1].H};
+    // Runs of two steps (heads_fwd.cu): better up to D = 128 here (32 + 8
+    // heads, T = 16384: 87.9 -> 80.0 us; D = 64, 16 + 16: 41.5 -> 38.0), worse
+    // for wider heads (16 + 2 of 256 beside a gate, T = 8192: 55.1 -> 60.0).
+    deal(p.share, heads, 2, p.T, p.cs_rows, fast ? 32 / p.lanes : 1, kWarps, sms * kQkBwdCtasPerSm, p.lanes <= 8);
     for (int i = 0; i < 2; ++i) {
-        const int H = p.x[i].H;
-        p.nblk[i] = 0;
-        p.chunks[i] = p.steps[i] = 1;
-        if (H == 0) continue;
-        // This tensor's share of the resident CTAs, and a token's heads split
-        // over warps while they would leave some of them without work.
-        int64_t share = i == 0 ? most : most - p.nblk[0];
-        if (i == 0 && p.x[1].H > 0) {
-            share = (int64_t)most * H / all;
-            if (share < 1) share = 1;
-            if (share > most - 1) share = most - 1;
-        }
-        const int total = (H + rpw - 1) / rpw;
-        int64_t chunks = (share * kWarps + p.T - 1) / p.T;
-        if (chunks > total) chunks = total;
-        p.steps[i] = (int)((total + chunks - 1) / chunks);
-        p.chunks[i] = (total + p.steps[i] - 1) / p.steps[i];
-        const int64_t tasks = fast ? (int64_t)p.T * p.chunks[i] : (int64_t)p.T * H;
-        const int64_t blocks = (tasks + kWarps - 1) / kWarps;
-        p.nblk[i] = (int)(blocks < share ? blocks : share);
+        Share &sh = p.share[i];
+        set_strides(sh.in, sh, heads[i], p.g[i].ld, p.g[i].hs);
+        set_strides(sh.in2, sh, heads[i], p.x[i].ld, p.x[i].hs);
+        set_strides(sh.out, sh, heads[i], p.dx[i].ld, p.dx[i].hs);
     }
-    const dim3 grid((unsigned)(p.nblk[0] + p.nblk[1])), block(kThreads);
+    const dim3 grid((unsigned)(p.share[0].blocks + p.share[1].blocks)), block(kThreads);
     cudaError_t e;
+    const bool whole = p.R == p.D;
     if (!fast) e = launch_pdl(k_qk_bwd_any, grid, block, 0, s, p, norm);
-    else if (norm) e = p.pairs ? launch_pdl(k_qk_bwd<true, true>, grid, block, 0, s, p)
-                               : launch_pdl(k_qk_bwd<true, false>, grid, block, 0, s, p);
-    else e = p.pairs ? launch_pdl(k_qk_bwd<false, true>, grid, block, 0, s, p)
-                     : launch_pdl(k_qk_bwd<false, false>, grid, block, 0, s, p);
+    else if (p.D == 64) e = whole ? go<4, true>(p, norm, grid, s) : go<4, false>(p, norm, grid, s);
+    else if (p.D == 128) e = whole ? go<8, true>(p, norm, grid, s) : go<8, false>(p, norm, grid, s);
+    else if (p.D == 256) e = whole ? go<16, true>(p, norm, grid, s) : go<16, false>(p, norm, grid, s);
+    else e = go<0, false>(p, norm, grid, s);
     if (e != cudaSuccess || !norm) return e;
     return launch_pdl(k_qk_dw_reduce, dim3((unsigned)((p.D + 31) / 32), p.x[1].H > 0 ? 2 : 1),
                       dim3(32 * kReduceWarps), 0, s, p);
