@@ -425,41 +425,101 @@ def as_heads(t: torch.Tensor, name: str = "q") -> tuple[int, int, int, int, int]
     return math.prod(shape[:-2]), H, D, st[-3], st[-2]
 
 
-def _head_tensor(t, name, like, shape):
-    """as_heads of a BF16 tensor of `like`'s device and the given shape."""
-    if t.dtype is not torch.bfloat16 or t.device != like.device:
-        raise TypeError(f"{name} must be bfloat16 on {like.device}, got {t.dtype} on {t.device}")
+_BF16 = torch.bfloat16
+_F32 = torch.float32
+# The current device without torch.cuda's checks (a call costs 0.07 instead of
+# 0.3 us), where the tensors have shown that CUDA is up.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _head_tensor(t, name, dev, shape):
+    """(pointer, token stride, head stride) of a BF16 tensor of this shape on
+    CUDA device `dev`."""
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        raise TypeError(f"{name} must be bfloat16 on cuda:{dev}, got {t.dtype} on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    return as_heads(t, name)
+    if len(shape) == 3:
+        ld, hs, one = t.stride()
+        if one == 1 or shape[2] <= 1:
+            return t.data_ptr(), ld, hs
+    return (t.data_ptr(), *as_heads(t, name)[3:])
 
 
-def _head_weights(wq, wk, D, device, has_k):
-    """w_dtype of the two weights (0 when there are none)."""
+def _first_head_tensor(t, name):
+    """(device, shape, tokens, heads, D) of the tensor that the others of a
+    call are measured by."""
+    _need_cuda(t, name)
+    shape = t.shape
+    if len(shape) == 3:
+        T, H, D = shape
+    else:
+        T, H, D = as_heads(t, name)[:3]
+    return t.get_device(), shape, T, H, D
+
+
+def _like(t):
+    """A new contiguous tensor of t's shape and dtype."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
+def _kv_shape(shape, t, name):
+    """The shape that t must have: `shape` with t's own heads."""
+    own = t.shape
+    if len(own) != len(shape):
+        raise ValueError(f"{name} must have {len(shape)} dimensions")
+    return (*shape[:-2], own[-2], shape[-1])
+
+
+def _weight_ptr(w, name, D, dev):
+    if w.get_device() != dev or w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{D}] tensor on cuda:{dev}")
+    return w.data_ptr()
+
+
+def _head_weights(wq, wk, D, dev, has_q, has_k):
+    """(pointers, w_dtype) of the two weights."""
     if wq is None and wk is None:
-        return 0
-    if wq is None or (has_k and wk is None):
+        return None, None, 0
+    if (has_q and wq is None) or (has_k and wk is None):
         raise ValueError("wq and wk: both or neither")
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None and (w.device != device or w.dim() != 1 or w.shape[0] != D or (D > 1 and w.stride(0) != 1)):
-            raise ValueError(f"{name} must be a contiguous [{D}] tensor on {device}")
-    if wk is not None and wk.dtype != wq.dtype:
+    one = wq if has_q else wk
+    dtype = one.dtype
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"wq and wk must be bfloat16 or float32, got {dtype}")
+    if has_q and has_k and wk.dtype is not dtype:
         raise TypeError("wq and wk must have the same dtype")
-    if wq.dtype is torch.bfloat16:
-        return BF16
-    if wq.dtype is torch.float32:
-        return F32
-    raise TypeError(f"wq and wk must be bfloat16 or float32, got {wq.dtype}")
+    return (_weight_ptr(wq, "wq", D, dev) if has_q else None, _weight_ptr(wk, "wk", D, dev) if has_k else None,
+            BF16 if dtype is _BF16 else F32)
 
 
-def _rotation(cos_sin, device):
+def _rotation(cos_sin, dev):
     """(pointer, row stride, rows, R) of the cosines and sines; None: none."""
     if cos_sin is None:
         return None, 0, 1, 0
-    if cos_sin.dtype is not torch.float32 or cos_sin.device != device:
-        raise TypeError(f"cos_sin must be float32 on {device}, got {cos_sin.dtype} on {cos_sin.device}")
+    if cos_sin.dtype is not _F32 or cos_sin.get_device() != dev:
+        raise TypeError(f"cos_sin must be float32 on cuda:{dev}, got {cos_sin.dtype} on {cos_sin.device}")
+    if cos_sin.dim() == 2:
+        rows, R = cos_sin.shape
+        ld, one = cos_sin.stride()
+        if one == 1 or R <= 1:
+            return cos_sin.data_ptr(), ld, rows, R
     rows, R, ld = as_rows(cos_sin, "cos_sin")
     return cos_sin.data_ptr(), ld, rows, R
+
+
+def _enqueue(name, dev, *args):
+    """The C call `name`, its last argument being the current stream of `dev`,
+    with that device current."""
+    fn = getattr(_lib(), name)
+    stream = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    if dev == _current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        check(name, st)
 
 
 def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = False,
@@ -469,48 +529,41 @@ def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = Fa
     int64), or [axes, ...] when `sections` (the columns of each axis) names
     more than one axis.  One call serves every layer.  Returns out."""
     _need_cuda(positions, "positions")
-    device = positions.device
+    dev = positions.get_device()
     kind = _INDEX.get(positions.dtype)
     if kind is None:
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-    if inv_freq.dtype is not torch.float32 or inv_freq.device != device:
-        raise TypeError(f"inv_freq must be float32 on {device}")
+    if inv_freq.dtype is not _F32 or inv_freq.get_device() != dev:
+        raise TypeError(f"inv_freq must be float32 on cuda:{dev}")
     if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D tensor")
     R = 2 * inv_freq.shape[0]
-    axes = 1 if sections is None else len(sections)
-    if axes < 1:
-        raise ValueError("sections must name at least one axis")
-    shape, ldp = positions.shape, 0
+    shape, ldp, axes, parts = positions.shape, 0, 1, None
+    if sections is not None:
+        axes = len(sections)
+        if axes < 1:
+            raise ValueError("sections must name at least one axis")
+        parts = (_abi.ctypes.c_int32 * axes)(*sections)
     if axes > 1:
-        if positions.dim() < 2 or shape[0] != axes:
+        if len(shape) < 2 or shape[0] != axes:
             raise ValueError(f"positions must be [{axes}, ...]")
         shape, ldp = shape[1:], positions.stride(0)
-        if not positions[0].is_contiguous():
+        if not positions.is_contiguous() and not positions[0].is_contiguous():
             raise ValueError("positions: each axis must be contiguous")
     elif not positions.is_contiguous():
         raise ValueError("positions must be contiguous")
+    whole = (*shape, R)
     if out is None:
-        out = torch.empty(*shape, R, dtype=torch.float32, device=device)
-    elif out.dtype is not torch.float32 or out.device != device or out.shape != (*shape, R):
-        raise TypeError(f"out must be float32 {(*shape, R)} on {device}")
-    T = math.prod(shape)
-    ldo = as_rows(out, "out")[2]
-    parts = None if sections is None else (_abi.ctypes.c_int32 * axes)(*sections)
-    with _on_device(positions):
-        st = _lib().rope_cos_sin(positions.data_ptr(), kind, ldp, axes, parts, int(interleaved_axes),
-                                 inv_freq.data_ptr(), float(scaling), T, R, out.data_ptr(), ldo,
-                                 _stream(positions))
-    if st:
-        check("rope_cos_sin", st)
+        out = torch.empty(whole, dtype=_F32, device=positions.device)
+        ldo = R
+    else:
+        if out.dtype is not _F32 or out.get_device() != dev or out.shape != whole:
+            raise TypeError(f"out must be float32 {whole} on cuda:{dev}")
+        ldo = as_rows(out, "out")[2]
+    T = shape[0] if len(shape) == 1 else math.prod(shape)
+    _enqueue("rope_cos_sin", dev, positions.data_ptr(), kind, ldp, axes, parts, interleaved_axes,
+             inv_freq.data_ptr(), scaling, T, R, out.data_ptr(), ldo)
     return out
-
-
-def _kv_shape(q, k):
-    """The shape of k: q's with k's own heads."""
-    if k.dim() != q.dim() or k.dim() < 3:
-        raise ValueError("k must have q's dimensions")
-    return (*q.shape[:-2], k.shape[-2], q.shape[-1])
 
 
 def qk_rmsnorm_rope_fwd(q, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: float = 0.0,
@@ -520,31 +573,23 @@ def qk_rmsnorm_rope_fwd(q, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: f
     wq = wk = None: no norm; cos_sin None: no rotation.  cos_sin [P, R] serves
     token t with row t % P.  q_out may be q, k_out may be k.  Returns
     (q_out, k_out)."""
-    _need_cuda(q, "q")
-    device = q.device
-    T, Hq, D, ldq, hsq = _head_tensor(q, "q", q, q.shape)
-    Hk = ldk = hsk = ldko = hsko = 0
-    kp = kop = None
+    dev, shape, T, Hq, D = _first_head_tensor(q, "q")
+    qp = _head_tensor(q, "q", dev, shape)
+    if q_out is None:
+        q_out = _like(q)
+    qo = _head_tensor(q_out, "q_out", dev, shape)
+    Hk, kp, ko = 0, (None, 0, 0), (None, 0, 0)
     if k is not None:
-        _, Hk, _, ldk, hsk = _head_tensor(k, "k", q, _kv_shape(q, k))
+        kshape = _kv_shape(shape, k, "k")
+        Hk, kp = kshape[-2], _head_tensor(k, "k", dev, kshape)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=device)
-        _, _, _, ldko, hsko = _head_tensor(k_out, "k_out", q, k.shape)
-        kp, kop = k.data_ptr(), k_out.data_ptr()
+            k_out = _like(k)
+        ko = _head_tensor(k_out, "k_out", dev, kshape)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    kind = _head_weights(wq, wk, D, device, k is not None)
-    cs, ldcs, rows, R = _rotation(cos_sin, device)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
-    _, _, _, ldqo, hsqo = _head_tensor(q_out, "q_out", q, q.shape)
-    with _on_device(q):
-        st = _lib().qk_rmsnorm_rope_fwd(q.data_ptr(), ldq, hsq, Hq, kp, ldk, hsk, Hk, _ptr(wq),
-                                        _ptr(wk) if k is not None else None, kind, weight_bias, eps, cs, ldcs, rows, R,
-                                        interleaved, T, D, q_out.data_ptr(), ldqo, hsqo, kop, ldko, hsko,
-                                        _stream(q))
-    if st:
-        check("qk_rmsnorm_rope_fwd", st)
+    wqp, wkp, kind = _head_weights(wq, wk, D, dev, True, k is not None)
+    _enqueue("qk_rmsnorm_rope_fwd", dev, *qp, Hq, *kp, Hk, wqp, wkp, kind, weight_bias, eps, *_rotation(cos_sin, dev),
+             interleaved, T, D, *qo, *ko)
     return q_out, k_out
 
 
@@ -557,11 +602,11 @@ def qk_rmsnorm_rope_bwd_workspace_bytes(D: int, device=None) -> int:
     return n
 
 
-def _dw_tensor(dw, name, D, device):
+def _dw_tensor(dw, name, D, like):
     if dw is None:
-        return torch.empty(D, dtype=torch.float32, device=device)
-    if dw.dtype is not torch.float32 or dw.device != device or dw.shape != (D,) or not dw.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 [{D}] tensor on {device}")
+        return torch.empty(D, dtype=_F32, device=like.device)
+    if dw.dtype is not _F32 or dw.device != like.device or dw.shape != (D,) or not dw.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [{D}] tensor on {like.device}")
     return dw
 
 
@@ -571,62 +616,56 @@ def qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cos_sin, eps: float = 1e-6, weight
     inputs q, k: dq, dk (BF16) and the FP32 dwq, dwk, added in a fixed order.
     Without weights q and k may be None and dwq, dwk are None.  Returns
     (dq, dk, dwq, dwk)."""
-    _need_cuda(gq, "gq")
-    device = gq.device
-    norm = wq is not None or wk is not None
-    T, Hq, D, ldgq, hsgq = _head_tensor(gq, "gq", gq, gq.shape)
-    kind = _head_weights(wq, wk, D, device, gk is not None)
-    ldq = hsq = Hk = ldgk = hsgk = ldk = hsk = lddk = hsdk = 0
-    qp = kp = gkp = dkp = dwqp = dwkp = wsp = wkp = None
-    wsn = 0
+    dev, shape, T, Hq, D = _first_head_tensor(gq, "gq")
+    gqp = _head_tensor(gq, "gq", dev, shape)
     if dq is None:
-        dq = torch.empty(gq.shape, dtype=torch.bfloat16, device=device)
-    _, _, _, lddq, hsdq = _head_tensor(dq, "dq", gq, gq.shape)
+        dq = _like(gq)
+    dqp = _head_tensor(dq, "dq", dev, shape)
+    none = (None, 0, 0)
+    Hk, gkp, dkp, qp, kp = 0, none, none, none, none
     if gk is not None:
-        _, Hk, _, ldgk, hsgk = _head_tensor(gk, "gk", gq, _kv_shape(gq, gk))
+        kshape = _kv_shape(shape, gk, "gk")
+        Hk, gkp = kshape[-2], _head_tensor(gk, "gk", dev, kshape)
         if dk is None:
-            dk = torch.empty(gk.shape, dtype=torch.bfloat16, device=device)
-        _, _, _, lddk, hsdk = _head_tensor(dk, "dk", gq, gk.shape)
-        gkp, dkp = gk.data_ptr(), dk.data_ptr()
+            dk = _like(gk)
+        dkp = _head_tensor(dk, "dk", dev, kshape)
     elif dk is not None or dwk is not None:
         raise ValueError("dk or dwk without gk")
-    if norm:
+    wqp, wkp, kind = _head_weights(wq, wk, D, dev, True, gk is not None)
+    dwqp = dwkp = wsp = None
+    wsn = 0
+    if wqp is not None:
         if q is None or (gk is not None and k is None):
             raise ValueError("q and k are needed with weights")
-        _, _, _, ldq, hsq = _head_tensor(q, "q", gq, gq.shape)
-        qp = q.data_ptr()
-        dwq = _dw_tensor(dwq, "dwq", D, device)
+        qp = _head_tensor(q, "q", dev, shape)
+        dwq = _dw_tensor(dwq, "dwq", D, gq)
         dwqp = dwq.data_ptr()
         if gk is not None:
-            _, _, _, ldk, hsk = _head_tensor(k, "k", gq, gk.shape)
-            dwk = _dw_tensor(dwk, "dwk", D, device)
-            kp, dwkp, wkp = k.data_ptr(), dwk.data_ptr(), wk.data_ptr()
+            kp = _head_tensor(k, "k", dev, kshape)
+            dwk = _dw_tensor(dwk, "dwk", D, gq)
+            dwkp = dwk.data_ptr()
         if workspace is None:
-            workspace = torch.empty(qk_rmsnorm_rope_bwd_workspace_bytes(D, device), dtype=torch.uint8, device=device)
-        elif workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous on {device}")
-        wsp, wsn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            wsn = _lib().qk_rmsnorm_rope_bwd_workspace_bytes(D, dev)
+            workspace = torch.empty(wsn, dtype=torch.uint8, device=gq.device)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+        else:
+            wsn = workspace.numel() * workspace.element_size()
+        wsp = workspace.data_ptr()
     elif dwq is not None or dwk is not None:
         raise ValueError("dwq or dwk without weights")
-    cs, ldcs, rows, R = _rotation(cos_sin, device)
-    with _on_device(gq):
-        st = _lib().qk_rmsnorm_rope_bwd(gq.data_ptr(), ldgq, hsgq, gkp, ldgk, hsgk, qp, ldq, hsq, Hq, kp, ldk,
-                                        hsk, Hk, _ptr(wq), wkp, kind, weight_bias, eps, cs, ldcs, rows, R,
-                                        interleaved, T, D, dq.data_ptr(), lddq, hsdq, dkp, lddk, hsdk, dwqp,
-                                        dwkp, wsp, wsn, _stream(gq))
-    if st:
-        check("qk_rmsnorm_rope_bwd", st)
+    _enqueue("qk_rmsnorm_rope_bwd", dev, *gqp, *gkp, *qp, Hq, *kp, Hk, wqp, wkp, kind, weight_bias, eps,
+             *_rotation(cos_sin, dev), interleaved, T, D, *dqp, *dkp, dwqp, dwkp, wsp, wsn)
     return dq, dk, dwq, dwk
 
 
-def _cache_scale(scale, name, fp8, device):
+def _cache_scale(scale, name, fp8, dev):
     if not fp8:
         if scale is not None:
             raise ValueError(f"{name} without an FP8 cache")
         return None
-    if not isinstance(scale, torch.Tensor) or scale.dtype is not torch.float32 or scale.device != device \
-            or scale.numel() != 1:
-        raise TypeError(f"{name} must be a float32 tensor of one value on {device}")
+    if not isinstance(scale, torch.Tensor) or scale.dtype is not _F32 or scale.get_device() != dev or scale.numel() != 1:
+        raise TypeError(f"{name} must be a float32 tensor of one value on cuda:{dev}")
     return scale.data_ptr()
 
 
@@ -640,46 +679,38 @@ def qk_rmsnorm_rope_append(q, k, v, wq, wk, cos_sin, k_cache, v_cache, slots, ep
     value).  Token t goes to slot slots[t] = page * page_size + row (int32 or
     int64); a negative or too large slot writes nothing.  Slots must differ.
     q None: the cache alone.  Returns q_out."""
-    _need_cuda(k, "k")
-    device = k.device
-    T, Hk, D, ldk, hsk = _head_tensor(k, "k", k, k.shape)
-    _, _, _, ldv, hsv = _head_tensor(v, "v", k, k.shape)
-    Hq = ldq = hsq = ldqo = hsqo = 0
-    qp = qop = None
+    dev, kshape, T, Hk, D = _first_head_tensor(k, "k")
+    kp, vp = _head_tensor(k, "k", dev, kshape), _head_tensor(v, "v", dev, kshape)
+    Hq, qp, qo = 0, (None, 0, 0), (None, 0, 0)
     if q is not None:
-        _, Hq, _, ldq, hsq = _head_tensor(q, "q", k, _kv_shape(k, q))
+        shape = _kv_shape(kshape, q, "q")
+        Hq, qp = shape[-2], _head_tensor(q, "q", dev, shape)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
-        _, _, _, ldqo, hsqo = _head_tensor(q_out, "q_out", k, q.shape)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
+            q_out = _like(q)
+        qo = _head_tensor(q_out, "q_out", dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    kind = _head_weights(wk if q is None else wq, wk, D, device, True)
-    cs, ldcs, rows, R = _rotation(cos_sin, device)
+    wqp, wkp, kind = _head_weights(wq, wk, D, dev, q is not None, True)
     ck = _CACHE.get(k_cache.dtype)
-    if ck is None or v_cache.dtype != k_cache.dtype or k_cache.device != device or v_cache.device != device:
-        raise TypeError(f"k_cache and v_cache must be bfloat16, float8_e4m3fn or float8_e5m2, both, on {device}")
-    shape = k_cache.shape
-    if len(shape) != 4 or shape != v_cache.shape or shape[2] != Hk or shape[3] != D:
+    if ck is None or v_cache.dtype is not k_cache.dtype or k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise TypeError(f"k_cache and v_cache must be bfloat16, float8_e4m3fn or float8_e5m2, both, on cuda:{dev}")
+    cshape = k_cache.shape
+    if len(cshape) != 4 or cshape != v_cache.shape or cshape[2] != Hk or cshape[3] != D:
         raise ValueError(f"k_cache and v_cache must be [pages, page_size, {Hk}, {D}]")
-    kst, vst = k_cache.stride(), v_cache.stride()
-    if D > 1 and (kst[3] != 1 or vst[3] != 1):
+    kps, kss, khs, k1 = k_cache.stride()
+    vps, vss, vhs, v1 = v_cache.stride()
+    if D > 1 and (k1 != 1 or v1 != 1):
         raise ValueError("k_cache and v_cache: D must be contiguous")
     sk = _INDEX.get(slots.dtype)
-    if sk is None or slots.device != device:
-        raise TypeError(f"slots must be int32 or int64 on {device}, got {slots.dtype} on {slots.device}")
+    if sk is None or slots.get_device() != dev:
+        raise TypeError(f"slots must be int32 or int64 on cuda:{dev}, got {slots.dtype} on {slots.device}")
     if slots.numel() != T or not slots.is_contiguous():
         raise ValueError("slots must be contiguous with one slot per token")
     fp8 = ck != _abi.CACHE_BF16
-    ks, vs = _cache_scale(k_scale, "k_scale", fp8, device), _cache_scale(v_scale, "v_scale", fp8, device)
-    with _on_device(k):
-        st = _lib().qk_rmsnorm_rope_append(qp, ldq, hsq, Hq, k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, Hk,
-                                           _ptr(wq) if q is not None else None, _ptr(wk), kind, weight_bias, eps, cs, ldcs, rows, R,
-                                           interleaved, T, D, qop, ldqo, hsqo, k_cache.data_ptr(), kst[0],
-                                           kst[1], kst[2], v_cache.data_ptr(), vst[0], vst[1], vst[2], ck,
-                                           shape[0], shape[1], slots.data_ptr(), sk, ks, vs, _stream(k))
-    if st:
-        check("qk_rmsnorm_rope_append", st)
+    _enqueue("qk_rmsnorm_rope_append", dev, *qp, Hq, *kp, *vp, Hk, wqp, wkp, kind, weight_bias, eps,
+             *_rotation(cos_sin, dev), interleaved, T, D, *qo, k_cache.data_ptr(), kps, kss, khs, v_cache.data_ptr(), vps,
+             vss, vhs, ck, cshape[0], cshape[1], slots.data_ptr(), sk, _cache_scale(k_scale, "k_scale", fp8, dev),
+             _cache_scale(v_scale, "v_scale", fp8, dev))
     return q_out
 
 

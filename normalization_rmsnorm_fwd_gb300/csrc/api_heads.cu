@@ -335,7 +335,7 @@ crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp, int
     p.T = T;
     p.half = half;
     p.out = cos_sin;
-    p.ldo = ldcs;
+    p.ldo = T > 1 ? ldcs : R;
     const bool vec = half % 4 == 0 && al(cos_sin, 16) && (T <= 1 || ldcs % 4 == 0);
     return launched(launch_rope(p, vec, sms, stream));
 }

@@ -152,9 +152,9 @@ def test_angles(T, R, sections, mixed, kind):
     p = pos if axes > 1 else pos[0]
     out = crm.rope_cos_sin(p.to(kind).to(DEV), f.to(DEV), sections, mixed, 0.75)
     assert out.shape == (T, R)
-    # Two steps of the library's cosine and sine, the angle's rounding (an
-    # eighth of a turn in 24 bits, times pi: below 2^-25) and the scaling's:
-    # below 6 u of the scaling.
+    # The polynomials' steps (at most 2 u of values up to 1), the angle's
+    # rounding (an eighth of a turn in 24 bits, times pi: below u) and the
+    # scaling's: below 6 u of the scaling.
     exact = qk_ref.angles(pos, f, sections, mixed, 0.75)
     assert ((out.cpu().double() - exact).abs() <= 6 * 2.0 ** -24 * 0.75).all()
     assert out[0, 0] == 0.75 or axes > 1 and sections[0] == 0
