@@ -46,17 +46,16 @@ struct BwdSharedPlain {
 };
 
 // The lane and the place among its 16 values of column j.
-__device__ __forceinline__ void column_place(int j, int R, int &l, int &i)
+__device__ __forceinline__ void column_place(int j, int R, int D, int &l, int &i)
 {
-    if (j < R) {
-        const bool second = j >= R / 2;
-        const int k = second ? j - R / 2 : j;
-        l = k >> 3;
-        i = (k & 7) + (second ? 8 : 0);
-    } else {
-        l = R / 16 + ((j - R) >> 4);
-        i = (j - R) & 15;
+    const int first = j < R ? 0 : R, half = j < R ? R / 2 : (D - R + 15) / 16 * 8;
+    int k = j - first;
+    i = k & 7;
+    if (k >= half) {
+        k -= half;
+        i += 8;
     }
+    l = first / 16 + (k >> 3);
 }
 
 // Four values (two packed pairs) join a compensated sum in shared memory.
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, kQkBwdCtasPerSm) k_qk_bwd(const QkBw
         __syncthreads();
         for (int j = tid; j < p.D; j += kThreads) {
             int l, i;
-            column_place(j, p.R, l, i);
+            column_place(j, p.R, p.D, l, i);
             const float *hi = reinterpret_cast<const float *>(sm.hi[i >> 2]) + (i & 3);
             const float *lo = reinterpret_cast<const float *>(sm.lo[i >> 2]) + (i & 3);
             float h = 0.f, e = 0.f;
