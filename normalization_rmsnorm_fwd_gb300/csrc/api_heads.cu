@@ -144,9 +144,9 @@ crmsn_status check_heads(const Heads &h, int64_t T, int64_t D)
     return al(h.p, 2) ? CRMSN_OK : CRMSN_ERR_ALIGNMENT;
 }
 
-bool heads_vec(const Heads &h, int64_t T)
+bool heads_vec(const Heads &h, int64_t T, int v)
 {
-    return !given(h) || (al(h.p, 16) && (T <= 1 || h.ld % 8 == 0) && (h.H <= 1 || h.hs % 8 == 0));
+    return !given(h) || (al(h.p, 2 * v) && (T <= 1 || h.ld % v == 0) && (h.H <= 1 || h.hs % v == 0));
 }
 
 Region heads_region(const Heads &h, int64_t T, int64_t D, bool out = false, int may_replace = -1)
@@ -194,11 +194,24 @@ crmsn_status check_common(const Common &c)
     return CRMSN_OK;
 }
 
-bool common_vec(const Common &c)
+// The pieces that the kernels move (heads.cuh) hold whole pairs and whole
+// accesses of v elements; the 16-byte form also reads weights, cosines and
+// sines by 16 bytes.
+bool common_vec(const Common &c, int v)
 {
-    if (c.D % 8 || c.R % 16) return false;
+    if (c.D % v || (c.R / 2) % v || (c.R / 2 + 7) / 8 + (c.D - c.R + 15) / 16 > 32) return false;
+    if (v < 8) return true;
     if (c.R > 0 && (!al(c.cs, 16) || (c.cs_rows > 1 && c.ldcs % 4))) return false;
     return al(c.wq, 16) && al(c.wk, 16);
+}
+
+// The widest access that every tensor of a call allows (fits(v)), or 0.
+template <typename Fits>
+int widest(const Common &c, Fits fits)
+{
+    for (int v = 8; v >= 2; v /= 2)
+        if (common_vec(c, v) && fits(v)) return v;
+    return 0;
 }
 
 Region weight_region(const Common &c, const void *w)
@@ -267,9 +280,10 @@ crmsn_status check_cache(const void *p, int64_t ps, int64_t ss, int64_t hs, int 
     return al(p, es) ? CRMSN_OK : CRMSN_ERR_ALIGNMENT;
 }
 
-bool cache_vec(const void *p, int64_t ps, int64_t ss, int64_t hs, int es, int64_t pages, int64_t page_size, int64_t Hk)
+bool cache_vec(const void *p, int64_t ps, int64_t ss, int64_t hs, int es, int64_t pages, int64_t page_size, int64_t Hk,
+               int v)
 {
-    return al(p, 8 * es) && (pages <= 1 || ps % 8 == 0) && (page_size <= 1 || ss % 8 == 0) && (Hk <= 1 || hs % 8 == 0);
+    return al(p, v * es) && (pages <= 1 || ps % v == 0) && (page_size <= 1 || ss % v == 0) && (Hk <= 1 || hs % v == 0);
 }
 
 Region cache_region(const void *p, int64_t ps, int64_t ss, int64_t hs, int es, int64_t pages, int64_t page_size,
@@ -351,12 +365,13 @@ crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_
     if (Hq < 1) return CRMSN_ERR_SHAPE;
     if (T == 0) return CRMSN_OK;
     const Heads in[2] = {{q, ldq, hsq, Hq}, {k, ldk, hsk, Hk}}, out[2] = {{q_out, ldqo, hsqo, Hq}, {k_out, ldko, hsko, Hk}};
-    bool fast = common_vec(c);
     for (int i = 0; i < 2; ++i) {
         if (crmsn_status s = check_heads(in[i], T, D)) return s;
         if (crmsn_status s = check_heads(out[i], T, D)) return s;
-        fast = fast && heads_vec(in[i], T) && heads_vec(out[i], T);
     }
+    const int vec = widest(c, [&](int v) {
+        return heads_vec(in[0], T, v) && heads_vec(in[1], T, v) && heads_vec(out[0], T, v) && heads_vec(out[1], T, v);
+    });
     const Region ts[] = {
         heads_region(in[0], T, D), heads_region(in[1], T, D), weight_region(c, wq), weight_region(c, wk), cs_region(c),
         heads_region(out[0], T, D, true, 0), heads_region(out[1], T, D, true, 1),
@@ -372,7 +387,7 @@ crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_
         p.out[i] = view(out[i]);
     }
     p.heads = (int)(Hq + Hk);
-    return launched(launch_qk_fwd(p, wq || wk, false, fast, sms, stream));
+    return launched(launch_qk_fwd(p, wq || wk, false, vec, sms, stream));
 }
 
 size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device)
@@ -406,13 +421,13 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
     }
     const Heads g[2] = {{gq, ldgq, hsgq, Hq}, {gk, ldgk, hsgk, Hk}}, dx[2] = {{dq, lddq, hsdq, Hq}, {dk, lddk, hsdk, Hk}};
     const Heads x[2] = {{norm ? q : nullptr, ldq, hsq, norm ? Hq : 0}, {norm ? k : nullptr, ldk, hsk, norm ? Hk : 0}};
-    bool fast = common_vec(c);
-    for (int i = 0; i < 2; ++i) {
-        for (const Heads *h : {&g[i], &x[i], &dx[i]}) {
+    for (int i = 0; i < 2; ++i)
+        for (const Heads *h : {&g[i], &x[i], &dx[i]})
             if (crmsn_status s = check_heads(*h, T, D)) return s;
-            fast = fast && heads_vec(*h, T);
-        }
-    }
+    const int vec = widest(c, [&](int v) {
+        return heads_vec(g[0], T, v) && heads_vec(g[1], T, v) && heads_vec(x[0], T, v) && heads_vec(x[1], T, v) &&
+               heads_vec(dx[0], T, v) && heads_vec(dx[1], T, v);
+    });
     if (norm && !workspace) return CRMSN_ERR_NULL;
     if (norm && (workspace_bytes == 0 || workspace_bytes > (size_t)1 << 40)) return CRMSN_ERR_WORKSPACE;
     const Region ts[] = {
@@ -438,7 +453,7 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
         p.dw[i] = dw[i];
     }
     p.part = static_cast<float *>(workspace);
-    return launched(launch_qk_bwd(p, norm, fast, sms, stream));
+    return launched(launch_qk_bwd(p, norm, vec, sms, stream));
 }
 
 crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int64_t Hq, const void *k, int64_t ldk,
@@ -461,11 +476,8 @@ crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int
     const bool fp8 = cache_kind != CRMSN_CACHE_BF16;
     const int es = fp8 ? 1 : 2;
     const Heads in[3] = {{q, ldq, hsq, Hq}, {k, ldk, hsk, Hk}, {v, ldv, hsv, Hk}}, out = {q_out, ldqo, hsqo, Hq};
-    bool fast = common_vec(c) && heads_vec(out, T);
-    for (const Heads &h : in) {
+    for (const Heads &h : in)
         if (crmsn_status s = check_heads(h, T, D)) return s;
-        fast = fast && heads_vec(h, T);
-    }
     if (crmsn_status s = check_heads(out, T, D)) return s;
     if (!slots || (fp8 && (!k_scale || !v_scale))) return CRMSN_ERR_NULL;
     if (!al(slots, slot_dtype == CRMSN_I64 ? 8 : 4) || (fp8 && (!al(k_scale, 4) || !al(v_scale, 4))))
@@ -473,9 +485,12 @@ crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int
     if (num_pages > 0) {
         if (crmsn_status s = check_cache(k_cache, kps, kss, khs, es, num_pages, page_size, Hk, D)) return s;
         if (crmsn_status s = check_cache(v_cache, vps, vss, vhs, es, num_pages, page_size, Hk, D)) return s;
-        fast = fast && cache_vec(k_cache, kps, kss, khs, es, num_pages, page_size, Hk) &&
-               cache_vec(v_cache, vps, vss, vhs, es, num_pages, page_size, Hk);
     }
+    const int vec = widest(c, [&](int v) {
+        return heads_vec(in[0], T, v) && heads_vec(in[1], T, v) && heads_vec(in[2], T, v) && heads_vec(out, T, v) &&
+               (num_pages == 0 || (cache_vec(k_cache, kps, kss, khs, es, num_pages, page_size, Hk, v) &&
+                                   cache_vec(v_cache, vps, vss, vhs, es, num_pages, page_size, Hk, v)));
+    });
     const int64_t pages = num_pages > 0 ? num_pages : 1;
     const Region ts[] = {
         heads_region(in[0], T, D), heads_region(in[1], T, D), heads_region(in[2], T, D),
@@ -504,7 +519,7 @@ crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int
     p.num_slots = num_pages * page_size;
     p.page_size = (int)page_size;
     p.heads = (int)(Hq + 2 * Hk);
-    return launched(launch_qk_fwd(p, wq || wk, true, fast, sms, stream));
+    return launched(launch_qk_fwd(p, wq || wk, true, vec, sms, stream));
 }
 
 }  // extern "C"

@@ -1,15 +1,17 @@
 // heads.cuh -- device helpers of the query / key kernels.
 //
-// A head is a row of D elements.  In the 16-byte form a row belongs to
-// n = ceil(D / 16) lanes, each holding two pieces of 8 elements: a lane of the
-// rotated part (the first R/16 lanes) holds [8l, 8l+8) and [R/2 + 8l,
-// R/2 + 8l + 8), so that both members of every pair are in one lane whichever
-// pairing is used; the lanes behind them hold a piece each of the two halves
-// of the rest.  The rotation then needs no exchange between lanes, and the
+// A head is a row of D elements.  A row belongs to n lanes (about D / 16), each
+// holding two pieces of at most 8 elements: a lane of the rotated part (the
+// first ceil(R/16) lanes) holds [8l, 8l+8) and [R/2 + 8l, R/2 + 8l + 8), so
+// that both members of every pair are in one lane whichever pairing is used;
+// the lanes behind them hold a piece each of the two halves of the rest.  The rotation then needs no exchange between lanes, and the
 // pieces that neighbouring lanes load are neighbours in memory (16 elements in
 // a row in one lane instead, so that each load takes half of every 32-byte
 // sector: D = 256, R = 64 backward 54 instead of 46 us).  A warp works on
 // 32 / n rows at a time.
+//
+// A piece is moved V elements at a time: 8 (16-byte accesses), or 4 or 2 where
+// sizes, strides or addresses allow no more.
 //
 // Rows of one tensor are numbered t H + h.  A warp walks through its rows by
 // running offsets (no division or product per row), and its rows stream
@@ -32,7 +34,7 @@ constexpr unsigned DBG_ASYNC_COPY_KIND = 0;
 
 struct Pieces {
     int a, b;        // first element of the two pieces
-    bool va, vb;     // piece inside the row
+    int ca, cb;      // their elements inside the row: 8, or in the row's last pieces 0 .. 8
     bool rot;        // rotated pieces
 };
 
@@ -40,23 +42,25 @@ struct Pieces {
 template <int N, bool WHOLE>
 __device__ __forceinline__ Pieces lane_pieces(int l, int R, int D)
 {
-    if constexpr (WHOLE) return {8 * l, 8 * l + 8 * N, true, true, true};
+    if constexpr (WHOLE) return {8 * l, 8 * l + 8 * N, 8, 8, true};
     Pieces s;
-    s.rot = l < R / 16;
+    const int turned = (R / 2 + 7) / 8;              // rotated lanes
+    s.rot = l < turned;
     if (s.rot) {
         s.a = 8 * l;
         s.b = R / 2 + 8 * l;
-        s.va = s.vb = true;
+        s.ca = s.cb = min(8, R / 2 - s.a);
     } else {
-        const int rest = (D - R + 15) / 16;
-        s.a = R + 8 * (l - R / 16);
-        s.b = s.a + 8 * rest;
-        s.va = s.a < D;
-        s.vb = s.b < D;
+        s.a = R + 8 * (l - turned);
+        s.b = s.a + (D - R + 15) / 16 * 8;
+        s.ca = max(0, min(8, D - s.a));
+        s.cb = max(0, min(8, D - s.b));
     }
-    if (N > 0) s.va = s.vb = true;
+    if (N > 0) s.ca = s.cb = 8;
     return s;
 }
+// The lanes of a row.
+__host__ __device__ inline int row_lanes(int R, int D) { return (R / 2 + 7) / 8 + (D - R + 15) / 16; }
 
 // The cosines and sines of a lane's 8 pairs: columns 8l.. (halves), or
 // 4l.. and R/4 + 4l.. (adjacent pairs: 4 pairs in each piece).
@@ -76,14 +80,32 @@ __device__ __forceinline__ void ld_f32x4(const float *p, F2 &x, F2 &y)
     y = f2(c, d);
 }
 
-template <bool PAIRS>
-__device__ __forceinline__ void ld_turn(Turn &t, const float *row, int l, int R)
+template <bool PAIRS, int V>
+__device__ __forceinline__ void ld_turn(Turn &t, const float *row, int l, int R, const Pieces &pc)
 {
     const int c0 = PAIRS ? 4 * l : 8 * l, c1 = PAIRS ? R / 4 + 4 * l : 8 * l + 4;
-    ld_f32x4(row + c0, t.c[0], t.c[1]);
-    ld_f32x4(row + c1, t.c[2], t.c[3]);
-    ld_f32x4(row + R / 2 + c0, t.s[0], t.s[1]);
-    ld_f32x4(row + R / 2 + c1, t.s[2], t.s[3]);
+    if constexpr (V == 8) {
+        ld_f32x4(row + c0, t.c[0], t.c[1]);
+        ld_f32x4(row + c1, t.c[2], t.c[3]);
+        ld_f32x4(row + R / 2 + c0, t.s[0], t.s[1]);
+        ld_f32x4(row + R / 2 + c1, t.s[2], t.s[3]);
+    } else {
+        // As many pairs as the pieces hold; zeros behind them.
+        const int pairs = PAIRS ? pc.ca / 2 : pc.ca;
+        float c[8], s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool on = PAIRS ? (i & 3) < pairs : i < pairs;
+            const int k = i < 4 ? c0 + i : c1 + i - 4;
+            c[i] = on ? ld_f32_ro(row + k) : 0.f;
+            s[i] = on ? ld_f32_ro(row + R / 2 + k) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            t.c[i] = f2(c[2 * i], c[2 * i + 1]);
+            t.s[i] = f2(s[2 * i], s[2 * i + 1]);
+        }
+    }
 }
 
 // The rotation of a lane's 8 pairs, in place: (a, b) -> (a c - b s, b c + a s)
@@ -152,26 +174,25 @@ struct Lanes {
     template <int K>
     __device__ __forceinline__ void sum(float (&v)[K]) const
     {
-        if (N > 0 || (n & (n - 1)) == 0) {
+        if constexpr (N > 0) {
 #pragma unroll
-            for (int o = N > 0 ? N / 2 : 16; o > 0; o >>= 1) {
-                if (N == 0 && o >= n) continue;
+            for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
                 for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-            }
-            return;
+        } else if ((n & (n - 1)) == 0) {
+            for (int o = n >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        } else {
+            for (int o = 1 << (31 - __clz(n)); o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float w = __shfl_down_sync(0xffffffffu, v[k], o);
+                    if (l + o < n) v[k] += w;
+                }
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], grp * n);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            if (o >= n) continue;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float w = __shfl_down_sync(0xffffffffu, v[k], o);
-                if (l + o < n) v[k] += w;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], grp * n);
     }
 };
 __device__ __forceinline__ float warp_sum(float v)
@@ -220,15 +241,23 @@ struct LaneRows {
     }
 };
 
-__device__ __forceinline__ void cp_async16(void *smem, const void *g)
+// A piece of `count` elements into a slot of the ring.
+template <int V>
+__device__ __forceinline__ void copy_piece(uint4 *slot, const uint16_t *g, int count)
 {
-    if (!dbg_shared(smem, 16)) return;
-    if (!dbg_global(g, 16, false, DBG_ASYNC_COPY_KIND)) {
-        *static_cast<uint4 *>(smem) = make_uint4(0, 0, 0, 0);
-        return;
+#pragma unroll
+    for (int e = 0; e < 8; e += V) {
+        if (e >= count) continue;
+        uint16_t *to = reinterpret_cast<uint16_t *>(slot) + e;
+        if (!dbg_shared(to, 2 * V)) continue;
+        if (!dbg_global(g + e, 2 * V, false, DBG_ASYNC_COPY_KIND)) {
+            for (int i = 0; i < V; ++i) to[i] = 0;
+            continue;
+        }
+        const unsigned a = (unsigned)__cvta_generic_to_shared(to);
+        if constexpr (V == 8) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(a), "l"(g + e) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(a), "l"(g + e), "n"(2 * V) : "memory");
     }
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                 :: "r"((unsigned)__cvta_generic_to_shared(smem)), "l"(g) : "memory");
 }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -248,12 +277,20 @@ __device__ __forceinline__ BVec<8> ld_slot(const uint4 *s)
     v.w[3] = q.w;
     return v;
 }
-__device__ __forceinline__ void st_f2x4(uint16_t *y, const F2 (&a)[4])
+// A piece of `count` values to BF16 memory.
+template <int V>
+__device__ __forceinline__ void st_piece(uint16_t *y, const F2 (&a)[4], int count)
 {
-    BVec<8> v;
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v.w[i] = bf16_f2(a[i]);
-    if (dbg_global(y, 16, true)) *reinterpret_cast<uint4 *>(y) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    for (int i = 0; i < 4; ++i) w[i] = bf16_f2(a[i]);
+#pragma unroll
+    for (int e = 0; e < 8; e += V) {
+        if (e >= count || !dbg_global(y + e, 2 * V, true)) continue;
+        if constexpr (V == 8) *reinterpret_cast<uint4 *>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (V == 4) *reinterpret_cast<uint2 *>(y + e) = make_uint2(w[e / 2], w[e / 2 + 1]);
+        else *reinterpret_cast<uint32_t *>(y + e) = w[e / 2];
+    }
 }
 
 // One element at a time (any alignment a BF16 or FP8 tensor can have).
@@ -276,6 +313,20 @@ __device__ __forceinline__ float weight_1(const void *w, int w32, float bias, in
 {
     if (w32) return __fadd_rn(ld_f32_ro(static_cast<const float *>(w) + i), bias);
     return __fadd_rn(ld_bf16_1(static_cast<const uint16_t *>(w) + i), bias);
+}
+// The effective weights of a piece, zeros behind it.
+template <int V>
+__device__ __forceinline__ void ld_weights(F2 (&f)[4], const void *w, int w32, float bias, int i, int count)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = f2(0.f);
+    if constexpr (V == 8) {
+        if (count > 0) ld_weight8(f, w, w32, bias, i);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (2 * j < count) f[j] = f2(weight_1(w, w32, bias, i + 2 * j), weight_1(w, w32, bias, i + 2 * j + 1));
+    }
 }
 __device__ __forceinline__ int64_t ld_index(const void *p, int is64, int64_t i)
 {

@@ -103,6 +103,9 @@ struct RopeParams {
 #endif
 };
 
+// CTAs per SM of the forward and the append: 128 threads of at most 80
+// registers, 16 KB of ring each.
+constexpr int kQkFwdCtasPerSm = 6;
 // Most CTAs per SM of the backward (its workspace holds one row for each).
 constexpr int kQkBwdCtasPerSm = 4;
 
@@ -113,10 +116,16 @@ void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_pe
           bool runs);
 void set_strides(Stride (&d)[2], const Share &s, int H, int64_t ld, int64_t hs);
 
-// norm: with weights; fast: the 16-byte form (D a multiple of 8, R of 16,
-// aligned tensors).
-cudaError_t launch_qk_fwd(QkParams p, bool norm, bool append, bool fast, int sms, cudaStream_t s);
-cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, bool fast, int sms, cudaStream_t s);
+// norm: with weights; vec: elements of an access, 8, 4 or 2 (row_lanes() at
+// most 32), or 0: the element-wise form.
+cudaError_t launch_qk_fwd(QkParams p, bool norm, bool append, int vec, int sms, cudaStream_t s);
+cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, int vec, int sms, cudaStream_t s);
+// The kernels of one translation unit each (compiled in parallel).
+cudaError_t run_qk_fwd(const QkParams &p, bool norm, dim3 grid, cudaStream_t s);
+cudaError_t run_qk_append(const QkParams &p, bool norm, dim3 grid, cudaStream_t s);
+cudaError_t run_qk_narrow(const QkParams &p, bool norm, bool append, int vec, dim3 grid, cudaStream_t s);
+cudaError_t run_qk_bwd(const QkBwdParams &p, bool norm, dim3 grid, cudaStream_t s);
+cudaError_t run_qk_bwd_narrow(const QkBwdParams &p, bool norm, int vec, dim3 grid, cudaStream_t s);
 cudaError_t launch_rope(const RopeParams &p, bool vec, int sms, cudaStream_t s);
 
 }  // namespace crmsn

@@ -32,8 +32,9 @@ def heads(g, T, H, D, layout="plain", scale=1.0):
         t = buf[:, 2:2 + H]
     elif layout == "heads":
         t = torch.empty(H, T, D, dtype=BF16, device=DEV).transpose(0, 1)
-    elif layout == "odd":        # two bytes off: the element-wise form
-        t = torch.empty(T * H * D + 1, dtype=BF16, device=DEV)[1:].view(T, H, D)
+    elif layout in ("odd", "off4", "off8"):      # 2, 4 or 8 bytes off: the element-wise form, 4- and 8-byte accesses
+        n = {"odd": 1, "off4": 2, "off8": 4}[layout]
+        t = torch.empty(T * H * D + n, dtype=BF16, device=DEV)[n:].view(T, H, D)
     else:
         t = torch.empty(T, H, D, dtype=BF16, device=DEV)
     t.copy_(x)
@@ -77,6 +78,18 @@ SHAPES = [
     (3000, 20, 4, 64, 64, False, "bf16", "plain", 1000),
     (12, 3, 2, 128, 0, False, "f32", "plain", 12),
     (12, 3, 2, 128, 128, False, None, "plain", 12),
+    # 8- and 4-byte accesses: pieces that end inside a lane
+    (15, 3, 2, 72, 72, False, "bf16", "plain", 15),
+    (700, 16, 16, 72, 72, True, "f32", "packed", 700),
+    (31, 5, 5, 88, 88, False, "bias", "gated", 31),
+    (22, 4, 1, 40, 40, True, "bf16", "heads", 11),
+    (22, 4, 1, 100, 100, False, "bf16", "plain", 22),
+    (1300, 7, 3, 100, 20, True, "f32", "plain", 1300),
+    (9, 2, 2, 44, 8, False, None, "plain", 9),
+    (23, 5, 3, 128, 128, False, "bf16", "off8", 23),
+    (23, 5, 3, 128, 64, True, "bf16", "off4", 23),
+    (6, 2, 1, 470, 440, False, "f32", "plain", 6),
+    (30, 2, 1, 12, 0, False, "bf16", "off4", 30),
     # the element-wise form
     (13, 3, 2, 2, 2, True, "bf16", "plain", 13),
     (13, 3, 2, 6, 4, False, "f32", "plain", 13),
@@ -116,7 +129,7 @@ def test_forward(T, Hq, Hk, D, R, pairs, weight, layout, P):
 def test_backward(T, Hq, Hk, D, R, pairs, weight, layout, P):
     g = gen(2 * T + D)
     q, qc = heads(g, T, Hq, D, layout)
-    gq, gqc = heads(g, T, Hq, D, "plain" if layout != "odd" else "odd", 0.02)
+    gq, gqc = heads(g, T, Hq, D, layout if layout in ("odd", "off4", "off8") else "plain", 0.02)
     (k, kc), (gk, gkc) = (heads(g, T, Hk, D, layout), heads(g, T, Hk, D, "plain", 0.02)) if Hk else ((None, None), (None, None))
     wq, wk, bias = weights(g, D, weight)
     wk = wk if Hk else None
@@ -298,6 +311,9 @@ def caches(g, pages, page, Hk, D, dtype, order):
     (29, 3, 2, 256, 256, True, "bf16", 64, "mixed", torch.int64),
     (31, 3, 3, 50, 20, False, "bias", 5, "token", torch.int64),
     (23, 0, 2, 128, 128, False, "bf16", 16, "token", torch.int64),
+    (90, 4, 2, 72, 72, False, "f32", 16, "token", torch.int64),
+    (90, 4, 2, 100, 60, True, "bf16", 16, "head", torch.int32),
+    (41, 2, 1, 40, 40, True, None, 3, "both", torch.int64),
 ])
 def test_append(T, Hq, Hk, D, R, pairs, weight, page, order, idx, dtype):
     g = gen(3 * T + D)
