@@ -379,10 +379,14 @@ crmsn_status layernorm_quant(void *out, int64_t ldo, int fp8_kind,
  *   - Column j turns the pair (j, j + R/2) (interleaved = 0) or
  *     (2j, 2j + 1) (interleaved = 1); elements R .. D-1 are not rotated.
  *   - FP32 throughout, one rounding to the output format.
- *   - Fast form: D a multiple of 8, R of 16, BF16 bases, strides and cache
- *     16-byte aligned (FP8 cache: 8-byte), FP32 weights and cos_sin rows
- *     16-byte.  Anything else that is aligned to its own elements runs an
- *     element-wise form with the same results up to the order of the sums.
+ *   - T < 2^31 - 2^20, at most 4096 heads.
+ *   - Alignment: any tensor may be aligned to its own elements only.  Memory
+ *     is accessed by 16, 8 or 4 bytes (8, 4 or 2 BF16 elements), the widest
+ *     that divides D, R/2 and every stride and that every base is aligned to
+ *     (FP8 caches: half as many bytes; 16 bytes also want 16-byte aligned
+ *     weights and cos_sin rows); where none does, or R/2 is odd, an
+ *     element-wise form runs.  The forms agree up to the order of the sums
+ *     of a row.
  */
 
 /*

@@ -95,7 +95,7 @@ _eager_lock = threading.Lock()
 
 
 def _note_graph(ctx, inputs):
-    leaves = [t for t in inputs if t is not None and t.requires_grad and t.is_leaf]
+    leaves = [t for t in inputs if t is not None and t.requires_grad and t.is_leaf and t.is_cuda]
     if not leaves:
         return
     stream = binding._stream(leaves[0])

@@ -13,7 +13,8 @@ using namespace crmsn;
 
 namespace {
 
-constexpr int64_t kMaxTokens = 0x7fffffff, kMaxHeads = 4096, kMaxStride = (int64_t)1 << 40;
+// Tokens: the kernels count them, and a step beyond, in 32 bits.
+constexpr int64_t kMaxTokens = 0x7ff00000, kMaxHeads = 4096, kMaxStride = (int64_t)1 << 40;
 
 bool al(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
@@ -137,8 +138,8 @@ crmsn_status check_heads(const Heads &h, int64_t T, int64_t D)
     if (!h.p) return CRMSN_ERR_NULL;
     if ((T > 1 && (h.ld < D || h.ld > kMaxStride)) || (h.H > 1 && (h.hs < D || h.hs > kMaxStride)))
         return CRMSN_ERR_SHAPE;
-    // Strides within 2^40 and T < 2^31 heads < 2^12: the spans stay below
-    // 2^72 / 2^52, so the token span is tested by division.
+    // Strides within 2^40 and at most 2^12 heads: only the span of the
+    // tokens can pass 64 bits, so it is tested by division.
     if (T > 1 && h.ld > ((int64_t)1 << 60) / T) return CRMSN_ERR_SHAPE;
     if (T > 1 && h.H > 1 && h.ld < (h.H - 1) * h.hs + D && h.hs < (T - 1) * h.ld + D) return CRMSN_ERR_SHAPE;
     return al(h.p, 2) ? CRMSN_OK : CRMSN_ERR_ALIGNMENT;
@@ -470,7 +471,7 @@ crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int
     if (cache_kind != CRMSN_CACHE_BF16 && cache_kind != CRMSN_CACHE_E4M3 && cache_kind != CRMSN_CACHE_E5M2)
         return CRMSN_ERR_DTYPE;
     if (slot_dtype != CRMSN_I32 && slot_dtype != CRMSN_I64) return CRMSN_ERR_DTYPE;
-    if (Hk < 1 || num_pages < 0 || page_size < 1 || page_size > kMaxTokens || num_pages > kMaxTokens / page_size)
+    if (Hk < 1 || num_pages < 0 || page_size < 1 || page_size > 0x7fffffff || num_pages > 0x7fffffff / page_size)
         return CRMSN_ERR_SHAPE;
     if (T == 0) return CRMSN_OK;
     const bool fp8 = cache_kind != CRMSN_CACHE_BF16;

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_fwd_any(const QkParams p, bool 
         const int which = flat < Hq ? 0 : flat < Hq + Hk ? 1 : 2;
         const int h = flat - (which > 0 ? Hq : 0) - (which > 1 ? Hk : 0);
         int64_t base = 0;
-        if (append && which > 0) base = cache_row(p, p.cache[which - 1], t);
+        if (append && which > 0) base = cache_row(p, p.cache[which - 1], ld_index(p.slots, p.slot64, t));
         if (base < 0) continue;
         const uint16_t *x = p.in[which].p + (int64_t)t * p.in[which].ld + (int64_t)h * p.in[which].hs;
         float v[kUnits][2], ss = 0.f;

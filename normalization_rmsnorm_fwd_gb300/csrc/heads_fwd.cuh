@@ -17,10 +17,9 @@ namespace {
 
 constexpr int kThreads = 128, kStages = 2 * kRun;
 
-// Where a token's row of the cache begins (elements); -1: not written.
-__device__ __forceinline__ int64_t cache_row(const QkParams &p, const CacheView &c, int64_t t)
+// Where the row of a cache slot begins (elements); -1: not written.
+__device__ __forceinline__ int64_t cache_row(const QkParams &p, const CacheView &c, int64_t s)
 {
-    const int64_t s = ld_index(p.slots, p.slot64, t);
     if (s < 0 || s >= p.num_slots) return -1;                // num_slots < 2^31
     const uint32_t page = (uint32_t)s / (uint32_t)p.page_size, row = (uint32_t)s - page * (uint32_t)p.page_size;
     return (int64_t)page * c.ps + (int64_t)row * c.ss;
@@ -103,8 +102,11 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
     int tc = (int)(t % P);                           // row of cos_sin
     Turn turn;
     if (kRotate && pc.rot && mine.mine > 0) ld_turn<PAIRS, V>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R, pc);
+    // A token's slot is asked for a step before it is looked at.
+    int64_t slot = -1;
+    bool fresh = true;
     if constexpr (ROLE != TO_HEADS)
-        if (mine.mine > 0) base = cache_row(p, p.cache[which - 1], t);
+        if (mine.mine > 0) slot = ld_index(p.slots, p.slot64, t);
     for (int i0 = 0; i0 < mine.most; i0 += kStages) {
 #pragma unroll
         for (int stage = 0; stage < kStages; ++stage) {
@@ -147,10 +149,12 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
                     st_piece<V>(out.p, a, pc.ca);
                     st_piece<V>(out.p + delta, b, pc.cb);
                 }
-            } else if (on && base >= 0) {
+            } else if (on) {
+                if (fresh) base = cache_row(p, p.cache[which - 1], slot);
                 void *c = p.cache[which - 1].p;
-                st_cache<V>(c, base + head, p.kind, a, inv, pc.ca);
-                st_cache<V>(c, base + head + delta, p.kind, b, inv, pc.cb);
+                const int ca = base < 0 ? 0 : pc.ca, cb = base < 0 ? 0 : pc.cb;
+                st_cache<V>(c, base + head, p.kind, a, inv, ca);
+                st_cache<V>(c, base + head + delta, p.kind, b, inv, cb);
             }
             // The lane's next row; what a new token needs is asked for now.
             const int e = stage % kRun == kRun - 1;
@@ -169,9 +173,10 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
             }
             tc += sh.dtc[e] + over;
             if (tc >= P) tc -= P;
-            if ((over || sh.dt[e] > 0) && i + 1 < mine.mine) {
+            fresh = over || sh.dt[e] > 0;
+            if (fresh && i + 1 < mine.mine) {
                 if (kRotate && pc.rot) ld_turn<PAIRS, V>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R, pc);
-                if constexpr (ROLE != TO_HEADS) base = cache_row(p, p.cache[which - 1], t);
+                if constexpr (ROLE != TO_HEADS) slot = ld_index(p.slots, p.slot64, t);
             }
         }
     }
