@@ -124,13 +124,16 @@ def _readable_heads(t: torch.Tensor) -> torch.Tensor:
 
 
 class QKRMSNormRopeFunction(torch.autograd.Function):
-    """(q_out, k_out) of qk_rmsnorm_rope_fwd (k_out None without k)."""
+    """(q_out, k_out) of qk_rmsnorm_rope_fwd (k_out None without k);
+    recording: whether gradients are being recorded (forward() itself always
+    runs without)."""
 
     @staticmethod
-    def forward(ctx, q, k, wq, wk, cos_sin, eps, weight_bias, interleaved):
+    def forward(ctx, q, k, wq, wk, cos_sin, eps, weight_bias, interleaved, recording):
         if cos_sin is not None and cos_sin.requires_grad:
             raise ValueError("cos_sin takes no gradient")
-        _note_graph(ctx, (q, k, wq, wk))
+        if recording:
+            _note_graph(ctx, (q, k, wq, wk))
         q = _readable_heads(q)
         k = None if k is None else _readable_heads(k)
         q_out, k_out = qk_rmsnorm_rope_fwd(q, k, wq, wk, cos_sin, eps, weight_bias, interleaved)
@@ -147,12 +150,12 @@ class QKRMSNormRopeFunction(torch.autograd.Function):
         q, k, wq, wk, cos_sin = ctx.saved_tensors
         like = gq if gq is not None else gk
         if like is None:
-            return (None,) * 8
+            return (None,) * 9
         g = [None if shape is None else like.new_zeros(shape) if t is None else _readable_heads(t)
              for t, shape in zip((gq, gk), ctx.shapes)]
         dq, dk, dwq, dwk = qk_rmsnorm_rope_bwd(g[0], g[1], q, k, wq, wk, cos_sin, *ctx.how)
         return (dq, dk, None if dwq is None else dwq.to(wq.dtype), None if dwk is None else dwk.to(wk.dtype),
-                None, None, None, None)
+                None, None, None, None, None)
 
 
 def qk_rmsnorm_rope(q: torch.Tensor, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: float = 0.0,
@@ -162,4 +165,5 @@ def qk_rmsnorm_rope(q: torch.Tensor, k, wq, wk, cos_sin, eps: float = 1e-6, weig
     (rope_cos_sin) takes no gradient.  To capture a training step, record the
     forward and the backward in one graph and let no eager graph of the same
     leaves live from another stream (refused with RuntimeError)."""
-    return QKRMSNormRopeFunction.apply(q, k, wq, wk, cos_sin, eps, weight_bias, interleaved)
+    return QKRMSNormRopeFunction.apply(q, k, wq, wk, cos_sin, eps, weight_bias, interleaved,
+                                       torch.is_grad_enabled())

@@ -460,7 +460,7 @@ def _first_head_tensor(t, name):
 
 def _like(t):
     """A new contiguous tensor of t's shape and dtype."""
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _kv_shape(shape, t, name):

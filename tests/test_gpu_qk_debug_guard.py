@@ -33,7 +33,7 @@ def inputs(T, Hq, Hk, D, R, kind, off):
     return g, t(Hq), t(Hk), t(Hk), *w, cs
 
 
-SHAPES = [(1, 32, 8, 128, 128, BF16, 0), (5, 3, 1, 64, 32, torch.float32, 0), (900, 24, 8, 128, 128, BF16, 0),
+SHAPES = [(1, 32, 8, 128, 128, BF16, 0), (5, 3, 1, 64, 32, torch.float32, 0), (900, 20, 8, 128, 128, BF16, 0),
           (33, 5, 2, 80, 80, BF16, 0), (7, 2, 1, 512, 64, BF16, 0), (40, 3, 3, 24, 16, None, 0), (40, 2, 1, 8, 0, BF16, 0),
           (17, 3, 2, 50, 18, BF16, 0), (1200, 3, 2, 128, 128, torch.float32, 1), (9, 2, 2, 2, 2, None, 0),
           (60, 4, 2, 72, 72, BF16, 0), (60, 4, 2, 100, 36, torch.float32, 0), (60, 4, 2, 128, 128, BF16, 2), (30, 2, 1, 88, 88, None, 4)]

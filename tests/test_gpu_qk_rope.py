@@ -76,6 +76,7 @@ SHAPES = [
     (25, 9, 2, 24, 16, True, None, "plain", 25),
     (300, 40, 40, 128, 128, True, "bf16", "plain", 300),
     (3000, 20, 4, 64, 64, False, "bf16", "plain", 1000),
+    (37, 3, 2, 64, 64, False, "bf16", "plain", 1),         # one rotation for all tokens
     (12, 3, 2, 128, 0, False, "f32", "plain", 12),
     (12, 3, 2, 128, 128, False, None, "plain", 12),
     # 8- and 4-byte accesses: pieces that end inside a lane
@@ -673,6 +674,13 @@ def test_autograd_capture():
             crm.qk_rmsnorm_rope(z, None, w, None, cs)
     torch.cuda.synchronize()
     assert eager.grad_fn is not None
+    # Nothing is refused where no gradient is recorded.
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph), torch.no_grad():
+        z, _ = crm.qk_rmsnorm_rope(x, None, w, None, cs)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(z, eager)
 
 
 # ------------------------------------------------------------- run together --
@@ -754,3 +762,66 @@ def test_training_block():
     # factor of 2 for sums that cancel.
     for x, y in zip(a, b):
         assert (x.cpu().double() - y).norm() <= 20 * 2.0 ** -8 * y.norm()
+
+
+# ------------------------------------------------------------ random shapes --
+
+def spaced(g, rng, T, H, D, scale=1.0):
+    """Heads somewhere in a larger buffer: random gaps, order and offset, the
+    rest of the buffer 9.  Returns the view, its CPU copy and the buffer."""
+    step = rng.choice([1, 2, 4, 8, 8, 8])                  # alignment of strides and offset, in elements
+    up = lambda n: -(-n // step) * step
+    if rng.random() < 0.3:                                 # head-major
+        ld = up(D) + step * rng.randint(0, 2)
+        hs = up((T - 1) * ld + D) + step * rng.randint(0, 2)
+    else:
+        hs = up(D) + step * rng.randint(0, 2)
+        ld = up((H - 1) * hs + D) + step * rng.randint(0, 2)
+    off = step * rng.randint(0, 3)
+    size = off + (T - 1) * ld + (H - 1) * hs + D
+    buf = torch.full((size + 16,), 9.0, dtype=BF16, device=DEV)
+    x = (scale * torch.randn(T, H, D, generator=g)).to(BF16)
+    t = buf.as_strided((T, H, D), (ld, hs, 1), off)
+    t.copy_(x)
+    return t, x, buf
+
+
+@pytest.mark.parametrize("seed", range(48))
+def test_random_shapes(seed):
+    import random
+    rng, g = random.Random(seed), gen(seed)
+    D = rng.choice([64, 128, 256, 2 * rng.randint(1, 256), 4 * rng.randint(1, 64), 8 * rng.randint(1, 64), 16 * rng.randint(1, 32)])
+    R = rng.choice([0, D, D, D // 4 * 2, min(D, 2 * rng.randint(1, 128))])
+    Hk, pairs = rng.randint(1, 9), rng.random() < 0.5
+    Hq = Hk * rng.randint(1, 4)
+    P = rng.choice([1, 1, 2, 7, rng.randint(1, 400)])
+    T = P * rng.randint(1, max(1, 1500 // P // max(1, Hq * D // 512)) or 1)
+    wq, wk, bias = weights(g, D, rng.choice(["bf16", "f32", "bias", None]))
+    cs = rotation(g, P if R else 1, R)
+    if not R:
+        P = 1
+    (q, qc, _), (k, kc, _), (v, vc, _) = spaced(g, rng, T, Hq, D), spaced(g, rng, T, Hk, D), spaced(g, rng, T, Hk, D)
+    qo, _, qbuf = spaced(g, rng, T, Hq, D)
+    before = qbuf.clone()
+    yq, yk = crm.qk_rmsnorm_rope_fwd(q, k, wq, wk, cs, 1e-6, bias, pairs, q_out=qo)
+    for y, x, w in ((yq, qc, wq), (yk, kc, wk)):
+        qk_ref.check(y, *qk_ref.forward(x, cpu(w), cpu(cs), 1e-6, bias, pairs))
+    rest = qbuf.clone()                                    # nothing beside the output is written
+    rest.as_strided(qo.shape, qo.stride(), qo.storage_offset()).copy_(before.as_strided(qo.shape, qo.stride(), qo.storage_offset()))
+    assert torch.equal(rest, before)
+    (gq, gqc, _), (gk, gkc, _) = spaced(g, rng, T, Hq, D, 0.1), spaced(g, rng, T, Hk, D, 0.1)
+    dq, dk, dwq, dwk = crm.qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cs, 1e-6, bias, pairs)
+    for d, dw, gr, x, w in ((dq, dwq, gqc, qc, wq), (dk, dwk, gkc, kc, wk)):
+        rdx, bdx, rdw, bdw = qk_ref.backward(gr, x, cpu(w), cpu(cs), 1e-6, bias, pairs)
+        qk_ref.check(d, rdx, bdx, what="dx")
+        if w is not None:
+            qk_ref.check(dw, rdw, bdw, what="dw")
+    page = rng.choice([1, 5, 16, 64])
+    pages = -(-T // page) + 2
+    kc_, vc_, _ = caches(g, pages, page, Hk, D, BF16, rng.choice(["token", "head", "both", "mixed"]))
+    slots = torch.randperm(pages * page, generator=g)[:T].to(DEV)
+    z = crm.qk_rmsnorm_rope_append(q, k, v, wq, wk, cs, kc_, vc_, slots, 1e-6, bias, pairs)
+    got_k, got_v = (c[slots // page, slots % page] for c in (kc_, vc_))
+    qk_ref.check(z, *qk_ref.forward(qc, cpu(wq), cpu(cs), 1e-6, bias, pairs))
+    qk_ref.check(got_k, *qk_ref.forward(kc, cpu(wk), cpu(cs), 1e-6, bias, pairs))
+    assert torch.equal(got_v.cpu(), vc)
