@@ -4,11 +4,12 @@
 // holding two pieces of at most 8 elements: a lane of the rotated part (the
 // first ceil(R/16) lanes) holds [8l, 8l+8) and [R/2 + 8l, R/2 + 8l + 8), so
 // that both members of every pair are in one lane whichever pairing is used;
-// the lanes behind them hold a piece each of the two halves of the rest.  The rotation then needs no exchange between lanes, and the
-// pieces that neighbouring lanes load are neighbours in memory (16 elements in
-// a row in one lane instead, so that each load takes half of every 32-byte
-// sector: D = 256, R = 64 backward 54 instead of 46 us).  A warp works on
-// 32 / n rows at a time.
+// the lanes behind them hold a piece each of the two halves of the rest.  The
+// rotation then needs no exchange between lanes, and the pieces that
+// neighbouring lanes load are neighbours in memory (with 16 elements in a row
+// in one lane instead, each load takes half of every 32-byte sector: D = 256,
+// R = 64 backward beside a gate 54 instead of 44 us).  A warp works on 32 / n
+// rows at a time.
 //
 // A piece is moved V elements at a time: 8 (16-byte accesses), or 4 or 2 where
 // sizes, strides or addresses allow no more.
@@ -16,9 +17,9 @@
 // Rows of one tensor are numbered t H + h.  A warp walks through its rows by
 // running offsets (no division or product per row), and its rows stream
 // through a ring of shared-memory slots filled with cp.async: every thread
-// copies exactly the pieces that it will itself use, kStages - 1 steps ahead,
-// and waits only on its own copies, so that the loads in flight cost no
-// registers and no barrier.
+// copies exactly the pieces that it will itself use, the next two steps while
+// it works on two, and waits only on its own copies, so that the loads in
+// flight cost no registers and no barrier.
 #pragma once
 
 #include "common.cuh"

@@ -39,6 +39,7 @@ struct Share {
     int dt[2], dtc[2], dh[2];
     Stride in[2], in2[2], out[2];
 };
+// Steps of a run, and of a copy group of the rings.
 constexpr int kRun = 2;
 
 struct QkParams {
@@ -110,7 +111,7 @@ constexpr int kQkFwdCtasPerSm = 6;
 constexpr int kQkBwdCtasPerSm = 4;
 
 // Deals `ctas` CTAs of `warps` warps out to n tensors of heads[i] heads
-// (heads_fwd.cu): each gets its share of the rows, at least one CTA and no more
+// (heads.cu): each gets its share of the rows, at least one CTA and no more
 // than its rows fill; runs: runs of kRun steps where there are enough.
 void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_per_step, int warps, int ctas,
           bool runs);

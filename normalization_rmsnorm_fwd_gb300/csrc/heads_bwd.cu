@@ -108,50 +108,59 @@ __global__ void __launch_bounds__(kBwdThreads) k_qk_bwd_any(const QkBwdParams p,
 }
 
 // dw[j] = sum over the CTAs' partial rows, compensated, in a fixed order: a
-// block covers 32 columns of dwq (blockIdx.y 0) or dwk, warp w a contiguous
-// range of rows with up to kBatch loads in flight, then warp j adds the
-// warps' pairs of column j in a butterfly.
-constexpr int kReduceWarps = 16, kBatch = 16;
+// block covers 8 columns (a 32-byte sector of every row) of dwq (blockIdx.y 0)
+// or dwk; thread r * 8 + c adds rows r, r + 64, ... of column c, its loads in
+// flight together; lanes, then warps meet in fixed butterflies.  (32 columns a
+// block, a warp to each contiguous range of rows: 11.6 instead of 10.5 us for
+// the whole backward at T = 1024 with 32 + 8 heads of 128.)
+constexpr int kReduceThreads = 512, kReduceRows = kReduceThreads / 8, kBatch = 10;
 
-__global__ void __launch_bounds__(32 * kReduceWarps) k_qk_dw_reduce(const QkBwdParams p)
+__device__ __forceinline__ void pair_xor(float &h, float &l, int o)
+{
+    const float ch = __shfl_xor_sync(0xffffffffu, h, o), cl = __shfl_xor_sync(0xffffffffu, l, o);
+    pair_acc(h, l, ch, cl);
+}
+
+__global__ void __launch_bounds__(kReduceThreads) k_qk_dw_reduce(const QkBwdParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     CRMSN_DEBUG_ENTER(p.dbg);
-    __shared__ float sh[2][kReduceWarps][33];
+    __shared__ float sh[2][8][kReduceThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y;
-    const int col = blockIdx.x * 32 + lane, n = p.share[which].blocks;
+    const int col = blockIdx.x * 8 + (lane & 7), n = p.share[which].blocks;
     const float *part = p.part + (which ? (int64_t)p.share[0].blocks * p.D : 0) + col;
-    const int c0 = (int)((int64_t)warp * n / kReduceWarps), c1 = (int)((int64_t)(warp + 1) * n / kReduceWarps);
     float h = 0.f, l = 0.f;
-    if (col < p.D) {
-        for (int c = c0; c < c1; c += kBatch) {
-            float v[kBatch];
+    for (int r = threadIdx.x >> 3; r < n; r += kBatch * kReduceRows) {
+        float v[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                v[i] = c + i < c1 && dbg_global(part + (int64_t)(c + i) * p.D, 4, false)
-                           ? __ldcg(part + (int64_t)(c + i) * p.D) : 0.f;
+        for (int i = 0; i < kBatch; ++i) {
+            const int row = r + i * kReduceRows;
+            v[i] = col < p.D && row < n && dbg_global(part + (int64_t)row * p.D, 4, false)
+                       ? __ldcg(part + (int64_t)row * p.D) : 0.f;
+        }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                float s, e;
-                two_sum(h, v[i], s, e);
-                h = s;
-                l = __fadd_rn(l, e);
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            float s, e;
+            two_sum(h, v[i], s, e);
+            h = s;
+            l = __fadd_rn(l, e);
         }
     }
-    sh[0][warp][lane] = h;
-    sh[1][warp][lane] = l;
-    __syncthreads();
-    // Two columns a warp, 16 lanes each: lane i holds warp i's pair.
-    const int j = 2 * warp + (lane >> 4);
-    float a = sh[0][lane & 15][j], b = sh[1][lane & 15][j];
-    for (int o = 8; o > 0; o >>= 1) {
-        const float ch = __shfl_xor_sync(0xffffffffu, a, o), cl = __shfl_xor_sync(0xffffffffu, b, o);
-        pair_acc(a, b, ch, cl);
+    pair_xor(h, l, 8);
+    pair_xor(h, l, 16);
+    if (lane < 8) {
+        sh[0][lane][warp] = h;
+        sh[1][lane][warp] = l;
     }
-    const int out = blockIdx.x * 32 + j;
-    if ((lane & 15) == 0 && out < p.D) st_f32(p.dw[which] + out, joined(a, b));
+    __syncthreads();
+    // Column c of the block: lanes 16 c .. 16 c + 15 hold its warps' pairs.
+    if (warp >= 4) return;
+    const int c = threadIdx.x >> 4, w = threadIdx.x & 15, out = blockIdx.x * 8 + c;
+    h = sh[0][c][w];
+    l = sh[1][c][w];
+    for (int o = 8; o > 0; o >>= 1) pair_xor(h, l, o);
+    if (w == 0 && out < p.D) st_f32(p.dw[which] + out, joined(h, l));
 }
 
 }  // namespace
@@ -160,10 +169,11 @@ cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, int vec, int sms, cudaStream
 {
     p.lanes = row_lanes(p.R, p.D);
     const int heads[2] = {p.g[0].H, p.g[1].H};
-    // Runs of two steps (heads_fwd.cu): better up to D = 128 here (32 + 8
+    // Runs of two steps (heads.cu): better up to D = 128 here (32 + 8
     // heads, T = 16384: 87.9 -> 80.0 us; D = 64, 16 + 16: 41.5 -> 38.0), worse
     // for wider heads (16 + 2 of 256 beside a gate, T = 8192: 55.1 -> 60.0).
-    deal(p.share, heads, 2, p.T, p.cs_rows, vec > 0 ? 32 / p.lanes : 1, kBwdWarps, sms * kQkBwdCtasPerSm, p.lanes <= 8);
+    deal(p.share, heads, 2, p.T, p.cs_rows, vec > 0 ? 32 / p.lanes : 1, kBwdWarps, sms * kQkBwdCtasPerSm,
+         p.lanes <= 8);
     for (int i = 0; i < 2; ++i) {
         Share &sh = p.share[i];
         set_strides(sh.in, sh, heads[i], p.g[i].ld, p.g[i].hs);
@@ -175,8 +185,8 @@ cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, int vec, int sms, cudaStream
                   : vec > 0  ? run_qk_bwd_narrow(p, norm, vec, grid, s)
                              : launch_pdl(k_qk_bwd_any, grid, dim3(kBwdThreads), 0, s, p, norm);
     if (e != cudaSuccess || !norm) return e;
-    return launch_pdl(k_qk_dw_reduce, dim3((unsigned)((p.D + 31) / 32), p.g[1].H > 0 ? 2 : 1),
-                      dim3(32 * kReduceWarps), 0, s, p);
+    return launch_pdl(k_qk_dw_reduce, dim3((unsigned)((p.D + 7) / 8), p.g[1].H > 0 ? 2 : 1), dim3(kReduceThreads), 0, s,
+                      p);
 }
 
 cudaError_t run_qk_bwd(const QkBwdParams &p, bool norm, dim3 grid, cudaStream_t s)

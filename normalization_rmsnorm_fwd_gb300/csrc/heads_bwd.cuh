@@ -139,65 +139,66 @@ __global__ void __launch_bounds__(kBwdThreads, kQkBwdCtasPerSm) k_qk_bwd(const Q
     if (pc.rot && mine.mine > 0) ld_turn<PAIRS, V>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R, pc);
     for (int i0 = 0; i0 < mine.most; i0 += kBwdStages) {
 #pragma unroll
-      for (int stage = 0; stage < kBwdStages; ++stage) {
-        const int i = i0 + stage;
-        if (i >= mine.most) break;
-        if (stage % kRun == 0) {
+        for (int stage = 0; stage < kBwdStages; ++stage) {
+            const int i = i0 + stage;
+            if (i >= mine.most) break;
+            if (stage % kRun == 0) {
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) issue((stage + kRun + k) % kBwdStages);
-            ring_commit();
-            ring_wait<1>();
-        }
-        const bool on = i < mine.mine;
-        const BVec<8> ga = ld_slot(&sm.ring[stage][0][tid]);
-        const BVec<8> gb = ld_slot(&sm.ring[stage][1][tid]);
-        F2 a[4], b[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            a[k] = f2_bf16(ga.w[k]);
-            b[k] = f2_bf16(gb.w[k]);
-        }
-        if (pc.rot) rotate<PAIRS, true>(a, b, turn);
-        if constexpr (NORM) {
-            const BVec<8> xa = ld_slot(&sm.ring[stage][2][tid]);
-            const BVec<8> xb = ld_slot(&sm.ring[stage][3][tid]);
-            F2 va[4], vb[4], ss = f2(0.f), m2 = f2(0.f);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                va[k] = f2_bf16(xa.w[k]);
-                vb[k] = f2_bf16(xb.w[k]);
-                ss = f2_fma(va[k], va[k], ss);
-                ss = f2_fma(vb[k], vb[k], ss);
-                m2 = f2_fma(f2_mul(a[k], wa[k]), va[k], m2);
-                m2 = f2_fma(f2_mul(b[k], wb[k]), vb[k], m2);
+                for (int k = 0; k < kRun; ++k) issue((stage + kRun + k) % kBwdStages);
+                ring_commit();
+                ring_wait<1>();
             }
-            float sum[2] = {f2_lo(ss) + f2_hi(ss), f2_lo(m2) + f2_hi(m2)};
-            L.sum(sum);
-            const float rstd = __frsqrt_rn(__fmaf_rn(sum[0], p.inv_d, p.eps));
-            const F2 r2 = f2(on ? rstd : 0.f), n2 = f2(-__fmul_rn(__fmul_rn(sum[1], p.inv_d), rstd));
+            const bool on = i < mine.mine;
+            const BVec<8> ga = ld_slot(&sm.ring[stage][0][tid]);
+            const BVec<8> gb = ld_slot(&sm.ring[stage][1][tid]);
+            F2 a[4], b[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                va[k] = f2_mul(va[k], r2);
-                vb[k] = f2_mul(vb[k], r2);
-                if (on) {
-                    ba[k] = f2_fma(a[k], va[k], ba[k]);
-                    bb[k] = f2_fma(b[k], vb[k], bb[k]);
+                a[k] = f2_bf16(ga.w[k]);
+                b[k] = f2_bf16(gb.w[k]);
+            }
+            if (pc.rot) rotate<PAIRS, true>(a, b, turn);
+            if constexpr (NORM) {
+                const BVec<8> xa = ld_slot(&sm.ring[stage][2][tid]);
+                const BVec<8> xb = ld_slot(&sm.ring[stage][3][tid]);
+                F2 va[4], vb[4], ss = f2(0.f), m2 = f2(0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    va[k] = f2_bf16(xa.w[k]);
+                    vb[k] = f2_bf16(xb.w[k]);
+                    ss = f2_fma(va[k], va[k], ss);
+                    ss = f2_fma(vb[k], vb[k], ss);
+                    m2 = f2_fma(f2_mul(a[k], wa[k]), va[k], m2);
+                    m2 = f2_fma(f2_mul(b[k], wb[k]), vb[k], m2);
                 }
-                a[k] = f2_mul(r2, f2_fma(va[k], n2, f2_mul(a[k], wa[k])));
-                b[k] = f2_mul(r2, f2_fma(vb[k], n2, f2_mul(b[k], wb[k])));
+                float sum[2] = {f2_lo(ss) + f2_hi(ss), f2_lo(m2) + f2_hi(m2)};
+                L.sum(sum);
+                const float rstd = __frsqrt_rn(__fmaf_rn(sum[0], p.inv_d, p.eps));
+                const F2 r2 = f2(on ? rstd : 0.f), n2 = f2(-__fmul_rn(__fmul_rn(sum[1], p.inv_d), rstd));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    va[k] = f2_mul(va[k], r2);
+                    vb[k] = f2_mul(vb[k], r2);
+                    if (on) {
+                        ba[k] = f2_fma(a[k], va[k], ba[k]);
+                        bb[k] = f2_fma(b[k], vb[k], bb[k]);
+                    }
+                    a[k] = f2_mul(r2, f2_fma(va[k], n2, f2_mul(a[k], wa[k])));
+                    b[k] = f2_mul(r2, f2_fma(vb[k], n2, f2_mul(b[k], wb[k])));
+                }
+                if (++filled == kFold) fold();
             }
-            if (++filled == kFold) fold();
+            if (on) {
+                st_piece<V>(out.p, a, pc.ca);
+                st_piece<V>(out.p + delta, b, pc.cb);
+            }
+            const int e = stage % kRun == kRun - 1;
+            const bool over = out.step(sh.out[e], sh.dh[e], H);
+            tc += sh.dtc[e] + over;
+            if (tc >= P) tc -= P;
+            if ((over || sh.dt[e] > 0) && i + 1 < mine.mine && pc.rot)
+                ld_turn<PAIRS, V>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R, pc);
         }
-        if (on) {
-            st_piece<V>(out.p, a, pc.ca);
-            st_piece<V>(out.p + delta, b, pc.cb);
-        }
-        const int e = stage % kRun == kRun - 1;
-        const bool over = out.step(sh.out[e], sh.dh[e], H);
-        tc += sh.dtc[e] + over;
-        if (tc >= P) tc -= P;
-        if ((over || sh.dt[e] > 0) && i + 1 < mine.mine && pc.rot) ld_turn<PAIRS, V>(turn, p.cs + (int64_t)tc * p.ldcs, L.l, p.R, pc);
-      }
     }
     if constexpr (NORM) {
         fold();
