@@ -825,3 +825,35 @@ def test_random_shapes(seed):
     qk_ref.check(z, *qk_ref.forward(qc, cpu(wq), cpu(cs), 1e-6, bias, pairs))
     qk_ref.check(got_k, *qk_ref.forward(kc, cpu(wk), cpu(cs), 1e-6, bias, pairs))
     assert torch.equal(got_v.cpu(), vc)
+
+
+def test_more_than_2_31_elements():
+    # 2.3e9 elements a tensor: the last tokens' rows have the bits of a call
+    # on those tokens alone.
+    T, H, D = 280000, 64, 128
+    q = torch.randn(T, H, D, dtype=BF16, device=DEV)
+    w = weights(gen(20), D, "bf16")[0]
+    cs = crm.rope_cos_sin(torch.arange(T, device=DEV), torch.rand(D // 2, device=DEV))
+    y, _ = crm.qk_rmsnorm_rope_fwd(q, None, w, None, cs)
+    dq, _, dw, _ = crm.qk_rmsnorm_rope_bwd(y, None, q, None, w, None, cs)
+    for lo in (0, T // 2 - 3, T - 7):
+        part = slice(lo, lo + 7)
+        z, _ = crm.qk_rmsnorm_rope_fwd(q[part], None, w, None, cs[part])
+        assert torch.equal(z, y[part])
+        assert torch.equal(crm.qk_rmsnorm_rope_bwd(z, None, q[part], None, w, None, cs[part])[0], dq[part])
+    # dw against FP64 sums of the same terms, 64 u of the sum of magnitudes
+    # (qk_ref); with g = y the turned-back gradient is n up to BF16's rounding
+    # of y, so the terms are computed from y itself, a part at a time.
+    sums, sizes = torch.zeros(D, dtype=torch.float64, device=DEV), torch.zeros(D, dtype=torch.float64, device=DEV)
+    c, s = cs.double().chunk(2, -1)
+    for lo in range(0, T, 20000):
+        part = slice(lo, lo + 20000)
+        a, b = y[part].double().chunk(2, -1)
+        cc, ss = c[part, None], s[part, None]
+        u = torch.cat([a * cc + b * ss, b * cc - a * ss], -1)
+        size = torch.cat([a.abs() * cc.abs() + b.abs() * ss.abs(), b.abs() * cc.abs() + a.abs() * ss.abs()], -1)
+        x = q[part].double()
+        xhat = x / (x.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+        sums += (u * xhat).sum((0, 1))
+        sizes += (size * xhat.abs()).sum((0, 1))
+    assert ((dw.double() - sums).abs() <= 2.0 ** -18 * sizes).all()
