@@ -432,6 +432,9 @@ _F32 = torch.float32
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+_ABSENT = (None, 0, 0)           # a tensor that is not given
+
+
 def _head_tensor(t, name, dev, shape):
     """(pointer, token stride, head stride) of a BF16 tensor of this shape on
     CUDA device `dev`."""
@@ -458,17 +461,22 @@ def _first_head_tensor(t, name):
     return t.get_device(), shape, T, H, D
 
 
-def _like(t):
-    """A new contiguous tensor of t's shape and dtype."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _new_heads(t, H, D):
+    """A new contiguous tensor of t's shape and dtype, and what _head_tensor
+    says of it."""
+    n = torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return n, (n.data_ptr(), H * D, D)
 
 
 def _kv_shape(shape, t, name):
-    """The shape that t must have: `shape` with t's own heads."""
+    """The shape that t must have, `shape` with t's own heads, and those."""
     own = t.shape
     if len(own) != len(shape):
         raise ValueError(f"{name} must have {len(shape)} dimensions")
-    return (*shape[:-2], own[-2], shape[-1])
+    H = own[-2]
+    if len(own) == 3:
+        return (shape[0], H, shape[2]), H
+    return (*shape[:-2], H, shape[-1]), H
 
 
 def _weight_ptr(w, name, D, dev):
@@ -576,15 +584,17 @@ def qk_rmsnorm_rope_fwd(q, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: f
     dev, shape, T, Hq, D = _first_head_tensor(q, "q")
     qp = _head_tensor(q, "q", dev, shape)
     if q_out is None:
-        q_out = _like(q)
-    qo = _head_tensor(q_out, "q_out", dev, shape)
-    Hk, kp, ko = 0, (None, 0, 0), (None, 0, 0)
+        q_out, qo = _new_heads(q, Hq, D)
+    else:
+        qo = _head_tensor(q_out, "q_out", dev, shape)
+    Hk, kp, ko = 0, _ABSENT, _ABSENT
     if k is not None:
-        kshape = _kv_shape(shape, k, "k")
-        Hk, kp = kshape[-2], _head_tensor(k, "k", dev, kshape)
+        kshape, Hk = _kv_shape(shape, k, "k")
+        kp = _head_tensor(k, "k", dev, kshape)
         if k_out is None:
-            k_out = _like(k)
-        ko = _head_tensor(k_out, "k_out", dev, kshape)
+            k_out, ko = _new_heads(k, Hk, D)
+        else:
+            ko = _head_tensor(k_out, "k_out", dev, kshape)
     elif k_out is not None:
         raise ValueError("k_out without k")
     wqp, wkp, kind = _head_weights(wq, wk, D, dev, True, k is not None)
@@ -619,16 +629,17 @@ def qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cos_sin, eps: float = 1e-6, weight
     dev, shape, T, Hq, D = _first_head_tensor(gq, "gq")
     gqp = _head_tensor(gq, "gq", dev, shape)
     if dq is None:
-        dq = _like(gq)
-    dqp = _head_tensor(dq, "dq", dev, shape)
-    none = (None, 0, 0)
-    Hk, gkp, dkp, qp, kp = 0, none, none, none, none
+        dq, dqp = _new_heads(gq, Hq, D)
+    else:
+        dqp = _head_tensor(dq, "dq", dev, shape)
+    Hk, gkp, dkp, qp, kp = 0, _ABSENT, _ABSENT, _ABSENT, _ABSENT
     if gk is not None:
-        kshape = _kv_shape(shape, gk, "gk")
-        Hk, gkp = kshape[-2], _head_tensor(gk, "gk", dev, kshape)
+        kshape, Hk = _kv_shape(shape, gk, "gk")
+        gkp = _head_tensor(gk, "gk", dev, kshape)
         if dk is None:
-            dk = _like(gk)
-        dkp = _head_tensor(dk, "dk", dev, kshape)
+            dk, dkp = _new_heads(gk, Hk, D)
+        else:
+            dkp = _head_tensor(dk, "dk", dev, kshape)
     elif dk is not None or dwk is not None:
         raise ValueError("dk or dwk without gk")
     wqp, wkp, kind = _head_weights(wq, wk, D, dev, True, gk is not None)
@@ -681,13 +692,14 @@ def qk_rmsnorm_rope_append(q, k, v, wq, wk, cos_sin, k_cache, v_cache, slots, ep
     q None: the cache alone.  Returns q_out."""
     dev, kshape, T, Hk, D = _first_head_tensor(k, "k")
     kp, vp = _head_tensor(k, "k", dev, kshape), _head_tensor(v, "v", dev, kshape)
-    Hq, qp, qo = 0, (None, 0, 0), (None, 0, 0)
+    Hq, qp, qo = 0, _ABSENT, _ABSENT
     if q is not None:
-        shape = _kv_shape(kshape, q, "q")
-        Hq, qp = shape[-2], _head_tensor(q, "q", dev, shape)
+        shape, Hq = _kv_shape(kshape, q, "q")
+        qp = _head_tensor(q, "q", dev, shape)
         if q_out is None:
-            q_out = _like(q)
-        qo = _head_tensor(q_out, "q_out", dev, shape)
+            q_out, qo = _new_heads(q, Hq, D)
+        else:
+            qo = _head_tensor(q_out, "q_out", dev, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
     wqp, wkp, kind = _head_weights(wq, wk, D, dev, q is not None, True)
