@@ -448,7 +448,8 @@ crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_
  * workspace: at least qk_rmsnorm_rope_bwd_workspace_bytes(D, device) bytes,
  * 256-byte aligned, any content; scratch that a later call on the same
  * stream may use again (two calls that may run at the same time need two).
- * T == 0 writes dwq = dwk = 0 and launches no kernel.
+ * T == 0 writes dwq = dwk = 0 and launches no kernel; with Hk = 0 a dwk that
+ * is given is set to 0.
  */
 crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq,
                                  const void *gk, int64_t ldgk, int64_t hsgk,
@@ -522,7 +523,7 @@ crmsn_status crmsn_debug_status(uint64_t *violation);
 /*
  * rmsnorm_supports -- [API] supports_* helpers; [GUIDE] 6.1
  * is_cake_rmsnorm_train_supported.  CRMSN_OK when operation `op` (CRMSN_OP_*)
- * accepts hidden size H with weight dtype w_dtype, else the status the call
+ * accepts hidden size H (CRMSN_OP_QK_ROPE: head size) with weight dtype w_dtype, else the status the call
  * would return for that H / dtype.
  */
 crmsn_status rmsnorm_supports(int64_t H, int w_dtype, int op);

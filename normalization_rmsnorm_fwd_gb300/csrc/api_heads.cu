@@ -411,14 +411,16 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
     if (crmsn_status s = check_common(c)) return s;
     if (Hq < 1) return CRMSN_ERR_SHAPE;
     const bool norm = wq || wk;
-    float *const dw[2] = {norm && Hq ? dwq : nullptr, norm && Hk ? dwk : nullptr};
+    float *const dw[2] = {norm ? dwq : nullptr, norm ? dwk : nullptr};
     if (norm && ((Hq && !dwq) || (Hk && !dwk))) return CRMSN_ERR_NULL;
     if (!al(dw[0], 4) || !al(dw[1], 4)) return CRMSN_ERR_ALIGNMENT;
+    // Sums over no rows are zero.
+    auto zero = [&](float *w) {
+        return w ? launched(cudaMemsetAsync(w, 0, (size_t)D * sizeof(float), stream)) : CRMSN_OK;
+    };
     if (T == 0) {
-        for (float *w : dw)
-            if (w)
-                if (crmsn_status s = launched(cudaMemsetAsync(w, 0, (size_t)D * sizeof(float), stream))) return s;
-        return CRMSN_OK;
+        if (crmsn_status s = zero(dw[0])) return s;
+        return zero(dw[1]);
     }
     const Heads g[2] = {{gq, ldgq, hsgq, Hq}, {gk, ldgk, hsgk, Hk}}, dx[2] = {{dq, lddq, hsdq, Hq}, {dk, lddk, hsdk, Hk}};
     const Heads x[2] = {{norm ? q : nullptr, ldq, hsq, norm ? Hq : 0}, {norm ? k : nullptr, ldk, hsk, norm ? Hk : 0}};
@@ -454,6 +456,8 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
         p.dw[i] = dw[i];
     }
     p.part = static_cast<float *>(workspace);
+    if (Hk == 0)
+        if (crmsn_status s = zero(dw[1])) return s;
     return launched(launch_qk_bwd(p, norm, vec, sms, stream));
 }
 

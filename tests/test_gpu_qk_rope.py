@@ -255,6 +255,48 @@ def test_empty():
     assert (cache == 3).all()
 
 
+def test_no_key_heads():
+    # Keys of no heads: outputs of no heads, a zero weight gradient.
+    g = gen(6)
+    q, _ = heads(g, 5, 2, 64)
+    k = torch.zeros(5, 0, 64, dtype=BF16, device=DEV)
+    wq, wk, _ = weights(g, 64, "f32")
+    cs = rotation(g, 5, 64)
+    a, b = crm.qk_rmsnorm_rope_fwd(q, k, wq, wk, cs)
+    assert torch.equal(a, crm.qk_rmsnorm_rope_fwd(q, None, wq, None, cs)[0]) and b.shape == k.shape
+    dwk = torch.full((64,), 5.0, device=DEV)
+    out = crm.qk_rmsnorm_rope_bwd(a, b, q, k, wq, wk, cs, dwk=dwk)
+    one = crm.qk_rmsnorm_rope_bwd(a, None, q, None, wq, None, cs)
+    assert torch.equal(out[0], one[0]) and torch.equal(out[2], one[2]) and (dwk == 0).all()
+
+
+def test_batches_are_rows_of_tokens():
+    # [batch, sequence, heads, D] tensors, [batch, sequence] positions and
+    # slots: the bits of the same tokens in one dimension.
+    g = gen(7)
+    B, S, Hq, Hk, D = 3, 11, 4, 2, 64
+    (q, _), (k, _), (v, _) = (heads(g, B * S, h, D) for h in (Hq, Hk, Hk))
+    wq, wk, _ = weights(g, D, "bf16")
+    pos, f = torch.randint(999, (B, S), generator=g).to(DEV), torch.rand(D // 2, device=DEV)
+    cs, flat = crm.rope_cos_sin(pos, f), crm.rope_cos_sin(pos.view(-1), f)
+    assert cs.shape == (B, S, D) and torch.equal(cs.view(-1, D), flat)
+    q4, k4, v4 = (t.view(B, S, -1, D) for t in (q, k, v))
+    want = crm.qk_rmsnorm_rope_fwd(q, k, wq, wk, flat)
+    got = crm.qk_rmsnorm_rope_fwd(q4, k4, wq, wk, cs, q_out=torch.empty_like(q4))
+    assert all(torch.equal(a.view(b.shape), b) for a, b in zip(got, want))
+    want = crm.qk_rmsnorm_rope_bwd(q, k, q, k, wq, wk, flat)
+    got = crm.qk_rmsnorm_rope_bwd(q4, k4, q4, k4, wq, wk, cs, dk=torch.empty_like(k4))
+    assert all(torch.equal(a.view(b.shape), b) for a, b in zip(got, want))
+    kc, vc = (torch.zeros(5, 8, Hk, D, dtype=BF16, device=DEV) for _ in range(2))
+    slots = torch.randperm(40, generator=g)[:B * S].view(B, S).to(DEV)
+    crm.qk_rmsnorm_rope_append(q4, k4, v4, wq, wk, cs, kc, vc, slots)
+    assert torch.equal(vc.view(40, Hk, D)[slots], v4)
+    # The rotations of one sequence for every sequence of the batch.
+    got = crm.qk_rmsnorm_rope_fwd(q4, k4, wq, wk, cs[1])
+    want = crm.qk_rmsnorm_rope_fwd(q, k, wq, wk, cs[1:2].expand(B, S, D).reshape(-1, D))
+    assert all(torch.equal(a.view(b.shape), b) for a, b in zip(got, want))
+
+
 def test_special_values_stay_in_their_rows():
     # Infinities, NaN, zeros and the largest values give what the formula
     # gives, in their own row only (their own pair only, without norms).

@@ -227,6 +227,35 @@ def test_cpu_tensors_are_refused():
         crm.rope_cos_sin(torch.arange(4), torch.ones(32))
 
 
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    # The C call is made with the tensors' device current and on that
+    # device's current stream, whichever device is current outside.
+    seen, current = [], [0]
+
+    class Lib:
+        def rope_cos_sin(self, *args):
+            seen.append((current[0], args))
+            return 0
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.dev
+
+        def __exit__(self, *exc):
+            current[0] = self.old
+
+    monkeypatch.setattr(B, "_lib", Lib)
+    monkeypatch.setattr(B, "_current_device", lambda: current[0])
+    monkeypatch.setattr(B, "_raw_stream", lambda dev: 100 + dev)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    B._enqueue("rope_cos_sin", 0, 7)
+    B._enqueue("rope_cos_sin", 3, 7)
+    assert seen == [(0, (7, 100)), (3, (7, 103))] and current == [0]
+
+
 @pytest.mark.parametrize("pairs", [False, True])
 @pytest.mark.parametrize("weight", [True, False])
 @pytest.mark.parametrize("R", [0, 6, 10])
