@@ -380,6 +380,8 @@ crmsn_status layernorm_quant(void *out, int64_t ldo, int fp8_kind,
  *     (2j, 2j + 1) (interleaved = 1); elements R .. D-1 are not rotated.
  *   - FP32 throughout, one rounding to the output format.
  *   - T < 2^31 - 2^20, at most 4096 heads.
+ *   - The calls take their arguments as one HOST struct, read before the call
+ *     returns: zero-initialise it and set what the call uses.
  *   - Alignment: any tensor may be aligned to its own elements only.  Memory
  *     is accessed by 16, 8 or 4 bytes (8, 4 or 2 BF16 elements), the widest
  *     that divides D, R/2 and every stride and that every base is aligned to
@@ -388,6 +390,55 @@ crmsn_status layernorm_quant(void *out, int64_t ldo, int fp8_kind,
  *     element-wise form runs.  The forms agree up to the order of the sums
  *     of a row.
  */
+
+/* [T, H, D] in BF16: base, token stride and head stride. */
+typedef struct crmsn_heads {
+    void *p;
+    int64_t ld, hs;
+} crmsn_heads;
+
+/* What the query / key calls share. */
+typedef struct crmsn_qk_layer {
+    int64_t T, D;                   /* tokens, head size */
+    int64_t Hq, Hk;                 /* heads of the queries, of the keys */
+    const void *wq, *wk;            /* [D], or both NULL: no norm */
+    int32_t w_dtype;                /* CRMSN_BF16 or CRMSN_F32 */
+    int32_t interleaved;            /* 0: pairs (j, j + R/2), else (2j, 2j + 1) */
+    float weight_bias, eps;
+    const float *cos_sin;           /* [cs_rows, >= R], row stride ldcs */
+    int64_t ldcs, cs_rows, R;
+} crmsn_qk_layer;
+
+typedef struct crmsn_qk_fwd_call {
+    crmsn_qk_layer layer;
+    crmsn_heads q, k;               /* inputs */
+    crmsn_heads q_out, k_out;
+} crmsn_qk_fwd_call;
+
+typedef struct crmsn_qk_bwd_call {
+    crmsn_qk_layer layer;
+    crmsn_heads gq, gk;             /* gradients of q_out, k_out */
+    crmsn_heads q, k;               /* the forward's inputs */
+    crmsn_heads dq, dk;
+    float *dwq, *dwk;               /* FP32 [D] */
+    void *workspace;
+    uint64_t workspace_bytes;
+} crmsn_qk_bwd_call;
+
+typedef struct crmsn_qk_append_call {
+    crmsn_qk_layer layer;
+    crmsn_heads q, k, v;            /* v has Hk heads */
+    crmsn_heads q_out;
+    void *k_cache;                  /* [num_pages, page_size, Hk, D]: */
+    int64_t kps, kss, khs;          /* strides of a page, a slot, a head */
+    void *v_cache;
+    int64_t vps, vss, vhs;
+    int32_t cache_kind;             /* CRMSN_CACHE_* */
+    int32_t slot_dtype;             /* CRMSN_I32 or CRMSN_I64 */
+    int64_t num_pages, page_size;
+    const void *slots;              /* [T] */
+    const float *k_scale, *v_scale; /* FP8 caches: device FP32 [1] > 0 */
+} crmsn_qk_append_call;
 
 /*
  * rope_cos_sin -- the cosines and sines of rotary positions on 1..4 axes
@@ -424,15 +475,7 @@ crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp,
  * on the rotated pairs (a, b), y = bf16(n) elsewhere.  In place: q_out == q
  * and k_out == k (same pointer and strides) are allowed.
  */
-crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_t Hq,
-                                 const void *k, int64_t ldk, int64_t hsk, int64_t Hk,
-                                 const void *wq, const void *wk, int w_dtype,
-                                 float weight_bias, float eps,
-                                 const float *cos_sin, int64_t ldcs, int64_t cs_rows,
-                                 int64_t R, int interleaved, int64_t T, int64_t D,
-                                 void *q_out, int64_t ldqo, int64_t hsqo,
-                                 void *k_out, int64_t ldko, int64_t hsko,
-                                 cudaStream_t stream);
+crmsn_status qk_rmsnorm_rope_fwd(const crmsn_qk_fwd_call *call, cudaStream_t stream);
 
 /*
  * qk_rmsnorm_rope_bwd -- the gradient of qk_rmsnorm_rope_fwd: gq, gk are the
@@ -451,19 +494,7 @@ crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_
  * T == 0 writes dwq = dwk = 0 and launches no kernel; with Hk = 0 a dwk that
  * is given is set to 0.
  */
-crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq,
-                                 const void *gk, int64_t ldgk, int64_t hsgk,
-                                 const void *q, int64_t ldq, int64_t hsq, int64_t Hq,
-                                 const void *k, int64_t ldk, int64_t hsk, int64_t Hk,
-                                 const void *wq, const void *wk, int w_dtype,
-                                 float weight_bias, float eps,
-                                 const float *cos_sin, int64_t ldcs, int64_t cs_rows,
-                                 int64_t R, int interleaved, int64_t T, int64_t D,
-                                 void *dq, int64_t lddq, int64_t hsdq,
-                                 void *dk, int64_t lddk, int64_t hsdk,
-                                 float *dwq, float *dwk,
-                                 void *workspace, size_t workspace_bytes,
-                                 cudaStream_t stream);
+crmsn_status qk_rmsnorm_rope_bwd(const crmsn_qk_bwd_call *call, cudaStream_t stream);
 
 /* Bytes of workspace for head size D on `device`; 0 for an invalid D or device. */
 size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device);
@@ -488,20 +519,7 @@ size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device);
  * tensor returns CRMSN_ERR_ALIAS (k_cache and v_cache may interleave in one
  * buffer).  num_pages * page_size < 2^31.
  */
-crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int64_t Hq,
-                                    const void *k, int64_t ldk, int64_t hsk,
-                                    const void *v, int64_t ldv, int64_t hsv, int64_t Hk,
-                                    const void *wq, const void *wk, int w_dtype,
-                                    float weight_bias, float eps,
-                                    const float *cos_sin, int64_t ldcs, int64_t cs_rows,
-                                    int64_t R, int interleaved, int64_t T, int64_t D,
-                                    void *q_out, int64_t ldqo, int64_t hsqo,
-                                    void *k_cache, int64_t kps, int64_t kss, int64_t khs,
-                                    void *v_cache, int64_t vps, int64_t vss, int64_t vhs,
-                                    int cache_kind, int64_t num_pages, int64_t page_size,
-                                    const void *slots, int slot_dtype,
-                                    const float *k_scale, const float *v_scale,
-                                    cudaStream_t stream);
+crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream_t stream);
 
 /*
  * crmsn_debug_status -- no counterpart on the pages: the bounds guard of the

@@ -432,7 +432,7 @@ _F32 = torch.float32
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-_ABSENT = (None, 0, 0)           # a tensor that is not given
+_ABSENT = (0, 0, 0)           # a tensor that is not given
 
 
 def _head_tensor(t, name, dev, shape):
@@ -488,7 +488,7 @@ def _weight_ptr(w, name, D, dev):
 def _head_weights(wq, wk, D, dev, has_q, has_k):
     """(pointers, w_dtype) of the two weights."""
     if wq is None and wk is None:
-        return None, None, 0
+        return 0, 0, 0
     if (has_q and wq is None) or (has_k and wk is None):
         raise ValueError("wq and wk: both or neither")
     one = wq if has_q else wk
@@ -497,14 +497,14 @@ def _head_weights(wq, wk, D, dev, has_q, has_k):
         raise TypeError(f"wq and wk must be bfloat16 or float32, got {dtype}")
     if has_q and has_k and wk.dtype is not dtype:
         raise TypeError("wq and wk must have the same dtype")
-    return (_weight_ptr(wq, "wq", D, dev) if has_q else None, _weight_ptr(wk, "wk", D, dev) if has_k else None,
+    return (_weight_ptr(wq, "wq", D, dev) if has_q else 0, _weight_ptr(wk, "wk", D, dev) if has_k else 0,
             BF16 if dtype is _BF16 else F32)
 
 
 def _rotation(cos_sin, dev):
     """(pointer, row stride, rows, R) of the cosines and sines; None: none."""
     if cos_sin is None:
-        return None, 0, 1, 0
+        return 0, 0, 1, 0
     if cos_sin.dtype is not _F32 or cos_sin.get_device() != dev:
         raise TypeError(f"cos_sin must be float32 on cuda:{dev}, got {cos_sin.dtype} on {cos_sin.device}")
     if cos_sin.dim() == 2:
@@ -598,8 +598,9 @@ def qk_rmsnorm_rope_fwd(q, k, wq, wk, cos_sin, eps: float = 1e-6, weight_bias: f
     elif k_out is not None:
         raise ValueError("k_out without k")
     wqp, wkp, kind = _head_weights(wq, wk, D, dev, True, k is not None)
-    _enqueue("qk_rmsnorm_rope_fwd", dev, *qp, Hq, *kp, Hk, wqp, wkp, kind, weight_bias, eps, *_rotation(cos_sin, dev),
-             interleaved, T, D, *qo, *ko)
+    _enqueue("qk_rmsnorm_rope_fwd", dev,
+             _abi.QK_FWD_CALL.pack(T, D, Hq, Hk, wqp, wkp, kind, interleaved, weight_bias, eps, *_rotation(cos_sin, dev),
+                                   *qp, *kp, *qo, *ko))
     return q_out, k_out
 
 
@@ -643,9 +644,8 @@ def qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cos_sin, eps: float = 1e-6, weight
     elif dk is not None or dwk is not None:
         raise ValueError("dk or dwk without gk")
     wqp, wkp, kind = _head_weights(wq, wk, D, dev, True, gk is not None)
-    dwqp = dwkp = wsp = None
-    wsn = 0
-    if wqp is not None:
+    dwqp = dwkp = wsp = wsn = 0
+    if wq is not None:
         if q is None or (gk is not None and k is None):
             raise ValueError("q and k are needed with weights")
         qp = _head_tensor(q, "q", dev, shape)
@@ -665,8 +665,9 @@ def qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cos_sin, eps: float = 1e-6, weight
         wsp = workspace.data_ptr()
     elif dwq is not None or dwk is not None:
         raise ValueError("dwq or dwk without weights")
-    _enqueue("qk_rmsnorm_rope_bwd", dev, *gqp, *gkp, *qp, Hq, *kp, Hk, wqp, wkp, kind, weight_bias, eps,
-             *_rotation(cos_sin, dev), interleaved, T, D, *dqp, *dkp, dwqp, dwkp, wsp, wsn)
+    _enqueue("qk_rmsnorm_rope_bwd", dev,
+             _abi.QK_BWD_CALL.pack(T, D, Hq, Hk, wqp, wkp, kind, interleaved, weight_bias, eps, *_rotation(cos_sin, dev),
+                                   *gqp, *gkp, *qp, *kp, *dqp, *dkp, dwqp, dwkp, wsp, wsn))
     return dq, dk, dwq, dwk
 
 
@@ -674,7 +675,7 @@ def _cache_scale(scale, name, fp8, dev):
     if not fp8:
         if scale is not None:
             raise ValueError(f"{name} without an FP8 cache")
-        return None
+        return 0
     if not isinstance(scale, torch.Tensor) or scale.dtype is not _F32 or scale.get_device() != dev or scale.numel() != 1:
         raise TypeError(f"{name} must be a float32 tensor of one value on cuda:{dev}")
     return scale.data_ptr()
@@ -719,10 +720,12 @@ def qk_rmsnorm_rope_append(q, k, v, wq, wk, cos_sin, k_cache, v_cache, slots, ep
     if slots.numel() != T or not slots.is_contiguous():
         raise ValueError("slots must be contiguous with one slot per token")
     fp8 = ck != _abi.CACHE_BF16
-    _enqueue("qk_rmsnorm_rope_append", dev, *qp, Hq, *kp, *vp, Hk, wqp, wkp, kind, weight_bias, eps,
-             *_rotation(cos_sin, dev), interleaved, T, D, *qo, k_cache.data_ptr(), kps, kss, khs, v_cache.data_ptr(), vps,
-             vss, vhs, ck, cshape[0], cshape[1], slots.data_ptr(), sk, _cache_scale(k_scale, "k_scale", fp8, dev),
-             _cache_scale(v_scale, "v_scale", fp8, dev))
+    _enqueue("qk_rmsnorm_rope_append", dev,
+             _abi.QK_APPEND_CALL.pack(T, D, Hq, Hk, wqp, wkp, kind, interleaved, weight_bias, eps,
+                                      *_rotation(cos_sin, dev), *qp, *kp, *vp, *qo, k_cache.data_ptr(), kps, kss, khs,
+                                      v_cache.data_ptr(), vps, vss, vhs, ck, sk, cshape[0], cshape[1], slots.data_ptr(),
+                                      _cache_scale(k_scale, "k_scale", fp8, dev),
+                                      _cache_scale(v_scale, "v_scale", fp8, dev)))
     return q_out
 
 

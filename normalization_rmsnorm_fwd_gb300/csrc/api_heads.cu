@@ -169,6 +169,13 @@ struct Common {
     int64_t T, D, Hq, Hk;
 };
 
+Common common(const crmsn_qk_layer &l)
+{
+    return {l.wq, l.wk, l.w_dtype, l.weight_bias, l.eps, l.cos_sin, l.ldcs, l.cs_rows, l.R, l.T, l.D, l.Hq, l.Hk};
+}
+
+Heads heads(const crmsn_heads &h, int64_t H) { return {h.p, h.ld, h.hs, H}; }
+
 // What the three functions share; on CRMSN_OK with T == 0 there is nothing to
 // launch.
 crmsn_status check_common(const Common &c)
@@ -355,17 +362,16 @@ crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp, int
     return launched(launch_rope(p, vec, sms, stream));
 }
 
-crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_t Hq, const void *k, int64_t ldk,
-                                 int64_t hsk, int64_t Hk, const void *wq, const void *wk, int w_dtype,
-                                 float weight_bias, float eps, const float *cos_sin, int64_t ldcs, int64_t cs_rows,
-                                 int64_t R, int interleaved, int64_t T, int64_t D, void *q_out, int64_t ldqo,
-                                 int64_t hsqo, void *k_out, int64_t ldko, int64_t hsko, cudaStream_t stream)
+crmsn_status qk_rmsnorm_rope_fwd(const crmsn_qk_fwd_call *call, cudaStream_t stream)
 {
-    const Common c = {wq, wk, w_dtype, weight_bias, eps, cos_sin, ldcs, cs_rows, R, T, D, Hq, Hk};
+    if (!call) return CRMSN_ERR_NULL;
+    const Common c = common(call->layer);
+    const int64_t T = c.T, D = c.D, Hq = c.Hq, Hk = c.Hk;
     if (crmsn_status s = check_common(c)) return s;
     if (Hq < 1) return CRMSN_ERR_SHAPE;
     if (T == 0) return CRMSN_OK;
-    const Heads in[2] = {{q, ldq, hsq, Hq}, {k, ldk, hsk, Hk}}, out[2] = {{q_out, ldqo, hsqo, Hq}, {k_out, ldko, hsko, Hk}};
+    const Heads in[2] = {heads(call->q, Hq), heads(call->k, Hk)};
+    const Heads out[2] = {heads(call->q_out, Hq), heads(call->k_out, Hk)};
     for (int i = 0; i < 2; ++i) {
         if (crmsn_status s = check_heads(in[i], T, D)) return s;
         if (crmsn_status s = check_heads(out[i], T, D)) return s;
@@ -374,7 +380,7 @@ crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_
         return heads_vec(in[0], T, v) && heads_vec(in[1], T, v) && heads_vec(out[0], T, v) && heads_vec(out[1], T, v);
     });
     const Region ts[] = {
-        heads_region(in[0], T, D), heads_region(in[1], T, D), weight_region(c, wq), weight_region(c, wk), cs_region(c),
+        heads_region(in[0], T, D), heads_region(in[1], T, D), weight_region(c, c.wq), weight_region(c, c.wk), cs_region(c),
         heads_region(out[0], T, D, true, 0), heads_region(out[1], T, D, true, 1),
     };
     if (crmsn_status s = check_alias(ts, 7)) return s;
@@ -382,13 +388,13 @@ crmsn_status qk_rmsnorm_rope_fwd(const void *q, int64_t ldq, int64_t hsq, int64_
     if (crmsn_status s = device_sms(dev, sms)) return s;
     QkParams p{};
     CRMSN_SET_DEBUG(p, ts);
-    set_common(p, c, interleaved);
+    set_common(p, c, call->layer.interleaved);
     for (int i = 0; i < 2; ++i) {
         p.in[i] = view(in[i]);
         p.out[i] = view(out[i]);
     }
     p.heads = (int)(Hq + Hk);
-    return launched(launch_qk_fwd(p, wq || wk, false, vec, sms, stream));
+    return launched(launch_qk_fwd(p, c.wq || c.wk, false, vec, sms, stream));
 }
 
 size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device)
@@ -399,20 +405,18 @@ size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device)
     return ((size_t)sms * kQkBwdCtasPerSm * (size_t)D * sizeof(float) + 255) / 256 * 256;
 }
 
-crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, const void *gk, int64_t ldgk,
-                                 int64_t hsgk, const void *q, int64_t ldq, int64_t hsq, int64_t Hq, const void *k,
-                                 int64_t ldk, int64_t hsk, int64_t Hk, const void *wq, const void *wk, int w_dtype,
-                                 float weight_bias, float eps, const float *cos_sin, int64_t ldcs, int64_t cs_rows,
-                                 int64_t R, int interleaved, int64_t T, int64_t D, void *dq, int64_t lddq,
-                                 int64_t hsdq, void *dk, int64_t lddk, int64_t hsdk, float *dwq, float *dwk,
-                                 void *workspace, size_t workspace_bytes, cudaStream_t stream)
+crmsn_status qk_rmsnorm_rope_bwd(const crmsn_qk_bwd_call *call, cudaStream_t stream)
 {
-    const Common c = {wq, wk, w_dtype, weight_bias, eps, cos_sin, ldcs, cs_rows, R, T, D, Hq, Hk};
+    if (!call) return CRMSN_ERR_NULL;
+    const Common c = common(call->layer);
+    const int64_t T = c.T, D = c.D, Hq = c.Hq, Hk = c.Hk;
+    void *const workspace = call->workspace;
+    const uint64_t workspace_bytes = call->workspace_bytes;
     if (crmsn_status s = check_common(c)) return s;
     if (Hq < 1) return CRMSN_ERR_SHAPE;
-    const bool norm = wq || wk;
-    float *const dw[2] = {norm ? dwq : nullptr, norm ? dwk : nullptr};
-    if (norm && ((Hq && !dwq) || (Hk && !dwk))) return CRMSN_ERR_NULL;
+    const bool norm = c.wq || c.wk;
+    float *const dw[2] = {norm ? call->dwq : nullptr, norm ? call->dwk : nullptr};
+    if (norm && (!dw[0] || (Hk && !dw[1]))) return CRMSN_ERR_NULL;
     if (!al(dw[0], 4) || !al(dw[1], 4)) return CRMSN_ERR_ALIGNMENT;
     // Sums over no rows are zero.
     auto zero = [&](float *w) {
@@ -422,8 +426,8 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
         if (crmsn_status s = zero(dw[0])) return s;
         return zero(dw[1]);
     }
-    const Heads g[2] = {{gq, ldgq, hsgq, Hq}, {gk, ldgk, hsgk, Hk}}, dx[2] = {{dq, lddq, hsdq, Hq}, {dk, lddk, hsdk, Hk}};
-    const Heads x[2] = {{norm ? q : nullptr, ldq, hsq, norm ? Hq : 0}, {norm ? k : nullptr, ldk, hsk, norm ? Hk : 0}};
+    const Heads g[2] = {heads(call->gq, Hq), heads(call->gk, Hk)}, dx[2] = {heads(call->dq, Hq), heads(call->dk, Hk)};
+    const Heads x[2] = {heads(call->q, norm ? Hq : 0), heads(call->k, norm ? Hk : 0)};
     for (int i = 0; i < 2; ++i)
         for (const Heads *h : {&g[i], &x[i], &dx[i]})
             if (crmsn_status s = check_heads(*h, T, D)) return s;
@@ -432,10 +436,10 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
                heads_vec(dx[0], T, v) && heads_vec(dx[1], T, v);
     });
     if (norm && !workspace) return CRMSN_ERR_NULL;
-    if (norm && (workspace_bytes == 0 || workspace_bytes > (size_t)1 << 40)) return CRMSN_ERR_WORKSPACE;
+    if (norm && (workspace_bytes == 0 || workspace_bytes > (uint64_t)1 << 40)) return CRMSN_ERR_WORKSPACE;
     const Region ts[] = {
         heads_region(g[0], T, D), heads_region(g[1], T, D), heads_region(x[0], T, D), heads_region(x[1], T, D),
-        weight_region(c, wq), weight_region(c, wk), cs_region(c),
+        weight_region(c, c.wq), weight_region(c, c.wk), cs_region(c),
         heads_region(dx[0], T, D, true, 0), heads_region(dx[1], T, D, true, 1),
         vec_region(dw[0], D, 4, true), vec_region(dw[1], D, 4, true),
         vec_region(norm ? workspace : nullptr, (int64_t)workspace_bytes, 1, true),
@@ -447,7 +451,7 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
         return CRMSN_ERR_WORKSPACE;
     QkBwdParams p{};
     CRMSN_SET_DEBUG(p, ts);
-    set_common(p, c, interleaved);
+    set_common(p, c, call->layer.interleaved);
     for (int i = 0; i < 2; ++i) {
         p.g[i] = view(g[i]);
         p.x[i] = view(x[i]);
@@ -461,70 +465,66 @@ crmsn_status qk_rmsnorm_rope_bwd(const void *gq, int64_t ldgq, int64_t hsgq, con
     return launched(launch_qk_bwd(p, norm, vec, sms, stream));
 }
 
-crmsn_status qk_rmsnorm_rope_append(const void *q, int64_t ldq, int64_t hsq, int64_t Hq, const void *k, int64_t ldk,
-                                    int64_t hsk, const void *v, int64_t ldv, int64_t hsv, int64_t Hk, const void *wq,
-                                    const void *wk, int w_dtype, float weight_bias, float eps, const float *cos_sin,
-                                    int64_t ldcs, int64_t cs_rows, int64_t R, int interleaved, int64_t T, int64_t D,
-                                    void *q_out, int64_t ldqo, int64_t hsqo, void *k_cache, int64_t kps, int64_t kss,
-                                    int64_t khs, void *v_cache, int64_t vps, int64_t vss, int64_t vhs,
-                                    int cache_kind, int64_t num_pages, int64_t page_size, const void *slots,
-                                    int slot_dtype, const float *k_scale, const float *v_scale, cudaStream_t stream)
+crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream_t stream)
 {
-    const Common c = {wq, wk, w_dtype, weight_bias, eps, cos_sin, ldcs, cs_rows, R, T, D, Hq, Hk};
+    if (!call) return CRMSN_ERR_NULL;
+    const crmsn_qk_append_call &a = *call;
+    const Common c = common(a.layer);
+    const int64_t T = c.T, D = c.D, Hq = c.Hq, Hk = c.Hk, num_pages = a.num_pages, page_size = a.page_size;
     if (crmsn_status s = check_common(c)) return s;
-    if (cache_kind != CRMSN_CACHE_BF16 && cache_kind != CRMSN_CACHE_E4M3 && cache_kind != CRMSN_CACHE_E5M2)
+    if (a.cache_kind != CRMSN_CACHE_BF16 && a.cache_kind != CRMSN_CACHE_E4M3 && a.cache_kind != CRMSN_CACHE_E5M2)
         return CRMSN_ERR_DTYPE;
-    if (slot_dtype != CRMSN_I32 && slot_dtype != CRMSN_I64) return CRMSN_ERR_DTYPE;
+    if (a.slot_dtype != CRMSN_I32 && a.slot_dtype != CRMSN_I64) return CRMSN_ERR_DTYPE;
     if (Hk < 1 || num_pages < 0 || page_size < 1 || page_size > 0x7fffffff || num_pages > 0x7fffffff / page_size)
         return CRMSN_ERR_SHAPE;
     if (T == 0) return CRMSN_OK;
-    const bool fp8 = cache_kind != CRMSN_CACHE_BF16;
+    const bool fp8 = a.cache_kind != CRMSN_CACHE_BF16;
     const int es = fp8 ? 1 : 2;
-    const Heads in[3] = {{q, ldq, hsq, Hq}, {k, ldk, hsk, Hk}, {v, ldv, hsv, Hk}}, out = {q_out, ldqo, hsqo, Hq};
+    const Heads in[3] = {heads(a.q, Hq), heads(a.k, Hk), heads(a.v, Hk)}, out = heads(a.q_out, Hq);
     for (const Heads &h : in)
         if (crmsn_status s = check_heads(h, T, D)) return s;
     if (crmsn_status s = check_heads(out, T, D)) return s;
-    if (!slots || (fp8 && (!k_scale || !v_scale))) return CRMSN_ERR_NULL;
-    if (!al(slots, slot_dtype == CRMSN_I64 ? 8 : 4) || (fp8 && (!al(k_scale, 4) || !al(v_scale, 4))))
+    if (!a.slots || (fp8 && (!a.k_scale || !a.v_scale))) return CRMSN_ERR_NULL;
+    if (!al(a.slots, a.slot_dtype == CRMSN_I64 ? 8 : 4) || (fp8 && (!al(a.k_scale, 4) || !al(a.v_scale, 4))))
         return CRMSN_ERR_ALIGNMENT;
     if (num_pages > 0) {
-        if (crmsn_status s = check_cache(k_cache, kps, kss, khs, es, num_pages, page_size, Hk, D)) return s;
-        if (crmsn_status s = check_cache(v_cache, vps, vss, vhs, es, num_pages, page_size, Hk, D)) return s;
+        if (crmsn_status s = check_cache(a.k_cache, a.kps, a.kss, a.khs, es, num_pages, page_size, Hk, D)) return s;
+        if (crmsn_status s = check_cache(a.v_cache, a.vps, a.vss, a.vhs, es, num_pages, page_size, Hk, D)) return s;
     }
     const int vec = widest(c, [&](int v) {
         return heads_vec(in[0], T, v) && heads_vec(in[1], T, v) && heads_vec(in[2], T, v) && heads_vec(out, T, v) &&
-               (num_pages == 0 || (cache_vec(k_cache, kps, kss, khs, es, num_pages, page_size, Hk, v) &&
-                                   cache_vec(v_cache, vps, vss, vhs, es, num_pages, page_size, Hk, v)));
+               (num_pages == 0 || (cache_vec(a.k_cache, a.kps, a.kss, a.khs, es, num_pages, page_size, Hk, v) &&
+                                   cache_vec(a.v_cache, a.vps, a.vss, a.vhs, es, num_pages, page_size, Hk, v)));
     });
     const int64_t pages = num_pages > 0 ? num_pages : 1;
     const Region ts[] = {
         heads_region(in[0], T, D), heads_region(in[1], T, D), heads_region(in[2], T, D),
-        weight_region(c, wq), weight_region(c, wk), cs_region(c),
-        vec_region(slots, T, slot_dtype == CRMSN_I64 ? 8 : 4),
-        vec_region(fp8 ? k_scale : nullptr, 1, 4), vec_region(fp8 ? v_scale : nullptr, 1, 4),
+        weight_region(c, c.wq), weight_region(c, c.wk), cs_region(c),
+        vec_region(a.slots, T, a.slot_dtype == CRMSN_I64 ? 8 : 4),
+        vec_region(fp8 ? a.k_scale : nullptr, 1, 4), vec_region(fp8 ? a.v_scale : nullptr, 1, 4),
         heads_region(out, T, D, true, 0),
-        cache_region(num_pages > 0 ? k_cache : nullptr, kps, kss, khs, es, pages, page_size, Hk, D),
-        cache_region(num_pages > 0 ? v_cache : nullptr, vps, vss, vhs, es, pages, page_size, Hk, D),
+        cache_region(num_pages > 0 ? a.k_cache : nullptr, a.kps, a.kss, a.khs, es, pages, page_size, Hk, D),
+        cache_region(num_pages > 0 ? a.v_cache : nullptr, a.vps, a.vss, a.vhs, es, pages, page_size, Hk, D),
     };
     if (crmsn_status s = check_alias(ts, 12)) return s;
     int dev, sms;
     if (crmsn_status s = device_sms(dev, sms)) return s;
     QkParams p{};
     CRMSN_SET_DEBUG(p, ts);
-    set_common(p, c, interleaved);
+    set_common(p, c, call->layer.interleaved);
     for (int i = 0; i < 3; ++i) p.in[i] = view(in[i]);
     p.out[0] = view(out);
-    p.cache[0] = {k_cache, kps, kss, khs};
-    p.cache[1] = {v_cache, vps, vss, vhs};
-    p.kind = cache_kind;
-    p.scale[0] = k_scale;
-    p.scale[1] = v_scale;
-    p.slots = slots;
-    p.slot64 = slot_dtype == CRMSN_I64;
+    p.cache[0] = {a.k_cache, a.kps, a.kss, a.khs};
+    p.cache[1] = {a.v_cache, a.vps, a.vss, a.vhs};
+    p.kind = a.cache_kind;
+    p.scale[0] = a.k_scale;
+    p.scale[1] = a.v_scale;
+    p.slots = a.slots;
+    p.slot64 = a.slot_dtype == CRMSN_I64;
     p.num_slots = num_pages * page_size;
     p.page_size = (int)page_size;
     p.heads = (int)(Hq + 2 * Hk);
-    return launched(launch_qk_fwd(p, wq || wk, true, vec, sms, stream));
+    return launched(launch_qk_fwd(p, c.wq || c.wk, true, vec, sms, stream));
 }
 
 }  // extern "C"

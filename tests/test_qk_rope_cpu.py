@@ -2,6 +2,7 @@
 addresses are never dereferenced), the binding's layouts and refusals, and the
 FP64 forms that the GPU tests compare with, against differences."""
 import ctypes
+import subprocess
 
 import pytest
 import torch
@@ -20,26 +21,87 @@ G = 1 << 30            # distance between the fake tensors
 
 @pytest.fixture(scope="module")
 def L():
+    if torch.cuda.is_available():
+        pytest.skip("fake device addresses: only where no GPU could follow them")
     nbuild.build()
     return _abi.load()
 
 
-def call(L, name, names, defaults, kw):
-    a = dict(defaults)
+def fields(text):
+    """ctypes fields of a struct of the header, each with its short name here:
+    "p" pointer, "l" int64, "i" int32, "f" float, "h" crmsn_heads."""
+    kinds = {"p": [("", ctypes.c_void_p)], "l": [("", ctypes.c_int64)], "i": [("", ctypes.c_int32)], "f": [("", ctypes.c_float)]}
+    out = []
+    for word in text.split():
+        kind, name = word.split(":")
+        if kind == "h":
+            out += [(name, ctypes.c_void_p), ("ld" + name, ctypes.c_int64), ("hs" + name, ctypes.c_int64)]
+        else:
+            out += [(name, t) for _, t in kinds[kind]]
+    return out
+
+
+LAYER = "l:T l:D l:Hq l:Hk p:wq p:wk i:wd i:inter f:bias f:eps p:cs l:ldcs l:rows l:R "
+
+
+class Fwd(ctypes.Structure):
+    _fields_ = fields(LAYER + "h:q h:k h:qo h:ko")
+
+
+class Bwd(ctypes.Structure):
+    _fields_ = fields(LAYER + "h:gq h:gk h:q h:k h:dq h:dk p:dwq p:dwk p:ws l:wsn")
+
+
+class Append(ctypes.Structure):
+    _fields_ = fields(LAYER + "h:q h:k h:v h:qo p:kc l:kps l:kss l:khs p:vc l:vps l:vss l:vhs i:kind i:sd l:pages l:page "
+                      "p:slots p:ks p:vs")
+
+
+def call(L, name, struct, defaults, kw):
     for k in kw:
-        assert k in a, k
-    a.update(kw)
-    return getattr(L, name)(*(a[n] for n in names))
+        assert k in defaults, k
+    names = {n for n, _ in struct._fields_}
+    a = struct(**{k: v for k, v in {**defaults, **kw}.items() if k in names})
+    return getattr(L, name)(bytes(a), None)
 
 
-FWD = "q ldq hsq Hq k ldk hsk Hk wq wk wd bias eps cs ldcs rows R inter T D qo ldqo hsqo ko ldko hsko stream".split()
+def test_packed_calls_have_the_structs_layout():
+    for packed, struct in ((_abi.QK_FWD_CALL, Fwd), (_abi.QK_BWD_CALL, Bwd), (_abi.QK_APPEND_CALL, Append)):
+        values = [1.5 + i if t is ctypes.c_float else 1000 + i for i, (_, t) in enumerate(struct._fields_)]
+        assert packed.pack(*values) == bytes(struct(*values))
+
+
+def test_structs_are_the_headers(tmp_path):
+    # Sizes and offsets as a C compiler sees them.
+    last = {"layer": "layer.R", "Fwd": "k_out.hs", "Bwd": "workspace_bytes", "Append": "v_scale"}
+    source = tmp_path / "layout.c"
+    names = {"Fwd": "crmsn_qk_fwd_call", "Bwd": "crmsn_qk_bwd_call", "Append": "crmsn_qk_append_call"}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "crmsnorm.h"', "int main(void) {"]
+    for k, n in names.items():
+        lines.append(f'printf("%zu %zu %zu %zu\\n", sizeof({n}), offsetof({n}, layer.interleaved), '
+                     f"offsetof({n}, {last['layer']}), offsetof({n}, {last[k]}));")
+    source.write_text("\n".join(lines + ["return 0; }"]))
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", nbuild.INCLUDE, "-I", "/usr/local/cuda/include", str(source), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")
+    for line, struct, end in zip(out, (Fwd, Bwd, Append), ("hsko", "wsn", "vs")):
+        assert [int(x) for x in line.split()] == [ctypes.sizeof(struct), struct.inter.offset, struct.R.offset,
+                                                  getattr(struct, end).offset]
+
+
+def test_no_struct(L):
+    assert L.qk_rmsnorm_rope_fwd(None, None) == NULL
+    assert L.qk_rmsnorm_rope_bwd(None, None) == NULL
+    assert L.qk_rmsnorm_rope_append(None, None) == NULL
+
+
 HEADS = dict(q=A, ldq=1024, hsq=128, Hq=8, k=A + G, ldk=256, hsk=128, Hk=2, wq=A + 2 * G, wk=A + 3 * G, wd=0, bias=0.0,
              eps=1e-6, cs=A + 4 * G, ldcs=128, rows=16, R=128, inter=0, T=16, D=128, qo=A + 5 * G, ldqo=1024, hsqo=128,
-             ko=A + 6 * G, ldko=256, hsko=128, stream=None)
+             ko=A + 6 * G, ldko=256, hsko=128)
 
 
 def fwd(L, **kw):
-    return call(L, "qk_rmsnorm_rope_fwd", FWD, HEADS, kw)
+    return call(L, "qk_rmsnorm_rope_fwd", Fwd, HEADS, kw)
 
 
 def test_fwd_refusals(L):
@@ -93,14 +155,10 @@ def test_fwd_alias(L):
     assert fwd(L, **mixed, qo=A + 256, ldqo=2048, hsqo=256, ldko=1024) == ALIAS
 
 
-BWD = ("gq ldgq hsgq gk ldgk hsgk q ldq hsq Hq k ldk hsk Hk wq wk wd bias eps cs ldcs rows R inter T D dq lddq hsdq dk lddk "
-       "hsdk dwq dwk ws wsn stream").split()
-
-
 def bwd(L, **kw):
     d = dict(HEADS, gq=A + 7 * G, ldgq=1024, hsgq=128, gk=A + 8 * G, ldgk=256, hsgk=128, dq=A + 9 * G, lddq=1024, hsdq=128,
              dk=A + 10 * G, lddk=256, hsdk=128, dwq=A + 11 * G, dwk=A + 12 * G, ws=A + 13 * G, wsn=1 << 24)
-    return call(L, "qk_rmsnorm_rope_bwd", BWD, d, kw)
+    return call(L, "qk_rmsnorm_rope_bwd", Bwd, d, kw)
 
 
 def test_bwd_refusals(L):
@@ -119,14 +177,10 @@ def test_bwd_refusals(L):
     assert L.qk_rmsnorm_rope_bwd_workspace_bytes(514, 0) == 0
 
 
-APPEND = ("q ldq hsq Hq k ldk hsk v ldv hsv Hk wq wk wd bias eps cs ldcs rows R inter T D qo ldqo hsqo kc kps kss khs vc vps "
-          "vss vhs kind pages page slots sd ks vs stream").split()
-
-
 def append(L, **kw):
     d = dict(HEADS, v=A + 7 * G, ldv=256, hsv=128, kc=A + 8 * G, kps=4096, kss=256, khs=128, vc=A + 9 * G, vps=4096, vss=256,
              vhs=128, kind=0, pages=10, page=16, slots=A + 10 * G, sd=1, ks=None, vs=None)
-    return call(L, "qk_rmsnorm_rope_append", APPEND, d, kw)
+    return call(L, "qk_rmsnorm_rope_append", Append, d, kw)
 
 
 def test_append_refusals(L):
@@ -161,7 +215,9 @@ ROPE = "pos pd ldp axes parts mixed freq scaling T R out ldo stream".split()
 def rope(L, parts=None, **kw):
     d = dict(pos=A, pd=1, ldp=16, axes=1, mixed=0, freq=A + G, scaling=1.0, T=16, R=128, out=A + 2 * G, ldo=128, stream=None,
              parts=None if parts is None else (ctypes.c_int32 * len(parts))(*parts))
-    return call(L, "rope_cos_sin", ROPE, d, kw)
+    for k in kw:
+        assert k in d, k
+    return L.rope_cos_sin(*({**d, **kw}[n] for n in ROPE))
 
 
 def test_rope_refusals(L):
