@@ -453,18 +453,27 @@ typedef struct crmsn_qk_append_call {
  * |inv_freq| < 2^40 (columns beyond that, infinite or NaN give NaN).  The
  * product p * inv_freq is reduced modulo 2 pi exactly (64-bit fractions of a
  * turn): the angle is off by less than 2^-61 |p|, whatever inv_freq is.
- * sections: HOST array of n_axes column counts >= 0 with sum R/2, or NULL
- * with n_axes = 1.  interleaved_axes = 0: the columns of axis 0 come first,
- * then those of axis 1, ...; interleaved_axes = 1: column j belongs to axis
- * j % n_axes while that axis has columns left (j < n_axes * sections[axis]),
- * else to axis 0 (CRMSN_ERR_SHAPE when an axis then has another count).
- * T == 0 returns CRMSN_OK without a launch.
+ * sections: the columns of each axis, >= 0 with sum R/2 (one axis: 0 stands
+ * for R/2).  interleaved_axes = 0: the columns of axis 0 come first, then
+ * those of axis 1, ...; else column j belongs to axis j % n_axes while that
+ * axis has columns left (j < n_axes * sections[axis]), else to axis 0
+ * (CRMSN_ERR_SHAPE when an axis then has another count).  T == 0 returns
+ * CRMSN_OK without a launch.
  */
-crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp,
-                          int n_axes, const int32_t *sections,
-                          int interleaved_axes, const float *inv_freq,
-                          float scaling, int64_t T, int64_t R, float *cos_sin,
-                          int64_t ldcs, cudaStream_t stream);
+typedef struct crmsn_rope_call {
+    const void *positions;
+    int64_t ldp;
+    int32_t pos_dtype, n_axes;
+    int32_t sections[4];
+    int32_t interleaved_axes;
+    float scaling;
+    const float *inv_freq;
+    int64_t T, R;
+    float *cos_sin;                 /* [T, >= R], row stride ldcs */
+    int64_t ldcs;
+} crmsn_rope_call;
+
+crmsn_status rope_cos_sin(const crmsn_rope_call *call, cudaStream_t stream);
 
 /*
  * qk_rmsnorm_rope_fwd -- per row x of q (weight wq) and of k (weight wk):

@@ -35,7 +35,7 @@ SIGNATURES = {
     "fused_rmsnorm_silu": (_ST, [_P, _I, _INT, _P, _I, _P, _INT, _F, _P, _F, _I, _I, _P, _P]),
     "layernorm": (_ST, [_P, _I, _P, _I, _P, _P, _F, _I, _I, _P, _P, _P]),
     "layernorm_quant": (_ST, [_P, _I, _INT, _P, _I, _P, _P, _P, _F, _I, _I, _P, _P, _P]),
-    "rope_cos_sin": (_ST, [_P, _INT, _I, _INT, _P, _INT, _P, _F, _I, _I, _P, _I, _P]),
+    "rope_cos_sin": (_ST, [ctypes.c_char_p, _P]),
     "qk_rmsnorm_rope_fwd": (_ST, [ctypes.c_char_p, _P]),
     "qk_rmsnorm_rope_bwd": (_ST, [ctypes.c_char_p, _P]),
     "qk_rmsnorm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _INT]),
@@ -48,6 +48,7 @@ SIGNATURES = {
 # 40 values as single ctypes arguments 3.8.
 _LAYER = "qqqqPPiiffPqqq"        # crmsn_qk_layer
 _HEADS = "Pqq"                   # crmsn_heads
+ROPE_CALL = struct.Struct("@PqiiiiiiifPqqPq")
 QK_FWD_CALL = struct.Struct("@" + _LAYER + 4 * _HEADS)
 QK_BWD_CALL = struct.Struct("@" + _LAYER + 6 * _HEADS + "PPPQ")
 QK_APPEND_CALL = struct.Struct("@" + _LAYER + 4 * _HEADS + "PqqqPqqqiiqqPPP")

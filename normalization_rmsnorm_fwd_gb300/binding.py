@@ -530,6 +530,9 @@ def _enqueue(name, dev, *args):
         check(name, st)
 
 
+_ALL_COLUMNS = (0, 0, 0, 0)     # of the one axis
+
+
 def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = False,
                  scaling: float = 1.0, out=None):
     """Cosines and sines of rotary positions, FP32 [..., R] (R/2 cosines, then
@@ -546,12 +549,12 @@ def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = Fa
     if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous 1-D tensor")
     R = 2 * inv_freq.shape[0]
-    shape, ldp, axes, parts = positions.shape, 0, 1, None
+    shape, ldp, axes, parts = positions.shape, 0, 1, _ALL_COLUMNS
     if sections is not None:
         axes = len(sections)
-        if axes < 1:
-            raise ValueError("sections must name at least one axis")
-        parts = (_abi.ctypes.c_int32 * axes)(*sections)
+        if not 1 <= axes <= 4:
+            raise ValueError("sections must name one to four axes")
+        parts = (*sections, 0, 0, 0)[:4]
     if axes > 1:
         if len(shape) < 2 or shape[0] != axes:
             raise ValueError(f"positions must be [{axes}, ...]")
@@ -569,8 +572,9 @@ def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = Fa
             raise TypeError(f"out must be float32 {whole} on cuda:{dev}")
         ldo = as_rows(out, "out")[2]
     T = shape[0] if len(shape) == 1 else math.prod(shape)
-    _enqueue("rope_cos_sin", dev, positions.data_ptr(), kind, ldp, axes, parts, interleaved_axes,
-             inv_freq.data_ptr(), scaling, T, R, out.data_ptr(), ldo)
+    _enqueue("rope_cos_sin", dev,
+             _abi.ROPE_CALL.pack(positions.data_ptr(), ldp, kind, axes, *parts, interleaved_axes, scaling,
+                                 inv_freq.data_ptr(), T, R, out.data_ptr(), ldo))
     return out
 
 

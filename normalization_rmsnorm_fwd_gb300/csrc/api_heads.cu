@@ -306,31 +306,30 @@ Region cache_region(const void *p, int64_t ps, int64_t ss, int64_t hs, int es, i
 // ======================================================================
 extern "C" {
 
-crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp, int n_axes, const int32_t *sections,
-                          int interleaved_axes, const float *inv_freq, float scaling, int64_t T, int64_t R,
-                          float *cos_sin, int64_t ldcs, cudaStream_t stream)
+crmsn_status rope_cos_sin(const crmsn_rope_call *call, cudaStream_t stream)
 {
+    if (!call) return CRMSN_ERR_NULL;
+    const int64_t T = call->T, R = call->R, ldp = call->ldp, ldcs = call->ldcs;
+    const int n_axes = call->n_axes, pos_dtype = call->pos_dtype;
+    const void *const positions = call->positions;
+    const float *const inv_freq = call->inv_freq;
+    float *const cos_sin = call->cos_sin;
     if (T < 0 || T > kMaxTokens || R < 2 || (R & 1) || R > CRMSN_MAX_HEAD_DIM || n_axes < 1 || n_axes > 4)
         return CRMSN_ERR_SHAPE;
     if (pos_dtype != CRMSN_I32 && pos_dtype != CRMSN_I64) return CRMSN_ERR_DTYPE;
-    if (!std::isfinite(scaling)) return CRMSN_ERR_ARG;
+    if (!std::isfinite(call->scaling)) return CRMSN_ERR_ARG;
     const int half = (int)(R / 2);
     RopeParams p{};
-    if (!sections) {
-        if (n_axes != 1) return CRMSN_ERR_NULL;
-        p.sections[0] = half;
-    } else {
-        int64_t sum = 0;
-        for (int a = 0; a < n_axes; ++a) {
-            if (sections[a] < 0 || sections[a] > half) return CRMSN_ERR_SHAPE;
-            p.sections[a] = sections[a];
-            sum += sections[a];
-        }
-        if (sum != half) return CRMSN_ERR_SHAPE;
-        // Interleaved: the last column of every later axis must exist.
-        for (int a = 1; interleaved_axes && a < n_axes; ++a)
-            if (sections[a] > 0 && (int64_t)n_axes * (sections[a] - 1) + a >= half) return CRMSN_ERR_SHAPE;
+    int64_t sum = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        p.sections[a] = n_axes == 1 && call->sections[0] == 0 ? half : call->sections[a];
+        if (p.sections[a] < 0 || p.sections[a] > half) return CRMSN_ERR_SHAPE;
+        sum += p.sections[a];
     }
+    if (sum != half) return CRMSN_ERR_SHAPE;
+    // Interleaved: the last column of every later axis must exist.
+    for (int a = 1; call->interleaved_axes && a < n_axes; ++a)
+        if (p.sections[a] > 0 && (int64_t)n_axes * (p.sections[a] - 1) + a >= half) return CRMSN_ERR_SHAPE;
     if (T == 0) return CRMSN_OK;
     if (!positions || !inv_freq || !cos_sin) return CRMSN_ERR_NULL;
     const int es = pos_dtype == CRMSN_I64 ? 8 : 4;
@@ -351,9 +350,9 @@ crmsn_status rope_cos_sin(const void *positions, int pos_dtype, int64_t ldp, int
     p.pos64 = pos_dtype == CRMSN_I64;
     p.ldp = ldp;
     p.axes = n_axes;
-    p.mixed = interleaved_axes != 0;
+    p.mixed = call->interleaved_axes != 0;
     p.freq = inv_freq;
-    p.scaling = scaling;
+    p.scaling = call->scaling;
     p.T = T;
     p.half = half;
     p.out = cos_sin;

@@ -66,7 +66,7 @@ def call(L, name, struct, defaults, kw):
 
 
 def test_packed_calls_have_the_structs_layout():
-    for packed, struct in ((_abi.QK_FWD_CALL, Fwd), (_abi.QK_BWD_CALL, Bwd), (_abi.QK_APPEND_CALL, Append)):
+    for packed, struct in ((_abi.ROPE_CALL, Rope), (_abi.QK_FWD_CALL, Fwd), (_abi.QK_BWD_CALL, Bwd), (_abi.QK_APPEND_CALL, Append)):
         values = [1.5 + i if t is ctypes.c_float else 1000 + i for i, (_, t) in enumerate(struct._fields_)]
         assert packed.pack(*values) == bytes(struct(*values))
 
@@ -74,19 +74,21 @@ def test_packed_calls_have_the_structs_layout():
 def test_structs_are_the_headers(tmp_path):
     # Sizes and offsets as a C compiler sees them.
     last = {"layer": "layer.R", "Fwd": "k_out.hs", "Bwd": "workspace_bytes", "Append": "v_scale"}
+    rope = 'printf("%zu %zu %zu\\n", sizeof(crmsn_rope_call), offsetof(crmsn_rope_call, inv_freq), offsetof(crmsn_rope_call, ldcs));'
     source = tmp_path / "layout.c"
     names = {"Fwd": "crmsn_qk_fwd_call", "Bwd": "crmsn_qk_bwd_call", "Append": "crmsn_qk_append_call"}
     lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "crmsnorm.h"', "int main(void) {"]
     for k, n in names.items():
         lines.append(f'printf("%zu %zu %zu %zu\\n", sizeof({n}), offsetof({n}, layer.interleaved), '
                      f"offsetof({n}, {last['layer']}), offsetof({n}, {last[k]}));")
-    source.write_text("\n".join(lines + ["return 0; }"]))
+    source.write_text("\n".join(lines + [rope, "return 0; }"]))
     exe = tmp_path / "layout"
     subprocess.run(["gcc", "-I", nbuild.INCLUDE, "-I", "/usr/local/cuda/include", str(source), "-o", str(exe)], check=True)
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")
     for line, struct, end in zip(out, (Fwd, Bwd, Append), ("hsko", "wsn", "vs")):
         assert [int(x) for x in line.split()] == [ctypes.sizeof(struct), struct.inter.offset, struct.R.offset,
                                                   getattr(struct, end).offset]
+    assert [int(x) for x in out[3].split()] == [ctypes.sizeof(Rope), Rope.freq.offset, Rope.ldo.offset]
 
 
 def test_no_struct(L):
@@ -209,21 +211,21 @@ def test_append_refusals(L):
     assert append(L, T=0, q=None, k=None, v=None, qo=None, slots=None) == OK
 
 
-ROPE = "pos pd ldp axes parts mixed freq scaling T R out ldo stream".split()
+class Rope(ctypes.Structure):
+    _fields_ = fields("p:pos l:ldp i:pd i:axes i:s0 i:s1 i:s2 i:s3 i:mixed f:scaling p:freq l:T l:R p:out l:ldo")
 
 
-def rope(L, parts=None, **kw):
-    d = dict(pos=A, pd=1, ldp=16, axes=1, mixed=0, freq=A + G, scaling=1.0, T=16, R=128, out=A + 2 * G, ldo=128, stream=None,
-             parts=None if parts is None else (ctypes.c_int32 * len(parts))(*parts))
-    for k in kw:
-        assert k in d, k
-    return L.rope_cos_sin(*({**d, **kw}[n] for n in ROPE))
+def rope(L, parts=(), **kw):
+    d = dict(pos=A, pd=1, ldp=16, axes=1, mixed=0, freq=A + G, scaling=1.0, T=16, R=128, out=A + 2 * G, ldo=128)
+    d.update((f"s{i}", n) for i, n in enumerate((*parts, 0, 0, 0, 0)[:4]))
+    return call(L, "rope_cos_sin", Rope, d, kw)
 
 
 def test_rope_refusals(L):
-    assert rope(L) == CUDA and rope(L, parts=[64]) == CUDA
+    assert rope(L) == CUDA and rope(L, parts=[64]) == CUDA and rope(L, parts=[63]) == SHAPE
+    assert L.rope_cos_sin(None, None) == NULL
     assert rope(L, R=0) == SHAPE and rope(L, R=127) == SHAPE and rope(L, R=514, ldo=514) == SHAPE
-    assert rope(L, axes=0) == SHAPE and rope(L, axes=5) == SHAPE and rope(L, axes=3) == NULL
+    assert rope(L, axes=0) == SHAPE and rope(L, axes=5) == SHAPE and rope(L, axes=3) == SHAPE
     assert rope(L, axes=3, parts=[16, 24, 24]) == CUDA and rope(L, axes=3, parts=[16, 24, 23]) == SHAPE
     assert rope(L, axes=3, parts=[-8, 48, 24]) == SHAPE and rope(L, axes=3, parts=[0, 40, 24]) == CUDA
     assert rope(L, axes=3, parts=[24, 20, 20], mixed=1) == CUDA
