@@ -128,6 +128,14 @@ void set_strides(Stride (&d)[2], const Share &s, int H, int64_t ld, int64_t hs)
     for (int e = 0; e < 2; ++e) d[e] = {s.dt[e] * ld + s.dh[e] * hs, ld - H * hs};
 }
 
+bool split_sectors(int R, int D, const HeadView *v, int n)
+{
+    bool split = D % 16 || R / 2 % 16 || (D - R + 15) / 16 % 2;
+    for (int i = 0; i < n; ++i)
+        if (v[i].H > 0) split = split || v[i].ld % 16 || v[i].hs % 16 || (uintptr_t)v[i].p % 32;
+    return split;
+}
+
 cudaError_t launch_qk_fwd(QkParams p, bool norm, bool append, int vec, int sms, cudaStream_t s)
 {
     if (vec == 0) {
@@ -152,6 +160,7 @@ cudaError_t launch_qk_fwd(QkParams p, bool norm, bool append, int vec, int sms, 
         else set_strides(sh.out, sh, heads[i], p.out[i].ld, p.out[i].hs);
         blocks += sh.blocks;
     }
+    p.l1 = split_sectors(p.R, p.D, p.in, n);
     const dim3 grid((unsigned)blocks);
     if (vec < 8) return run_qk_narrow(p, norm, append, vec, grid, s);
     return append ? run_qk_append(p, norm, grid, s) : run_qk_fwd(p, norm, grid, s);

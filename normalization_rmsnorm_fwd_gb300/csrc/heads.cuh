@@ -242,9 +242,16 @@ struct LaneRows {
     }
 };
 
-// A piece of `count` elements into a slot of the ring.
-template <int V>
-__device__ __forceinline__ void copy_piece(uint4 *slot, const uint16_t *g, int count)
+// A piece of `count` elements into a slot of the ring.  Where a row's two
+// copies (its lanes' first and second pieces) meet inside a 32-byte sector the
+// copies go through L1, in which the second finds what the first fetched:
+// always in the general form (D = 80, R = 32 forward 47.5 -> 37.8 us, D = 32
+// 58.9 -> 54.5; D = 96, whose pieces are whole sectors, loses 1 %), never in
+// the wholly rotated forms, and as `l1` says in the partly rotated ones with
+// known lanes (D = 64, R = 16 65.0 -> 52.8 us; D = 128 and 256, R = 64 lose
+// 1 %).
+template <int N, bool WHOLE, int V>
+__device__ __forceinline__ void copy_piece(uint4 *slot, const uint16_t *g, int count, bool l1)
 {
 #pragma unroll
     for (int e = 0; e < 8; e += V) {
@@ -256,8 +263,10 @@ __device__ __forceinline__ void copy_piece(uint4 *slot, const uint16_t *g, int c
             continue;
         }
         const unsigned a = (unsigned)__cvta_generic_to_shared(to);
-        if constexpr (V == 8) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(a), "l"(g + e) : "memory");
-        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(a), "l"(g + e), "n"(2 * V) : "memory");
+        if (N == 0 || (!WHOLE && l1))
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(a), "l"(g + e), "n"(2 * V) : "memory");
+        else if constexpr (V == 8)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(a), "l"(g + e) : "memory");
     }
 }
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

@@ -63,6 +63,7 @@ struct QkParams {
     // launch
     int heads;                   // rows per token: Hq + Hk (+ Hk)
     int lanes;                   // lanes of a row
+    int l1;                      // copies of a partly rotated row through L1 (split_sectors)
     Share share[3];
 #ifdef CRMSN_DEBUG
     DebugRanges dbg;
@@ -80,7 +81,7 @@ struct QkBwdParams {
     int T, D;
     float *dw[2];
     float *part;                 // [CTAs of q, then of k][D] partial dw rows
-    int lanes;
+    int lanes, l1;
     Share share[2];
 #ifdef CRMSN_DEBUG
     DebugRanges dbg;
@@ -116,6 +117,9 @@ constexpr int kQkBwdCtasPerSm = 4;
 void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_per_step, int warps, int ctas,
           bool runs);
 void set_strides(Stride (&d)[2], const Share &s, int H, int64_t ld, int64_t hs);
+
+// Whether a row's two pieces (heads.cuh) meet inside a 32-byte sector.
+bool split_sectors(int R, int D, const HeadView *v, int n);
 
 // norm: with weights; vec: elements of an access, 8, 4 or 2 (row_lanes() at
 // most 32), or 0: the element-wise form.

@@ -180,6 +180,7 @@ cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, int vec, int sms, cudaStream
         set_strides(sh.in2, sh, heads[i], p.x[i].ld, p.x[i].hs);
         set_strides(sh.out, sh, heads[i], p.dx[i].ld, p.dx[i].hs);
     }
+    p.l1 = split_sectors(p.R, p.D, p.g, 2) || (norm && split_sectors(p.R, p.D, p.x, 2));
     const dim3 grid((unsigned)(p.share[0].blocks + p.share[1].blocks));
     cudaError_t e = vec == 8 ? run_qk_bwd(p, norm, grid, s)
                   : vec > 0  ? run_qk_bwd_narrow(p, norm, vec, grid, s)

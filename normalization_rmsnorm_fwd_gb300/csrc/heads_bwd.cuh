@@ -88,11 +88,11 @@ __global__ void __launch_bounds__(kBwdThreads, kQkBwdCtasPerSm) k_qk_bwd(const Q
     int to_issue = mine.mine;
     auto issue = [&](int stage) {
         if (to_issue > 0) {
-            copy_piece<V>(&sm.ring[stage][0][tid], g.p, pc.ca);
-            copy_piece<V>(&sm.ring[stage][1][tid], g.p + delta, pc.cb);
+            copy_piece<N, WHOLE, V>(&sm.ring[stage][0][tid], g.p, pc.ca, p.l1);
+            copy_piece<N, WHOLE, V>(&sm.ring[stage][1][tid], g.p + delta, pc.cb, p.l1);
             if constexpr (NORM) {
-                copy_piece<V>(&sm.ring[stage][2][tid], x, pc.ca);
-                copy_piece<V>(&sm.ring[stage][3][tid], x + delta, pc.cb);
+                copy_piece<N, WHOLE, V>(&sm.ring[stage][2][tid], x, pc.ca, p.l1);
+                copy_piece<N, WHOLE, V>(&sm.ring[stage][3][tid], x + delta, pc.cb, p.l1);
             }
         }
         --to_issue;

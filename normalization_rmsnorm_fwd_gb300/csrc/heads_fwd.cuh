@@ -70,8 +70,8 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
     int to_issue = mine.mine;
     auto issue = [&](int stage) {
         if (to_issue > 0) {
-            copy_piece<V>(&ring[stage][0][tid], in.p, pc.ca);
-            copy_piece<V>(&ring[stage][1][tid], in.p + delta, pc.cb);
+            copy_piece<N, WHOLE, V>(&ring[stage][0][tid], in.p, pc.ca, p.l1);
+            copy_piece<N, WHOLE, V>(&ring[stage][1][tid], in.p + delta, pc.cb, p.l1);
         }
         --to_issue;
         const int e = stage % kRun == kRun - 1;
