@@ -92,18 +92,19 @@ __global__ void __launch_bounds__(kThreads) k_qk_fwd_any(const QkParams p, bool 
 
 }  // namespace
 
-void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_per_step, int warps, int ctas,
-          bool runs)
+void deal(Share *s, const int *heads, const int *cost, int n, int64_t T, int cs_rows, int rows_per_step, int warps,
+          int ctas, bool runs)
 {
     int64_t all = 0, left = ctas;
-    for (int i = 0; i < n; ++i) all += heads[i];
+    for (int i = 0; i < n; ++i) all += (int64_t)heads[i] * cost[i];
     for (int i = 0; i < n; ++i) {
         s[i] = Share{};
         if (heads[i] == 0) continue;
-        // Every CTA of the launch has the same number of rows, up to rounding.
-        int64_t share = all == heads[i] ? left : (left * heads[i] + all / 2) / all;
+        // Every CTA of the launch has the same work, up to rounding.
+        const int64_t part = (int64_t)heads[i] * cost[i];
+        int64_t share = all == part ? left : (left * part + all / 2) / all;
         if (share < 1) share = 1;
-        if (share > left - 2 && all != heads[i]) share = left - 2;      // at least one for each tensor to come
+        if (share > left - 2 && all != part) share = left - 2;      // at least one for each tensor to come
         s[i].rows = T * heads[i];
         const int64_t steps = (s[i].rows + rows_per_step - 1) / rows_per_step;
         const int64_t need = (steps + warps - 1) / warps;
@@ -119,7 +120,7 @@ void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_pe
             s[i].dh[e] = (int)(on[e] % heads[i]);
         }
         left -= share;
-        all -= heads[i];
+        all -= part;
     }
 }
 
@@ -140,18 +141,24 @@ cudaError_t launch_qk_fwd(QkParams p, bool norm, bool append, int vec, int sms, 
 {
     if (vec == 0) {
         const int64_t rows = (int64_t)p.T * p.heads;
-        const int64_t blocks = (rows + kWarps - 1) / kWarps, most = (int64_t)sms * 4 * kQkFwdCtasPerSm;
+        const int64_t blocks = (rows + kWarps - 1) / kWarps, most = (int64_t)sms * 24;
         return launch_pdl(k_qk_fwd_any, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, s, p, norm,
                           append);
     }
     p.lanes = row_lanes(p.R, p.D);
+    // What a row of q, k and v costs: a key's row also finds its page, a
+    // value's is only copied.  (With equal costs the CTAs of the keys end last:
+    // a prompt of 8192 tokens, 32 + 8 heads of 128, 36.4 -> 33.7 us; 32 + 4
+    // heads of 96, E4M3, T = 16000 53.5 -> 45.6.)
+    const int cost[3] = {4, append ? 5 : 4, 3};
     const int heads[3] = {p.in[0].H, p.in[1].H, p.in[2].H}, n = append ? 3 : 2;
     // Runs of two steps load a token's cosines and sines half as often, which
     // narrow heads need (D = 64, T = 16384, 16 + 16 heads: 24.4 -> 21.2 us;
     // D = 96: 40.2 -> 37.3); single steps keep the memory that all warps
     // touch at a time closest together, which is worth more from D = 128 on
     // (32 + 8 heads: 60.1 -> 55.4 us; D = 256: 57.3 -> 49.5).
-    deal(p.share, heads, n, p.T, p.cs_rows, 32 / p.lanes, kWarps, sms * kQkFwdCtasPerSm, p.lanes < 8);
+    deal(p.share, heads, cost, n, p.T, p.cs_rows, 32 / p.lanes, kWarps,
+         sms * qk_fwd_ctas_per_sm(append, norm, !own_code(vec, p.D)), p.lanes < 8);
     int blocks = 0;
     for (int i = 0; i < n; ++i) {
         Share &sh = p.share[i];

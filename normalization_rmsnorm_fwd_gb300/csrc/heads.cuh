@@ -160,7 +160,7 @@ __device__ __forceinline__ void ld_weight8(F2 (&f)[4], const void *w, int w32, f
 }
 
 // The lanes of a warp: n to a row; lanes past the last whole row are idle
-// (their group is >= rows).  N > 0: n is known, a power of two, and D = 16 N.
+// (their group is >= rows).  N > 0: n is known, and D = 16 N.
 template <int N>
 struct Lanes {
     int n, l, grp;   // lanes of a row; lane in its row, row in the step
@@ -175,7 +175,7 @@ struct Lanes {
     template <int K>
     __device__ __forceinline__ void sum(float (&v)[K]) const
     {
-        if constexpr (N > 0) {
+        if constexpr (N > 0 && (N & (N - 1)) == 0) {
 #pragma unroll
             for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
@@ -185,9 +185,11 @@ struct Lanes {
 #pragma unroll
                 for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
         } else {
-            for (int o = 1 << (31 - __clz(n)); o > 0; o >>= 1)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
+                    if (o >= n) continue;
                     const float w = __shfl_down_sync(0xffffffffu, v[k], o);
                     if (l + o < n) v[k] += w;
                 }

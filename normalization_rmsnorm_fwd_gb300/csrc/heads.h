@@ -106,16 +106,20 @@ struct RopeParams {
 };
 
 // CTAs per SM of the forward and the append: 128 threads of at most 80
-// registers, 16 KB of ring each.
-constexpr int kQkFwdCtasPerSm = 6;
+// registers, 16 KB of ring each.  The general code of an append with norms
+// spills in 80 and has 102 (D = 80, 32 + 4 heads, T = 16000 48.5 -> 40.0 us).
+constexpr int qk_fwd_ctas_per_sm(bool append, bool norm, bool general) { return append && norm && general ? 5 : 6; }
+// Head sizes with code of their own (16-byte form).
+inline bool own_code(int vec, int D) { return vec == 8 && (D == 64 || D == 128 || D == 192 || D == 256); }
 // Most CTAs per SM of the backward (its workspace holds one row for each).
 constexpr int kQkBwdCtasPerSm = 4;
 
 // Deals `ctas` CTAs of `warps` warps out to n tensors of heads[i] heads
-// (heads.cu): each gets its share of the rows, at least one CTA and no more
-// than its rows fill; runs: runs of kRun steps where there are enough.
-void deal(Share *s, const int *heads, int n, int64_t T, int cs_rows, int rows_per_step, int warps, int ctas,
-          bool runs);
+// (heads.cu) by their rows times the cost of a row: at least one CTA to each
+// and no more than its rows fill; runs: runs of kRun steps where there are
+// enough.
+void deal(Share *s, const int *heads, const int *cost, int n, int64_t T, int cs_rows, int rows_per_step, int warps,
+          int ctas, bool runs);
 void set_strides(Stride (&d)[2], const Share &s, int H, int64_t ld, int64_t hs);
 
 // Whether a row's two pieces (heads.cuh) meet inside a 32-byte sector.

@@ -168,11 +168,11 @@ __global__ void __launch_bounds__(kReduceThreads) k_qk_dw_reduce(const QkBwdPara
 cudaError_t launch_qk_bwd(QkBwdParams p, bool norm, int vec, int sms, cudaStream_t s)
 {
     p.lanes = row_lanes(p.R, p.D);
-    const int heads[2] = {p.g[0].H, p.g[1].H};
+    const int heads[2] = {p.g[0].H, p.g[1].H}, cost[2] = {1, 1};
     // Runs of two steps (heads.cu): better up to D = 128 here (32 + 8
     // heads, T = 16384: 87.9 -> 80.0 us; D = 64, 16 + 16: 41.5 -> 38.0), worse
     // for wider heads (16 + 2 of 256 beside a gate, T = 8192: 55.1 -> 60.0).
-    deal(p.share, heads, 2, p.T, p.cs_rows, vec > 0 ? 32 / p.lanes : 1, kBwdWarps, sms * kQkBwdCtasPerSm,
+    deal(p.share, heads, cost, 2, p.T, p.cs_rows, vec > 0 ? 32 / p.lanes : 1, kBwdWarps, sms * kQkBwdCtasPerSm,
          p.lanes <= 8);
     for (int i = 0; i < 2; ++i) {
         Share &sh = p.share[i];
@@ -196,6 +196,7 @@ cudaError_t run_qk_bwd(const QkBwdParams &p, bool norm, dim3 grid, cudaStream_t 
     if (p.D == 64) return whole ? go_bwd<4, true, 8>(p, norm, grid, s) : go_bwd<4, false, 8>(p, norm, grid, s);
     if (p.D == 128) return whole ? go_bwd<8, true, 8>(p, norm, grid, s) : go_bwd<8, false, 8>(p, norm, grid, s);
     if (p.D == 256) return whole ? go_bwd<16, true, 8>(p, norm, grid, s) : go_bwd<16, false, 8>(p, norm, grid, s);
+    if (p.D == 192) return whole ? go_bwd<12, true, 8>(p, norm, grid, s) : go_bwd<12, false, 8>(p, norm, grid, s);
     return go_bwd<0, false, 8>(p, norm, grid, s);
 }
 

@@ -183,7 +183,7 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
 }
 
 template <int N, bool WHOLE, int V, bool NORM, bool PAIRS, bool APPEND>
-__global__ void __launch_bounds__(kThreads, kQkFwdCtasPerSm) k_qk_fwd(const QkParams p)
+__global__ void __launch_bounds__(kThreads, qk_fwd_ctas_per_sm(APPEND, NORM, N == 0)) k_qk_fwd(const QkParams p)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -206,10 +206,11 @@ cudaError_t go(const QkParams &p, bool norm, dim3 grid, cudaStream_t s)
                    : launch_pdl(k_qk_fwd<N, WHOLE, V, false, false, APPEND>, grid, b, sizeof(Ring), s, p);
 }
 
-// The 16-byte form: head sizes 64, 128 and 256 have code of their own, with
-// the lanes of a row (and, if all of it is rotated, the distance of its two
-// pieces) known.  Measured with the general code: D = 128 (32 + 8 heads, T =
-// 16384) 60.8 -> 56.2 us.
+// The 16-byte form: head sizes 64, 128, 192 and 256 have code of their own,
+// with the lanes of a row (and, if all of it is rotated, the distance of its
+// two pieces) known.  Measured with the general code: D = 128 (32 + 8 heads,
+// T = 16384) 60.8 -> 56.2 us; an append of D = 192 (32 + 4 heads, T = 8797)
+// 71.4 -> 54.7, its backward 86.1 -> 81.7.  (D = 80 and 96: 3 %, not kept.)
 template <bool APPEND>
 cudaError_t go(const QkParams &p, bool norm, dim3 grid, cudaStream_t s)
 {
@@ -217,6 +218,7 @@ cudaError_t go(const QkParams &p, bool norm, dim3 grid, cudaStream_t s)
     if (p.D == 64) return whole ? go<4, true, 8, APPEND>(p, norm, grid, s) : go<4, false, 8, APPEND>(p, norm, grid, s);
     if (p.D == 128) return whole ? go<8, true, 8, APPEND>(p, norm, grid, s) : go<8, false, 8, APPEND>(p, norm, grid, s);
     if (p.D == 256) return whole ? go<16, true, 8, APPEND>(p, norm, grid, s) : go<16, false, 8, APPEND>(p, norm, grid, s);
+    if (p.D == 192) return whole ? go<12, true, 8, APPEND>(p, norm, grid, s) : go<12, false, 8, APPEND>(p, norm, grid, s);
     return go<0, false, 8, APPEND>(p, norm, grid, s);
 }
 
