@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope(const RopeParams p)
         axis[i] = column_axis(p, g * N + i);
         one = one && axis[i] == axis[0];
     }
+    one = __all_sync(0xffffffffu, one);              // a warp takes one of the loops below
     const uint32_t first = id / groups;
     if (first >= lanes || first >= p.T) return;
     // One loop for columns of one axis (one position a token), one for the
