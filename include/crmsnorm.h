@@ -448,8 +448,8 @@ typedef struct crmsn_qk_append_call {
  *   cos_sin[t, R/2 + j] = f32(scaling * sin(p * inv_freq[j]))
  *   p = positions[axis(j), t],  0 <= j < R/2
  *
- * positions: [n_axes, T] of I32 or I64 (pos_dtype) with axis stride ldp;
- * negative positions are valid.  inv_freq: FP32 [R/2] on the device;
+ * positions: [n_axes, T] of I32 or I64 (pos_dtype) with axis stride ldp (0:
+ * the same positions on every axis); negative positions are valid.  inv_freq: FP32 [R/2] on the device;
  * |inv_freq| < 2^40 (columns beyond that, infinite or NaN give NaN).  The
  * product p * inv_freq is reduced modulo 2 pi exactly (64-bit fractions of a
  * turn): the angle is off by less than 2^-61 |p|, whatever inv_freq is.

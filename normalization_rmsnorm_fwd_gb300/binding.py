@@ -537,8 +537,8 @@ def rope_cos_sin(positions, inv_freq, sections=None, interleaved_axes: bool = Fa
                  scaling: float = 1.0, out=None):
     """Cosines and sines of rotary positions, FP32 [..., R] (R/2 cosines, then
     R/2 sines) with R = 2 * inv_freq.numel(): positions is [...] (int32 or
-    int64), or [axes, ...] when `sections` (the columns of each axis) names
-    more than one axis.  One call serves every layer.  Returns out."""
+    int64), or [axes, ...] (possibly expanded) when `sections` (the columns of each
+    axis) names more than one axis.  One call serves every layer.  Returns out."""
     _need_cuda(positions, "positions")
     dev = positions.get_device()
     kind = _INDEX.get(positions.dtype)

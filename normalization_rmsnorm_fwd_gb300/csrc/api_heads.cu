@@ -333,7 +333,8 @@ crmsn_status rope_cos_sin(const crmsn_rope_call *call, cudaStream_t stream)
     if (T == 0) return CRMSN_OK;
     if (!positions || !inv_freq || !cos_sin) return CRMSN_ERR_NULL;
     const int es = pos_dtype == CRMSN_I64 ? 8 : 4;
-    if ((n_axes > 1 && (ldp < T || ldp > kMaxStride)) ||
+    // Axis stride 0: the same positions on every axis.
+    if ((n_axes > 1 && ldp != 0 && (ldp < T || ldp > kMaxStride)) ||
         (T > 1 && (ldcs < R || ldcs > kMaxStride || ldcs > ((int64_t)1 << 60) / T)))
         return CRMSN_ERR_SHAPE;
     if (!al(positions, es) || !al(inv_freq, 4) || !al(cos_sin, 4)) return CRMSN_ERR_ALIGNMENT;

@@ -220,6 +220,15 @@ def test_angles_layouts_and_empty():
     assert crm.rope_cos_sin(torch.zeros(0, dtype=torch.int64, device=DEV), f).shape == (0, 32)
 
 
+@pytest.mark.parametrize("mixed", [False, True])
+def test_angles_of_text_alone_are_those_of_one_axis(mixed):
+    # One position per token, expanded over the axes, in both column orders.
+    f = torch.rand(32, device=DEV)
+    pos = torch.randint(1 << 20, (4, 25), device=DEV)
+    one = crm.rope_cos_sin(pos, f)
+    assert torch.equal(crm.rope_cos_sin(pos.expand(3, 4, 25), f, [12, 10, 10], mixed), one)
+
+
 def test_rows_do_not_depend_on_their_call():
     # A token's outputs are the same bits alone, in a larger batch, with other
     # heads, and in the appended form.

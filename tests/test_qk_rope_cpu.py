@@ -285,6 +285,11 @@ def test_cpu_tensors_are_refused():
         crm.rope_cos_sin(torch.arange(4), torch.ones(32))
 
 
+def test_rope_takes_the_same_positions_on_every_axis(L):
+    assert rope(L, axes=3, parts=[16, 24, 24], ldp=0) == CUDA
+    assert rope(L, axes=3, parts=[16, 24, 24], ldp=-16) == SHAPE and rope(L, axes=3, parts=[16, 24, 24], ldp=1) == SHAPE
+
+
 def test_calls_run_on_their_tensors_device(monkeypatch):
     # The C call is made with the tensors' device current and on that
     # device's current stream, whichever device is current outside.
