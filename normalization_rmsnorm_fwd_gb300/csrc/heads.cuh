@@ -159,6 +159,17 @@ __device__ __forceinline__ void ld_weight8(F2 (&f)[4], const void *w, int w32, f
     for (int j = 0; j < 4; ++j) f[j] = f2_add(f[j], f2(bias));
 }
 
+// The end of the kernels before: from here on their results may be read and
+// their inputs overwritten.  What needs the arguments alone (a warp's first
+// row, its count of rows: divisions) comes before it and overlaps with them:
+// one token's append 2.06 -> 1.70 us, its angles 1.94 -> 1.41, 1001 tokens of
+// 15 + 5 heads of 80 3.92 -> 3.28.
+__device__ __forceinline__ void grid_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // The lanes of a warp: n to a row; lanes past the last whole row are idle
 // (their group is >= rows).  N > 0: n is known, and D = 16 N.
 template <int N>

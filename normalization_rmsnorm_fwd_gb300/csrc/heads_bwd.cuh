@@ -67,8 +67,6 @@ __device__ __forceinline__ void fold4(float4 &hi, float4 &lo, F2 a, F2 b)
 template <int N, bool WHOLE, int V, bool NORM, bool PAIRS>
 __global__ void __launch_bounds__(kBwdThreads, kQkBwdCtasPerSm) k_qk_bwd(const QkBwdParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     CRMSN_DEBUG_ENTER(p.dbg);
     using Shared = typename std::conditional<NORM, BwdShared, BwdSharedPlain>::type;
     Shared &sm = *reinterpret_cast<Shared *>(heads_smem);
@@ -85,6 +83,7 @@ __global__ void __launch_bounds__(kBwdThreads, kQkBwdCtasPerSm) k_qk_bwd(const Q
     Walk<uint16_t> out = {const_cast<uint16_t *>(p.dx[which].p) + t * p.dx[which].ld + mine.h * p.dx[which].hs + pc.a,
                           mine.h};
     const uint16_t *x = NORM ? p.x[which].p + t * p.x[which].ld + mine.h * p.x[which].hs + pc.a : nullptr;
+    grid_wait();
     int to_issue = mine.mine;
     auto issue = [&](int stage) {
         if (to_issue > 0) {

@@ -64,9 +64,10 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
     const int H = p.in[which].H, tid = threadIdx.x, delta = pc.b - pc.a, P = p.cs_rows;
     const Share &sh = p.share[which];
     const LaneRows mine(sh, H, block * (kThreads / 32) + (tid >> 5), L.grp, L.rows());
-    if (mine.most == 0) return;
     int64_t t = mine.t;
     Walk<const uint16_t> in = {p.in[which].p + t * p.in[which].ld + mine.h * p.in[which].hs + pc.a, mine.h};
+    grid_wait();
+    if (mine.most == 0) return;
     int to_issue = mine.mine;
     auto issue = [&](int stage) {
         if (to_issue > 0) {
@@ -185,8 +186,6 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
 template <int N, bool WHOLE, int V, bool NORM, bool PAIRS, bool APPEND>
 __global__ void __launch_bounds__(kThreads, qk_fwd_ctas_per_sm(APPEND, NORM, N == 0)) k_qk_fwd(const QkParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     CRMSN_DEBUG_ENTER(p.dbg);
     Ring &ring = *reinterpret_cast<Ring *>(heads_smem);
     int block = blockIdx.x, which = 0;

@@ -113,9 +113,23 @@ __device__ __forceinline__ int column_axis(const RopeParams &p, int j)
 template <int N, bool POS64>
 __global__ void __launch_bounds__(kThreads, kPerSm) k_rope(const RopeParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     CRMSN_DEBUG_ENTER(p.dbg);
+    const uint32_t groups = (uint32_t)p.half / N, id = blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t lanes = gridDim.x * kThreads / groups;           // tokens in flight
+    const int g = (int)(id % groups);
+    int axis[N];
+    bool one = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        axis[i] = column_axis(p, g * N + i);
+        one = one && axis[i] == axis[0];
+    }
+    one = __all_sync(0xffffffffu, one);              // a warp takes one of the loops below
+    const uint32_t first = id / groups;
+    const bool any = first < lanes && first < p.T;
+    int64_t at = (int64_t)axis[0] * p.ldp + first;
+    grid_wait();
+    uint64_t pos = one && any ? (uint64_t)ld_index(p.pos, POS64, at) : 0;
     __shared__ uint64_t column_turn[CRMSN_MAX_HEAD_DIM / 2];
     __shared__ float column_scale[CRMSN_MAX_HEAD_DIM / 2];   // the scaling, or NaN
     static_assert(CRMSN_MAX_HEAD_DIM / 2 <= kThreads, "a thread for each column");
@@ -126,23 +140,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope(const RopeParams p)
         column_scale[threadIdx.x] = ok ? p.scaling : __int_as_float(0x7fffffff);
     }
     __syncthreads();
-    const uint32_t groups = (uint32_t)p.half / N, id = blockIdx.x * kThreads + threadIdx.x;
-    const uint32_t lanes = gridDim.x * kThreads / groups;           // tokens in flight
-    const int g = (int)(id % groups);
     uint64_t F[N];
-    int axis[N];
     float m[N];
-    bool one = true;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         F[i] = column_turn[g * N + i];
         m[i] = column_scale[g * N + i];
-        axis[i] = column_axis(p, g * N + i);
-        one = one && axis[i] == axis[0];
     }
-    one = __all_sync(0xffffffffu, one);              // a warp takes one of the loops below
-    const uint32_t first = id / groups;
-    if (first >= lanes || first >= p.T) return;
+    if (!any) return;
     // One loop for columns of one axis (one position a token), one for the
     // others.
     const int64_t by = (int64_t)lanes * p.ldo;
@@ -178,8 +183,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_rope(const RopeParams p)
     };
     if (one) {
         // The next token's position is asked for while this one's is used.
-        int64_t at = (int64_t)axis[0] * p.ldp + first;
-        uint64_t pos = (uint64_t)ld_index(p.pos, POS64, at);
         while (row < end) {
             uint64_t turn[N];
 #pragma unroll
