@@ -65,6 +65,25 @@ def _need_cuda(t: torch.Tensor, name: str):
         raise TypeError(f"{name} must be a CUDA tensor")
 
 
+def _collapsed(shape, st, name, what) -> tuple[int, int]:
+    """(count, stride) of the rows that leading dimensions collapse into.  A
+    dimension of size 1 has no say, whatever its stride; every other one must
+    step over all rows of those inside it."""
+    n, ld = 1, st[-1]
+    if 0 in shape:
+        return 0, ld
+    for size, step in zip(reversed(shape), reversed(st)):
+        if size == 1:
+            continue
+        if n == 1:
+            ld = step
+        elif step != ld * n:
+            raise ValueError(f"{name}: leading dimensions must be contiguous with one another "
+                             f"(stride(i) == stride(i+1) * size(i+1)) to collapse into {what}")
+        n *= size
+    return n, ld
+
+
 def as_rows(t: torch.Tensor, name: str = "x") -> tuple[int, int, int]:
     """(rows, H, row stride in elements) of a row-collapsible tensor."""
     shape = t.shape
@@ -418,11 +437,8 @@ def as_heads(t: torch.Tensor, name: str = "q") -> tuple[int, int, int, int, int]
         raise ValueError(f"{name}: D must be contiguous")
     if nd == 3:
         return shape[0], H, D, st[0], st[1]
-    for i in range(nd - 3):
-        if shape[i] > 1 and st[i] != st[i + 1] * shape[i + 1]:
-            raise ValueError(f"{name}: leading dimensions must be contiguous with one another "
-                             "(stride(i) == stride(i+1) * size(i+1)) to collapse into tokens")
-    return math.prod(shape[:-2]), H, D, st[-3], st[-2]
+    T, ld = _collapsed(shape[:-2], st[:-2], name, "tokens")
+    return T, H, D, ld, st[-2]
 
 
 _BF16 = torch.bfloat16

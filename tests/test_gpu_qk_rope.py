@@ -306,6 +306,35 @@ def test_batches_are_rows_of_tokens():
     assert all(torch.equal(a.view(b.shape), b) for a, b in zip(got, want))
 
 
+def test_dimensions_of_size_one():
+    # Single frames whose padding is cut off have no one token stride: direct
+    # calls refuse them, autograd copies them.
+    g = gen(21)
+    B, S, H, D = 2, 5, 3, 64
+    frames = torch.randn(B, 1, 8, H, D, generator=g).to(BF16).to(DEV)[:, :, :S]
+    x, gr = frames.contiguous(), torch.randn(B, 1, S, H, D, generator=g).to(BF16).to(DEV)
+    w, cs = weights(g, D, "bf16")[0], rotation(g, S, D)
+    cache, slots = torch.zeros(B * S, 1, H, D, dtype=BF16, device=DEV), torch.arange(B * S, device=DEV)
+    with pytest.raises(ValueError):
+        crm.qk_rmsnorm_rope_fwd(frames, None, w, None, cs)
+    with pytest.raises(ValueError):
+        crm.qk_rmsnorm_rope_fwd(x, None, w, None, cs, q_out=frames)
+    with pytest.raises(ValueError):
+        crm.qk_rmsnorm_rope_bwd(gr, None, frames, None, w, None, cs)
+    with pytest.raises(ValueError):
+        crm.qk_rmsnorm_rope_append(None, frames, x, None, w, cs, cache, cache.clone(), slots)
+    y, _ = crm.qk_rmsnorm_rope_fwd(x, None, w, None, cs)
+    dq, _, dw, _ = crm.qk_rmsnorm_rope_bwd(gr, None, x, None, w, None, cs)
+    leaf, weight = frames.detach().requires_grad_(), w.clone().requires_grad_()
+    z, _ = crm.qk_rmsnorm_rope(leaf, None, weight, None, cs)
+    a, b = torch.autograd.grad(z, (leaf, weight), gr)
+    assert torch.equal(z, y) and torch.equal(a, dq) and torch.equal(b, dw.to(BF16))
+    # One token of each sequence in [B, heads, 1, D] storage is read in place.
+    one = torch.randn(7, H, 1, D, generator=g).to(BF16).to(DEV).transpose(1, 2)
+    y, _ = crm.qk_rmsnorm_rope_fwd(one, None, w, None, cs[:1])
+    assert torch.equal(y, crm.qk_rmsnorm_rope_fwd(one.contiguous(), None, w, None, cs[:1])[0])
+
+
 def test_special_values_stay_in_their_rows():
     # Infinities, NaN, zeros and the largest values give what the formula
     # gives, in their own row only (their own pair only, without norms).

@@ -348,3 +348,28 @@ def test_reference_axes():
     assert qk_ref.axis_of(8, [2, 3, 3], False) == [0, 0, 1, 1, 1, 2, 2, 2]
     assert qk_ref.axis_of(8, [4, 2, 2], True) == [0, 1, 2, 0, 1, 2, 0, 0]
     assert qk_ref.axis_of(8, [0, 5, 3], False) == [1] * 5 + [2] * 3
+
+
+def test_heads_with_dimensions_of_size_one():
+    # A dimension of size 1 says nothing about its neighbours, whatever its
+    # own stride: single frames with cut-off padding have no one token stride.
+    z = torch.zeros
+    cut = z(2, 1, 8, 3, 16)[:, :, :5]
+    assert cut.stride(0) == cut.stride(1) * cut.size(1)                      # as if contiguous
+    for t in (cut, z(2, 1, 8, 3, 16)[:, :, 1:7], z(2, 1, 1, 8, 3, 16)[:, :, :, :5], z(4, 1, 2, 8, 3, 16)[:, :, :, :5]):
+        with pytest.raises(ValueError):
+            B.as_heads(t)
+        c = ag._readable_heads(t)
+        assert c is not t and c.is_contiguous() and torch.equal(c, t)
+    assert B.as_heads(z(2, 1, 5, 3, 16)) == (10, 3, 16, 48, 16)
+    assert B.as_heads(z(2, 5, 1, 3, 16)) == (10, 3, 16, 48, 16)
+    assert B.as_heads(z(2, 1, 5, 6, 16)[..., 3:, :]) == (10, 3, 16, 96, 16)
+    # One token of each sequence, heads before tokens; the first token of each.
+    one = z(4, 3, 1, 16).transpose(1, 2)
+    assert B.as_heads(one) == (4, 3, 16, 48, 16) and ag._readable_heads(one) is one
+    assert B.as_heads(z(4, 7, 3, 16)[:, :1]) == (4, 3, 16, 7 * 48, 16)
+    assert B.as_heads(z(1, 1, 3, 16)) == (1, 3, 16, 48, 16)
+    assert B.as_heads(z(0, 7, 3, 16)[:, :5])[:3] == (0, 3, 16)
+    assert B.as_heads(z(1, 5, 3, 16).expand(1, 5, 3, 16)) == (5, 3, 16, 48, 16)
+    with pytest.raises(ValueError):
+        B.as_heads(z(1, 5, 3, 16).expand(2, 5, 3, 16))                       # a repeated sequence
