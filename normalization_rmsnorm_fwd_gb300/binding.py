@@ -12,10 +12,11 @@ CUDA library; a failing status raises :class:`CrmsnError`.
 
 Row tensors are ``[..., H]`` with a contiguous feature dimension.  Leading
 dimensions collapse into rows when each is contiguous with the next in
-row-major order (``stride(i) == stride(i+1) * size(i+1)``), so a
-``[T, heads, H]`` slice of a wider ``[T, heads, W]`` buffer is read in place
-as ``T*heads`` rows of stride ``W`` ("cake_rmsnorm_det_train_forward"
-Parameters/x); any other layout raises ``ValueError``.
+row-major order (``stride(i) == stride(i+1) * size(i+1)``, dimensions of size 1
+aside), so a ``[T, heads, H]`` slice of a wider ``[T, heads, W]`` buffer is
+read in place as ``T*heads`` rows of stride ``W``
+("cake_rmsnorm_det_train_forward" Parameters/x); any other layout raises
+``ValueError``.
 """
 from __future__ import annotations
 
@@ -96,14 +97,8 @@ def as_rows(t: torch.Tensor, name: str = "x") -> tuple[int, int, int]:
         raise ValueError(f"{name}: the feature dimension must be contiguous")
     if nd == 1:
         return 1, H, H
-    for i in range(nd - 2):
-        if shape[i] > 1 and st[i] != st[i + 1] * shape[i + 1]:
-            raise ValueError(
-                f"{name}: leading dimensions must be contiguous with one another "
-                "(stride(i) == stride(i+1) * size(i+1)) to collapse into rows")
-    rows = shape[0] if nd == 2 else math.prod(shape[:-1])
-    ld = st[-2] if shape[-2] > 1 else max(H, st[-2])
-    return rows, H, ld
+    rows, ld = (shape[0], st[0]) if nd == 2 else _collapsed(shape[:-1], st[:-1], name, "rows")
+    return rows, H, ld if rows > 1 else max(H, ld)
 
 
 def _bf16(t, name):

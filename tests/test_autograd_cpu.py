@@ -28,3 +28,10 @@ def test_cpu_tensors_are_refused():
     w = torch.ones(64, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         crm.rmsnorm(x, w)
+
+
+def test_readable_with_dimensions_of_size_one():
+    cut = torch.zeros(2, 1, 8, 64, dtype=torch.bfloat16)[:, :, :5]
+    assert ag._readable(cut) is not cut and ag._readable(cut).is_contiguous()
+    first = torch.zeros(5, 3, 64, dtype=torch.bfloat16)[:, :1]
+    assert ag._readable(first) is first

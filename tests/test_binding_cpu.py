@@ -56,3 +56,20 @@ def test_operations_refuse_cpu_tensors():
         B.rmsnorm_bwd(x, x, w, torch.ones(4))
     with pytest.raises(TypeError):
         B.layernorm(x, w.float(), w.float())
+
+
+def test_dimensions_of_size_one():
+    # They say nothing about their neighbours, whatever their own stride.
+    for t in (torch.zeros(2, 1, 8, 64)[:, :, :5], torch.zeros(2, 1, 1, 8, 64)[..., 2:, :], torch.zeros(4, 1, 2, 8, 64)[:, :, :, :5]):
+        assert t.stride(0) == t.stride(1) * t.size(1)               # as if contiguous
+        with pytest.raises(ValueError):
+            rows(t)
+    assert rows(torch.zeros(2, 1, 5, 64)) == (10, 64, 64)
+    assert rows(torch.zeros(2, 1, 5, 256)[..., :64]) == (10, 64, 256)
+    assert rows(torch.zeros(2, 5, 1, 64)) == (10, 64, 64)
+    # The first row of each of five blocks; one row in the middle of a block.
+    assert rows(torch.zeros(5, 3, 64)[:, :1]) == (5, 64, 192)
+    assert rows(torch.zeros(3, 1, 4, 64).transpose(1, 2)) == (12, 64, 64)
+    assert rows(torch.zeros(1, 3, 64)[:, 1:2]) == (1, 64, 64)
+    assert rows(torch.zeros(1, 1, 256)[..., :64])[:2] == (1, 64)
+    assert rows(torch.zeros(0, 3, 64)[:, :2])[:2] == (0, 64)

@@ -53,6 +53,31 @@ def test_stride_pads_forward_and_backward(orc, pad, H):
     gu.check_bf16(gu.host_bits(dx), ref["dx_exact"], allowance=allow, what=f"dx pad {pad}")
 
 
+def test_dimensions_of_size_one():
+    # Blocks of rows behind a dimension of size 1, their padding cut off, have
+    # no one row stride: direct calls refuse them, autograd copies them.
+    H = 512
+    g = torch.Generator().manual_seed(31)
+    base = torch.randn(2, 1, 8, H, generator=g).to(torch.bfloat16).to(gu.DEV)
+    cut, w = base[:, :, :5], torch.ones(H, dtype=torch.bfloat16, device=gu.DEV)
+    x = cut.contiguous()
+    with pytest.raises(ValueError):
+        crm.rmsnorm_fwd(cut, w)
+    with pytest.raises(ValueError):
+        crm.rmsnorm_fwd(x, w, y=cut)
+    want, rstd, _ = crm.rmsnorm_fwd(x, w)
+    with pytest.raises(ValueError):
+        crm.rmsnorm_bwd(x, cut, w, rstd.reshape(-1))
+    assert torch.equal(crm.rmsnorm(cut, w), want)
+    cs = torch.zeros(2, 1, 8, 32, device=gu.DEV)[:, :, :5]
+    with pytest.raises(ValueError):
+        crm.rope_cos_sin(torch.zeros(2, 1, 5, dtype=torch.int64, device=gu.DEV), torch.rand(16, device=gu.DEV), out=cs)
+    # The first row of every block is read in place.
+    blocks = base[:, 0].view(4, 4, H)
+    y, _, _ = crm.rmsnorm_fwd(blocks[:, :1], w)
+    assert torch.equal(y, crm.rmsnorm_fwd(blocks[:, :1].contiguous(), w)[0])
+
+
 def test_persistent_forward_rows_do_not_depend_on_T():
     # The plain forward runs on a grid capped at the resident CTAs; a row's
     # outputs must not depend on how many rows the call has (or on the grid).
