@@ -513,7 +513,8 @@ size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device);
  * qk_rmsnorm_rope_fwd, and for the keys and values of token t
  *
  *   k_cache[slot] = the normed and rotated key,  v_cache[slot] = the value
- *   (BF16, or fp8(x * (1 / scale)), rounded to nearest even and saturating)
+ *   (BF16, or fp8(x * (1 / scale)), rounded to nearest even and saturating;
+ *   1 / scale is rounded to FP32, and FLT_MAX where it would be infinite)
  *
  * slot = slots[t] (I32 or I64): page slot / page_size, row slot % page_size.
  * A token whose slot is negative or >= num_pages * page_size (padding) writes

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) k_qk_fwd_any(const QkParams p, bool 
         if (norm) rstd = __frsqrt_rn(__fadd_rn(__fmul_rn(warp_sum(ss), p.inv_d), p.eps));
         const float *cs = p.cs + (int64_t)(t % p.cs_rows) * p.ldcs;
         float inv = 1.f;
-        if (append && which > 0 && p.kind != CRMSN_CACHE_BF16) inv = __frcp_rn(ld_f32_ro(p.scale[which - 1]));
+        if (append && which > 0 && p.kind != CRMSN_CACHE_BF16) inv = scale_reciprocal(p.scale[which - 1]);
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             const int u = lane + 32 * k;

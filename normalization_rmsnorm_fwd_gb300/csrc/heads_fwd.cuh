@@ -9,6 +9,8 @@
 // are large: 180 instructions for a step of 1 KB in and 1 KB out.
 #pragma once
 
+#include <cfloat>
+
 #include "heads.cuh"
 
 namespace crmsn {
@@ -23,6 +25,15 @@ __device__ __forceinline__ int64_t cache_row(const QkParams &p, const CacheView 
     if (s < 0 || s >= p.num_slots) return -1;                // num_slots < 2^31
     const uint32_t page = (uint32_t)s / (uint32_t)p.page_size, row = (uint32_t)s - page * (uint32_t)p.page_size;
     return (int64_t)page * c.ps + (int64_t)row * c.ss;
+}
+
+// What the values of an FP8 cache are multiplied by: RN(1 / scale), at most
+// the largest FP32 value (infinite, from a scale up to 2^-128, it would turn
+// zeros into NaN).
+__device__ __forceinline__ float scale_reciprocal(const float *scale)
+{
+    const float inv = __frcp_rn(ld_f32_ro(scale));
+    return inv > FLT_MAX ? FLT_MAX : inv;
 }
 
 // A piece of `count` values to a cache of BF16 or, divided by the scale, FP8.
@@ -93,7 +104,7 @@ __device__ __forceinline__ void walk_rows(const QkParams &p, int which, int bloc
     // Where the rows go: a heads tensor, or a head's place in a cache row.
     const bool fp8 = ROLE != TO_HEADS && p.kind != CRMSN_CACHE_BF16;
     float inv = 1.f;
-    if (fp8) inv = __frcp_rn(ld_f32_ro(p.scale[which - 1]));
+    if (fp8) inv = scale_reciprocal(p.scale[which - 1]);
     Walk<uint16_t> out = {nullptr, mine.h};
     int64_t head = 0, base = 0;
     if constexpr (ROLE == TO_HEADS)

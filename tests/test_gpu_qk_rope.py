@@ -448,6 +448,32 @@ def test_append_saturates(dtype):
         assert (c[0] == top).all() and (c[1, 0] == top).all() and (c[1, 1] == -top).all() and c[2].isnan().all() and (c[3] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [E4M3, E5M2])
+@pytest.mark.parametrize("scale", [2.0 ** -149, 3 * 2.0 ** -140, 2.0 ** -129, 2.0 ** -128, 2.0 ** -126 - 2.0 ** -149, 2.0 ** -126, 1e-30, 1e30])
+@pytest.mark.parametrize("D,layout", [(64, "plain"), (100, "plain"), (64, "off4"), (64, "odd")])
+def test_append_scales_of_any_size(D, layout, scale, dtype):
+    # Values that are zero, subnormal, next to the scale, and large.  The
+    # reciprocal of a scale up to 2^-128 is taken as the largest FP32 value.
+    g = gen(22)
+    T, H = 6, 2
+    v, vc = heads(g, T, H, D, layout)
+    vc[0], vc[1] = 0.0, vc[1] * 2.0 ** -127
+    vc[2] = (vc[2].double() * 16 * scale).to(BF16)
+    vc[3] = (vc[3].double() * 300 * scale).to(BF16)
+    vc[4, 0, 0], vc[4, 0, 1], vc[4, 0, 2], vc[4, 1] = 2.0 ** -133, -0.0, 3e38, vc[4, 1] * 2.0 ** 100
+    v.copy_(vc)
+    kc, vcache = (torch.zeros(T, 1, H, D, device=DEV).to(dtype) for _ in range(2))
+    s = torch.tensor([scale], dtype=torch.float32)
+    assert float(s) == pytest.approx(scale, rel=2.0 ** -24)
+    crm.qk_rmsnorm_rope_append(None, v.clone() if layout == "plain" else heads(g, T, H, D, layout)[0].copy_(vc), v, None, None, None,
+                               kc, vcache, torch.arange(T, device=DEV), k_scale=s.to(DEV), v_scale=s.to(DEV))
+    zero = torch.zeros(1, dtype=torch.float64)
+    for c in (kc, vcache):
+        got = c.view(torch.uint8)[:, 0].contiguous().view(dtype)
+        qk_ref.check(got, vc.double(), zero, scale=max(float(s), 1 / torch.finfo(torch.float32).max))
+        assert (got.cpu().float()[0] == 0).all()
+
+
 def test_append_far_slots():
     # A cache of more than 2^32 elements: the last pages' offsets pass 32 bits.
     g = gen(9)
