@@ -56,13 +56,16 @@ __device__ __forceinline__ uint64_t turn_fraction(float f)
 }
 
 // The nearest quarter turn q of a fraction u of a turn, and the signed rest in
-// half turns, |x| <= 1/4, as an FP32 value (each half of the integer rounds
-// once: exact to 2^-24 of itself however small it is).
+// half turns, |x| <= 1/4, as an FP32 value.  u is taken as hi 2^32 + lo with
+// the nearest hi and a signed lo; each part and their sum round once: within
+// 2^-22 of the rest however small it is, and opposite for -u.  (An unsigned lo
+// lost the digits of a small negative rest; the carry costs 1 %: 131072 tokens
+// on three axes 12.8 -> 13.0 us.  Adding it in the product instead: 13.3.)
 __device__ __forceinline__ float quarter(uint64_t u, uint32_t &q)
 {
-    const uint32_t hi = (uint32_t)(u >> 32);
+    const uint32_t hi = (uint32_t)((u + 0x80000000u) >> 32);
     q = (hi + 0x20000000u) >> 30;
-    return __fmaf_rn(__int2float_rn((int)(hi - (q << 30))), 0x1p-31f, __fmul_rn(__uint2float_rn((uint32_t)u), 0x1p-63f));
+    return __fmaf_rn(__int2float_rn((int)(hi - (q << 30))), 0x1p-31f, __fmul_rn(__int2float_rn((int)(uint32_t)u), 0x1p-63f));
 }
 
 // sin(pi x) and cos(pi x) for two |x| <= 1/4: x pi + x z Q(z) and

@@ -203,6 +203,27 @@ def test_angles_far_positions_and_odd_frequencies():
     assert out.isnan().tolist() == [[True, True, True, False] * 2]
 
 
+def test_angles_of_opposite_positions():
+    # cos(-a) = cos(a) and sin(-a) = -sin(a) to the bit, far and near.
+    g = gen(23)
+    f = torch.cat([torch.rand(24, generator=g), 10.0 ** -torch.arange(40)]).to(DEV)
+    pos = torch.cat([torch.arange(500), torch.randint(1 << 31, (500,), generator=g)]).to(DEV)
+    a, b = crm.rope_cos_sin(pos, f), crm.rope_cos_sin(-pos, f)
+    assert torch.equal(a[:, :64], b[:, :64]) and torch.equal(a[:, 64:], -b[:, 64:])
+
+
+def test_angles_next_to_a_whole_turn():
+    # Small angles of either sign keep the angle's bound, 2^-61 |p|, and the
+    # sine's few roundings of itself: the rest of a turn within 2^-22 of
+    # itself (two halves and their sum round), the polynomial's steps 2^-22.
+    pos = torch.tensor([1, -1, 2, -2, 3, -3, 1000, -1000, 12345, -12345])
+    f = torch.tensor([1e-9, 3e-10, 1e-10, 3e-11, 1e-11, 1e-12, 1e-14, 1e-16, 1e-18, 2.0 ** -62], dtype=torch.float32)
+    out = crm.rope_cos_sin(pos.to(DEV), f.to(DEV)).cpu().double()
+    exact = (pos.double()[:, None] * f.double()).sin()
+    assert ((out[:, 10:] - exact).abs() <= 2.0 ** -61 * pos.double().abs()[:, None] + 2.0 ** -21 * exact.abs()).all()
+    assert (out[:, :10] == 1).all()
+
+
 def test_angles_layouts_and_empty():
     f = torch.rand(16, device=DEV)
     pos = torch.randint(9999, (3, 4, 5), device=DEV)
