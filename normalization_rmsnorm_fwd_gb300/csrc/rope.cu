@@ -214,8 +214,8 @@ cudaError_t launch_rope(const RopeParams &p, bool vec, int sms, cudaStream_t s)
 {
     const int64_t groups = vec ? p.half / 4 : p.half;
     const int64_t want = (p.T * groups + kThreads - 1) / kThreads;
-    int64_t most = (int64_t)sms * kPerSm;
-    if (most * kThreads < groups) most = (groups + kThreads - 1) / kThreads;   // a token in flight at least
+    static_assert(CRMSN_MAX_HEAD_DIM / 2 <= kThreads * kPerSm, "a token in flight at least");
+    const int64_t most = (int64_t)sms * kPerSm;
     const dim3 grid((unsigned)(want < most ? want : most));
     const dim3 b(kThreads);
     if (vec) return p.pos64 ? launch_pdl(k_rope<4, true>, grid, b, 0, s, p) : launch_pdl(k_rope<4, false>, grid, b, 0, s, p);
