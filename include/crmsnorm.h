@@ -495,8 +495,9 @@ crmsn_status qk_rmsnorm_rope_fwd(const crmsn_qk_fwd_call *call, cudaStream_t str
  *   dw[j] = sum over the tensor's rows of u * xhat       (FP32, overwritten)
  *
  * Without weights dx = bf16(u); q, k, dwq, dwk and the workspace may then be
- * NULL.  dw is added in a fixed order that depends on the sizes and the SM
- * count alone (no atomics).  In place: dq == gq, dk == gk are allowed.
+ * NULL.  dw is added in a fixed order that depends on the sizes, the access
+ * width (the alignment rule above: strides and bases) and the SM count alone
+ * (no atomics).  In place: dq == gq, dk == gk are allowed.
  * workspace: at least qk_rmsnorm_rope_bwd_workspace_bytes(D, device) bytes,
  * 256-byte aligned, any content; scratch that a later call on the same
  * stream may use again (two calls that may run at the same time need two).

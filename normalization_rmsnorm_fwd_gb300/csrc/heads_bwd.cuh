@@ -8,8 +8,8 @@
 // keeps nothing but its inputs.  dw: every warp adds its rows in registers in
 // a fixed order, the CTA's warps are added in order into one partial row per
 // CTA, and a second kernel adds the partial rows in a fixed order: the bits
-// depend on the sizes and the number of SMs alone.  Each CTA works on q or on
-// k, so that a lane keeps one weight and one set of sums.
+// depend on the sizes, the access width and the number of SMs alone.  Each CTA
+// works on q or on k, so that a lane keeps one weight and one set of sums.
 #pragma once
 
 #include <type_traits>

@@ -151,6 +151,27 @@ def test_backward(T, Hq, Hk, D, R, pairs, weight, layout, P):
         assert (a is None and b is None) or torch.equal(a, b)
 
 
+def test_weight_gradients_depend_on_sizes_and_access_width_alone():
+    # dw's bits: the same for any strides and bases of one access width; other
+    # widths add in another order, within the bound.
+    g = gen(24)
+    T, Hq, Hk, D = 3000, 6, 2, 128
+    (q, qc), (k, _), (gq, gc), (gk, _) = (heads(g, T, h, D) for h in (Hq, Hk, Hq, Hk))
+    wq, wk, _ = weights(g, D, "bf16")
+    cs = rotation(g, T, D)
+    want = crm.qk_rmsnorm_rope_bwd(gq, gk, q, k, wq, wk, cs)
+    for layout in ("gated", "packed", "heads"):
+        a, b, c, d = (heads(g, T, t.shape[1], D, layout)[0].copy_(t) for t in (gq, gk, q, k))
+        got = crm.qk_rmsnorm_rope_bwd(a, b, c, d, wq, wk, cs)
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), layout
+    _, _, rdw, bdw = qk_ref.backward(gc, qc, cpu(wq), cpu(cs))
+    for layout in ("off8", "off4", "odd"):
+        a = heads(g, T, Hq, D, layout)[0].copy_(gq)
+        got = crm.qk_rmsnorm_rope_bwd(a, None, q, None, wq, None, cs)
+        qk_ref.check(got[2], rdw, bdw, what=layout)
+        assert torch.equal(crm.qk_rmsnorm_rope_bwd(a, None, q, None, wq, None, cs)[2], got[2])
+
+
 @pytest.mark.parametrize("kind", [torch.int32, torch.int64])
 @pytest.mark.parametrize("T,R,sections,mixed", [(1, 128, None, False), (77, 2, None, False), (5, 126, None, False), (1000, 64, [32], False),
                                                 (63, 128, [16, 24, 24], False), (63, 80, [0, 17, 23], False), (40, 128, [22, 21, 21], True),
