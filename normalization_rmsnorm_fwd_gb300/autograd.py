@@ -89,7 +89,8 @@ def rmsnorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual=None,
 # its leaves.  A leaf's gradient is accumulated on the stream on which its
 # first living graph was recorded; a captured backward pass that has to wait
 # for another stream than its own ends the process, so such a capture is
-# refused while it is still an ordinary call.
+# refused while it is still an ordinary call: at its forward, which cannot know
+# whether a backward will follow.
 _eager = weakref.WeakSet()
 _eager_lock = threading.Lock()
 
@@ -107,7 +108,8 @@ def _note_graph(ctx, inputs):
         held = [r() for c in _eager if c.graph_stream != stream for r in c.graph_leaves]
     if any(h is t for h in held for t in leaves):
         raise RuntimeError("qk_rmsnorm_rope: a graph recorded outside this capture, on another stream, still holds "
-                           "one of these leaves; drop it (its outputs and losses) before capturing")
+                           "one of these leaves; drop it (its outputs and losses) before capturing, or capture a forward "
+                           "alone under torch.no_grad()")
 
 
 def _readable_heads(t: torch.Tensor) -> torch.Tensor:
@@ -162,8 +164,16 @@ def qk_rmsnorm_rope(q: torch.Tensor, k, wq, wk, cos_sin, eps: float = 1e-6, weig
                     interleaved: bool = False):
     """Autograd-enabled per-head RMSNorm and rotation of q [..., Hq, D] and k
     [..., Hk, D] (arguments as qk_rmsnorm_rope_fwd): (q_out, k_out).  cos_sin
-    (rope_cos_sin) takes no gradient.  To capture a training step, record the
-    forward and the backward in one graph and let no eager graph of the same
-    leaves live from another stream (refused with RuntimeError)."""
+    (rope_cos_sin) takes no gradient.  The gradients of all other inputs are
+    worked out together, whichever are asked for.  Heads that no one token
+    stride describes ([B, heads, S, D] storage with B > 1, gradients among
+    them) are copied to a contiguous tensor once.
+
+    To capture a training step, record the forward and the backward in one
+    graph and let no eager graph of the same leaves live from another stream.
+    One of this function's is seen, and the captured forward refused with
+    RuntimeError while gradients are being recorded, with or without a
+    backward to come (capture a forward alone under torch.no_grad()); graphs
+    in which other operators hold the leaves are not seen."""
     return QKRMSNormRopeFunction.apply(q, k, wq, wk, cos_sin, eps, weight_bias, interleaved,
                                        torch.is_grad_enabled())
