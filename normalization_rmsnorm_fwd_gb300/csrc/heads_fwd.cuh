@@ -220,7 +220,8 @@ cudaError_t go(const QkParams &p, bool norm, dim3 grid, cudaStream_t s)
 // with the lanes of a row (and, if all of it is rotated, the distance of its
 // two pieces) known.  Measured with the general code: D = 128 (32 + 8 heads,
 // T = 16384) 60.8 -> 56.2 us; an append of D = 192 (32 + 4 heads, T = 8797)
-// 71.4 -> 54.7, its backward 86.1 -> 81.7.  (D = 80 and 96: 3 %, not kept.)
+// 71.4 -> 54.7 (50.2 with its CTAs dealt by cost), its backward 86.1 -> 81.7.
+// (D = 80 and 96: 3 %, not kept.)
 template <bool APPEND>
 cudaError_t go(const QkParams &p, bool norm, dim3 grid, cudaStream_t s)
 {

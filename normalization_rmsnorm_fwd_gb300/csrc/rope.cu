@@ -13,8 +13,8 @@ namespace crmsn {
 
 namespace {
 
-// CTAs per SM.  Five (3, 6) instead: 131072 tokens of 128 13.2 (15.9, 14.4)
-// instead of 12.9 us, 16384 tokens 2.99 instead of 2.83; 1 to 2 % better only
+// CTAs per SM.  Five (3, 6) instead: 131072 tokens of 128 13.5 (16.0, 14.4)
+// instead of 13.0 us, 16384 tokens 3.00 instead of 2.83; 1 to 2 % better only
 // where columns of several axes meet in a thread.
 constexpr int kThreads = 256, kPerSm = 4;
 
