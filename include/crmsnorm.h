@@ -94,7 +94,8 @@ enum {
     CRMSN_OP_GATED_ADA_FP8 = 5,
     CRMSN_OP_SILU = 6,
     CRMSN_OP_LAYERNORM = 7,
-    CRMSN_OP_QK_ROPE = 8            /* the query / key functions: H is the head size */
+    CRMSN_OP_QK_ROPE = 8,           /* the query / key functions: H is the head size */
+    CRMSN_OP_ATTENTION = 16         /* the attention functions: H is the head size */
 };
 /* Index types (positions, cache slots). */
 enum { CRMSN_I32 = 0, CRMSN_I64 = 1 };
@@ -533,6 +534,92 @@ size_t qk_rmsnorm_rope_bwd_workspace_bytes(int64_t D, int device);
 crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream_t stream);
 
 /*
+ * ---- Attention ----
+ *
+ * prompt_attention -- sequences over their own keys; paged_attention -- new
+ * tokens over the cache that qk_rmsnorm_rope_append writes.  No counterpart on
+ * the pages: what stands behind the query / key functions above.
+ *
+ * Token i of a sequence with n tokens and m keys stands on position
+ * p = m - n + i (the tokens are the last of the keys; prompt_attention: m = n)
+ * and sees key j when
+ *     j < m,   causal: j <= p,   window > 0 (causal only): j > p - window.
+ * Query head h reads key head h / (Hq / Hk).  Per token and query head
+ *     s_j = scale * q . k_j,   M = max s_j,
+ *     out = bf16(sum_j exp(s_j - M) v_j / sum_j exp(s_j - M)),
+ *     lse = M + ln(sum_j exp(s_j - M))              (FP32, nullable)
+ * over the keys it sees; a row that sees none gets zeros and lse = -inf.  What
+ * a row does not see never reaches it, whatever is stored there.  Scores and
+ * sums are FP32; the weights exp(s_j - M) are rounded to BF16 (FP8 caches:
+ * FP16) before the product with the values.
+ *
+ *   - q, out: [T, Hq, D], k, v: [T, Hk, D] heads as above (strides, their
+ *     limits); Hq a multiple of Hk, at most 128 query heads to a key head.
+ *     lse: FP32 [T, Hq] contiguous.
+ *   - B sequences, at most 2^20: sequence b holds the tokens starts[b] ..
+ *     starts[b + 1] - 1 (I32 [B + 1] on the device, not decreasing, in [0, T]);
+ *     starts NULL: T / B tokens each.  Tokens of no sequence are neither read
+ *     nor written.
+ *   - window: 0: none.
+ *   - Any layout and D is accepted (D even, at most CRMSN_MAX_HEAD_DIM); the
+ *     fast forms want D a multiple of 8 and at most 256, every stride a
+ *     multiple of 8 elements (FP8 caches: 16) and every base 16-byte aligned.
+ *   - workspace: at least attention_workspace_bytes(D, device) bytes, 256-byte
+ *     aligned, any content; scratch that a later call on the same stream may
+ *     use again (two calls that may run at the same time need two).
+ *   - The outputs may not overlap any input.
+ *   - The order of the sums of a row depends on the lengths of all sequences
+ *     of the call and on the SM count, and on nothing else.
+ */
+typedef struct crmsn_attention {
+    int64_t T, D, Hq, Hk, B;
+    crmsn_heads q, out;
+    float *lse;
+    const int32_t *starts;
+    float scale;
+    int32_t causal;
+    int64_t window;
+    void *workspace;
+    uint64_t workspace_bytes;
+} crmsn_attention;
+
+typedef struct crmsn_prompt_attention_call {
+    crmsn_attention attention;
+    crmsn_heads k, v;
+} crmsn_prompt_attention_call;
+
+typedef struct crmsn_paged_attention_call {
+    crmsn_attention attention;
+    const void *k_cache;            /* [num_pages, page_size, Hk, D]: */
+    int64_t kps, kss, khs;          /* strides of a page, a slot, a head */
+    const void *v_cache;
+    int64_t vps, vss, vhs;
+    int64_t num_pages, page_size;
+    const int32_t *page_table;      /* [B, table_pages], row stride ld_table */
+    int64_t ld_table, table_pages;
+    const int32_t *lens;            /* [B]: keys of each sequence */
+    const float *k_scale, *v_scale; /* FP8 caches: device FP32 [1] */
+    int32_t cache_kind;             /* CRMSN_CACHE_* */
+    int32_t reserved;               /* 0 */
+} crmsn_paged_attention_call;
+
+/* Bytes of workspace for head size D on `device`; 0 for an invalid D or device. */
+size_t attention_workspace_bytes(int64_t D, int device);
+
+crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStream_t stream);
+
+/*
+ * Key j of sequence b lies in row j % page_size of page page_table[b][j /
+ * page_size]; the keys of the new tokens have been appended before the call.
+ * Entries behind a sequence's last key are not read.  A page number outside
+ * [0, num_pages) reads as keys and values of zeros; a length is taken as
+ * within [0, table_pages * page_size].  An FP8 element stands for its value
+ * times k_scale or v_scale.  num_pages * page_size and table_pages * page_size
+ * are below 2^31 - 2^20.
+ */
+crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_t stream);
+
+/*
  * crmsn_debug_status -- no counterpart on the pages: the bounds guard of the
  * debug build (compiled with -DCRMSN_DEBUG; build.py's debug option).  In
  * that build every global load and store of every kernel is checked against
@@ -552,7 +639,7 @@ crmsn_status crmsn_debug_status(uint64_t *violation);
 /*
  * rmsnorm_supports -- [API] supports_* helpers; [GUIDE] 6.1
  * is_cake_rmsnorm_train_supported.  CRMSN_OK when operation `op` (CRMSN_OP_*)
- * accepts hidden size H (CRMSN_OP_QK_ROPE: head size) with weight dtype w_dtype, else the status the call
+ * accepts hidden size H (CRMSN_OP_QK_ROPE, CRMSN_OP_ATTENTION: head size) with weight dtype w_dtype, else the status the call
  * would return for that H / dtype.
  */
 crmsn_status rmsnorm_supports(int64_t H, int w_dtype, int op);

@@ -10,12 +10,15 @@ from .binding import (  # noqa: F401
     ada_rms_norm_style,
     as_heads,
     as_rows,
+    attention_workspace_bytes,
     fused_add_rmsnorm_fp8_block_quant,
     fused_add_rmsnorm_quant,
     fused_rmsnorm_silu,
     gate_residual_ada_norm_fp8,
     layernorm,
     layernorm_quant,
+    paged_attention,
+    prompt_attention,
     qk_rmsnorm_rope_append,
     qk_rmsnorm_rope_bwd,
     qk_rmsnorm_rope_bwd_workspace_bytes,

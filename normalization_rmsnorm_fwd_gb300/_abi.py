@@ -40,10 +40,13 @@ SIGNATURES = {
     "qk_rmsnorm_rope_bwd": (_ST, [ctypes.c_char_p, _P]),
     "qk_rmsnorm_rope_bwd_workspace_bytes": (ctypes.c_size_t, [_I, _INT]),
     "qk_rmsnorm_rope_append": (_ST, [ctypes.c_char_p, _P]),
+    "prompt_attention": (_ST, [ctypes.c_char_p, _P]),
+    "paged_attention": (_ST, [ctypes.c_char_p, _P]),
+    "attention_workspace_bytes": (ctypes.c_size_t, [_I, _INT]),
     "crmsn_debug_status": (_ST, [ctypes.POINTER(ctypes.c_uint64)]),
 }
 
-# The call structs of the query / key functions, field by field (pointers as
+# The call structs of the query / key and attention functions, field by field (pointers as
 # integers, 0 for NULL): one packed buffer costs 0.6 us to hand over, the same
 # 40 values as single ctypes arguments 3.8.
 _LAYER = "qqqqPPiiffPqqq"        # crmsn_qk_layer
@@ -52,6 +55,9 @@ ROPE_CALL = struct.Struct("@PqiiiiiiifPqqPq")
 QK_FWD_CALL = struct.Struct("@" + _LAYER + 4 * _HEADS)
 QK_BWD_CALL = struct.Struct("@" + _LAYER + 6 * _HEADS + "PPPQ")
 QK_APPEND_CALL = struct.Struct("@" + _LAYER + 4 * _HEADS + "PqqqPqqqiiqqPPP")
+_ATTENTION = "qqqqq" + 2 * _HEADS + "PPfiqPQ"   # crmsn_attention
+PROMPT_ATTENTION_CALL = struct.Struct("@" + _ATTENTION + 2 * _HEADS)
+PAGED_ATTENTION_CALL = struct.Struct("@" + _ATTENTION + "PqqqPqqqqqPqqPPPii")
 
 STATUS = {
     0: "CRMSN_OK", 1: "CRMSN_ERR_NULL", 2: "CRMSN_ERR_SHAPE", 3: "CRMSN_ERR_UNSUPPORTED_H",
@@ -64,6 +70,7 @@ BF16, F32 = 0, 1
 E4M3, E5M2 = 0, 1
 OP_FWD, OP_BWD, OP_QUANT, OP_BLOCK_QUANT, OP_ADA_STYLE, OP_GATED_ADA_FP8, OP_SILU, OP_LAYERNORM = range(8)
 OP_QK_ROPE = 8
+OP_ATTENTION = 16
 I32, I64 = 0, 1
 CACHE_BF16, CACHE_E4M3, CACHE_E5M2 = 0, 1, 2
 OUT_BF16, OUT_E4M3 = 0, 1

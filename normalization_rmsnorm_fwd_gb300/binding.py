@@ -744,5 +744,125 @@ def qk_rmsnorm_rope_append(q, k, v, wq, wk, cos_sin, k_cache, v_cache, slots, ep
     return q_out
 
 
+# -------------------------------------------------------------- attention --
+
+def attention_workspace_bytes(D: int, device=None) -> int:
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    idx = dev.index if dev.index is not None else torch.cuda.current_device()
+    n = _lib().attention_workspace_bytes(int(D), idx)
+    if n == 0:
+        raise CrmsnError("attention_workspace_bytes", 3, "invalid head size or device")
+    return n
+
+
+_I32 = torch.int32
+
+
+def _int32_vector(t, name, n, dev):
+    if t.dtype is not _I32 or t.get_device() != dev:
+        raise TypeError(f"{name} must be int32 on cuda:{dev}, got {t.dtype} on {t.device}")
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor")
+    return t.data_ptr()
+
+
+def _attention(q, shape, T, Hq, D, Hk, B, dev, starts, scale, causal, window, out, lse, workspace):
+    """(out, the packed fields of crmsn_attention): what the two attention
+    functions share."""
+    qp = _head_tensor(q, "q", dev, shape)
+    if Hk < 1 or Hq % Hk:
+        raise ValueError(f"{Hq} query heads are no multiple of {Hk} key heads")
+    if out is None:
+        out, op = _new_heads(q, Hq, D)
+    else:
+        op = _head_tensor(out, "out", dev, shape)
+    lp = 0
+    if lse is not None:
+        if lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != shape[:-1] or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 {tuple(shape[:-1])} tensor on cuda:{dev}")
+        lp = lse.data_ptr()
+    if workspace is None:
+        wsn = _lib().attention_workspace_bytes(D, dev)
+        workspace = torch.empty(wsn, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    else:
+        wsn = workspace.numel() * workspace.element_size()
+    return out, workspace, (T, D, Hq, Hk, B, *qp, *op, lp, 0 if starts is None else _int32_vector(starts, "starts", B + 1, dev),
+                            D ** -0.5 if scale is None else scale, bool(causal), window, workspace.data_ptr(), wsn)
+
+
+def prompt_attention(q, k, v, starts=None, scale=None, causal: bool = True, window: int = 0, out=None, lse=None,
+                     workspace=None):
+    """Attention of every token of q [..., Hq, D] over the keys k and values v
+    [..., Hk, D] of its own sequence: causal, over the last `window` keys
+    (0: all), or over all of them.  Head h reads key head h // (Hq // Hk).
+    starts (int32 [B + 1], on the device): the first token of each packed
+    sequence, and the end of the last; None: [T, H, D] is one sequence, [B, S,
+    H, D] holds B.  scale: of the scores, D ** -0.5 by default.  lse (float32
+    [..., Hq]) receives the logarithms of the sums.  Forward only; a call in
+    which gradients would be recorded is refused.  Returns out."""
+    dev, shape, T, Hq, D = _first_head_tensor(q, "q")
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        raise RuntimeError("prompt_attention has no gradient: call it under torch.no_grad()")
+    kshape, Hk = _kv_shape(shape, k, "k")
+    kp, vp = _head_tensor(k, "k", dev, kshape), _head_tensor(v, "v", dev, kshape)
+    if starts is not None:
+        if starts.dim() != 1 or starts.numel() < 1:
+            raise ValueError("starts must be a contiguous [sequences + 1] tensor")
+        B = starts.shape[0] - 1
+    else:
+        B = 1 if len(shape) == 3 else math.prod(shape[:-3])
+    out, workspace, packed = _attention(q, shape, T, Hq, D, Hk, B, dev, starts, scale, causal, window, out, lse, workspace)
+    _enqueue("prompt_attention", dev, _abi.PROMPT_ATTENTION_CALL.pack(*packed, *kp, *vp))
+    return out
+
+
+def paged_attention(q, k_cache, v_cache, page_table, lens, starts=None, scale=None, causal: bool = True,
+                    window: int = 0, k_scale=None, v_scale=None, out=None, lse=None, workspace=None):
+    """Attention of new tokens q [..., Hq, D] over a paged cache (k_cache,
+    v_cache and their scales as qk_rmsnorm_rope_append fills them; the new
+    tokens' own keys among them).  Sequence b has lens[b] keys (int32), in the
+    pages page_table[b] (int32 [B, pages]; what lies behind its last key is not
+    read), and its new tokens are the last of them: starts (int32 [B + 1])
+    names the first of each sequence, None: the tokens are shared out evenly
+    (one each: a decode step).  The rest as in prompt_attention."""
+    dev, shape, T, Hq, D = _first_head_tensor(q, "q")
+    if torch.is_grad_enabled() and q.requires_grad:
+        raise RuntimeError("paged_attention has no gradient: call it under torch.no_grad()")
+    ck = _CACHE.get(k_cache.dtype)
+    if ck is None or v_cache.dtype is not k_cache.dtype or k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise TypeError(f"k_cache and v_cache must be bfloat16, float8_e4m3fn or float8_e5m2, both, on cuda:{dev}")
+    cshape = k_cache.shape
+    if len(cshape) != 4 or cshape != v_cache.shape or cshape[3] != D:
+        raise ValueError(f"k_cache and v_cache must be [pages, page_size, heads, {D}]")
+    kps, kss, khs, k1 = k_cache.stride()
+    vps, vss, vhs, v1 = v_cache.stride()
+    if D > 1 and (k1 != 1 or v1 != 1):
+        raise ValueError("k_cache and v_cache: D must be contiguous")
+    if lens.dim() != 1:
+        raise ValueError("lens must be a contiguous [sequences] tensor")
+    B = lens.shape[0]
+    lp = _int32_vector(lens, "lens", B, dev)
+    if starts is None and (T % B if B else T):
+        raise ValueError(f"{T} tokens cannot be shared out evenly over {B} sequences: give starts")
+    if page_table.dtype is not _I32 or page_table.get_device() != dev:
+        raise TypeError(f"page_table must be int32 on cuda:{dev}, got {page_table.dtype} on {page_table.device}")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, pages]")
+    ldt, t1 = page_table.stride()
+    if page_table.shape[1] > 1 and t1 != 1:
+        raise ValueError("page_table: a sequence's pages must be contiguous")
+    out, workspace, packed = _attention(q, shape, T, Hq, D, cshape[2], B, dev, starts, scale, causal, window, out, lse,
+                                        workspace)
+    fp8 = ck != _abi.CACHE_BF16
+    _enqueue("paged_attention", dev,
+             _abi.PAGED_ATTENTION_CALL.pack(*packed, k_cache.data_ptr(), kps, kss, khs, v_cache.data_ptr(), vps, vss, vhs,
+                                            cshape[0], cshape[1], page_table.data_ptr(), ldt, page_table.shape[1], lp,
+                                            _cache_scale(k_scale, "k_scale", fp8, dev),
+                                            _cache_scale(v_scale, "v_scale", fp8, dev), ck, 0))
+    return out
+
+
 def rmsnorm_supports(H: int, w_dtype: int = BF16, op: int = _abi.OP_FWD) -> int:
     return _lib().rmsnorm_supports(int(H), int(w_dtype), int(op))

@@ -373,6 +373,9 @@ crmsn_status rmsnorm_supports(int64_t H, int w_dtype, int op)
         case CRMSN_OP_LAYERNORM:
             if (w_dtype != CRMSN_F32) return CRMSN_ERR_DTYPE;
             return check_h(H);
+        case CRMSN_OP_ATTENTION:
+            if (w_dtype != CRMSN_BF16) return CRMSN_ERR_DTYPE;
+            [[fallthrough]];
         case CRMSN_OP_QK_ROPE:
             if (H < 1) return CRMSN_ERR_SHAPE;
             return (H > CRMSN_MAX_HEAD_DIM || (H & 1)) ? CRMSN_ERR_UNSUPPORTED_H : CRMSN_OK;

@@ -1,0 +1,61 @@
+// attn.h -- parameter block and launches of the attention kernels
+// (attn_*.cu), shared with the host ABI (api_attn.cu).
+#pragma once
+
+#include "heads.h"
+
+namespace crmsn {
+
+// Division of 0 <= x < 2^31 by a divisor known on the host: with
+// l = ceil(log2 d) and mul = floor(2^(31+l) / d) + 1, mul d exceeds 2^(31+l)
+// by at most 2^l, so x mul >> (31 + l) is the exact quotient.
+struct FastDiv {
+    uint32_t mul;
+    int shift, d;
+    FastDiv() = default;
+    explicit FastDiv(int d_) : mul(0), shift(31), d(d_)
+    {
+        while (((int64_t)1 << (shift - 31)) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << shift) / (uint64_t)d) + 1);
+    }
+    __host__ __device__ __forceinline__ int div(int x) const
+    {
+        return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
+    }
+};
+
+// Keys or values: a paged cache (strides of a page, a slot in it, a head), or
+// [T, Hk, D] with ss the token stride.
+struct KvView {
+    const uint8_t *p;
+    int64_t ps, ss, hs;          // elements
+};
+
+struct AttnParams {
+    HeadView q, out;
+    KvView kv[2];                // keys, values
+    int kind;                    // CRMSN_CACHE_* of the keys and values
+    const float *scale[2];       // FP8 caches: device scales of keys, values
+    const int *table;            // page numbers (NULL: keys are the sequence's own tokens)
+    int64_t ldt;
+    int num_pages;
+    FastDiv page;
+    int max_keys;                // table_pages * page_size
+    const int *lens;             // keys of each sequence (paged)
+    const int *starts;           // first token of each sequence, or NULL: n each
+    int n;
+    int T, B, D, Hk;
+    FastDiv group;               // query heads of a key head
+    int causal, window;          // window 0: none
+    float qk_scale;              // scale * log2(e)
+    float *lse;
+    uint8_t *ws;
+#ifdef CRMSN_DEBUG
+    DebugRanges dbg;
+#endif
+};
+
+// One warp for each row (attn_row.cu): any layout and head size.
+cudaError_t launch_attn_row(const AttnParams &p, int sms, cudaStream_t s);
+
+}  // namespace crmsn
