@@ -65,8 +65,17 @@ void set_common(AttnParams &p, const crmsn_attention &a)
     p.ws = static_cast<uint8_t *>(a.workspace);
 }
 
-crmsn_status launch(const AttnParams &p, int sms, cudaStream_t stream)
+// What the tiled kernels want: 16-byte accesses and a head that they hold.
+bool tiled(const crmsn_attention &a, int es)
 {
+    return a.D <= kAttnMaxDim && a.D % (16 / es) == 0 && heads_vec(heads(a.q, a.Hq), a.T, 8) &&
+           heads_vec(heads(a.out, a.Hq), a.T, 8);
+}
+
+crmsn_status launch(const AttnParams &p, bool fast, int sms, cudaStream_t stream)
+{
+    if (!fast) return launched(launch_attn_row(p, sms, stream));
+    if (!p.starts && (int64_t)p.n * p.group.d <= kDecodeRows) return launched(launch_attn_decode(p, sms, stream));
     return launched(launch_attn_row(p, sms, stream));
 }
 
@@ -80,7 +89,9 @@ size_t attention_workspace_bytes(int64_t D, int device)
     if (D < 2 || D > CRMSN_MAX_HEAD_DIM || (D & 1)) return 0;
     const int sms = sm_count(device);
     if (sms <= 0) return 0;
-    return 256;
+    const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
+    const int64_t parts = D <= kAttnMaxDim ? 2 * ctas * attn_part_floats(kDecodeRows, attn_padded((int)D)) : 0;
+    return (size_t)(kAttnParts + parts * (int64_t)sizeof(float) + 255) / 256 * 256;
 }
 
 crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStream_t stream)
@@ -106,7 +117,7 @@ crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStrea
     p.kv[1] = {static_cast<const uint8_t *>(v.p), 0, v.ld, v.hs};
     p.kind = CRMSN_CACHE_BF16;
     p.page = FastDiv(1);
-    return launch(p, sms, stream);
+    return launch(p, tiled(a, 2) && heads_vec(k, a.T, 8) && heads_vec(v, a.T, 8), sms, stream);
 }
 
 crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_t stream)
@@ -160,7 +171,9 @@ crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_
     p.page = FastDiv((int)S);
     p.max_keys = (int)(c.table_pages * S);
     p.lens = c.lens;
-    return launch(p, sms, stream);
+    const int v = 16 / es;
+    return launch(p, tiled(a, es) && (P == 0 || (cache_vec(c.k_cache, c.kps, c.kss, c.khs, es, P, S, a.Hk, v) &&
+                                                 cache_vec(c.v_cache, c.vps, c.vss, c.vhs, es, P, S, a.Hk, v))), sms, stream);
 }
 
 }  // extern "C"

@@ -100,7 +100,7 @@ __device__ __forceinline__ void st_out(uint16_t *p, float v)
 // are never read.  Running maximum M and sum L in FP32:
 //   M' = max(M, s_j),  L = L 2^(M-M') + 2^(s_j-M'),  o = o 2^(M-M') + 2^(s_j-M') v_j
 template <int KIND, int NE>
-__device__ __forceinline__ void attend_row(const AttnParams &p, int b, const Seq &s, int i, int hq, bool with_lse)
+__device__ __noinline__ void attend_row(const AttnParams &p, int b, const Seq &s, int i, int hq, bool with_lse)
 {
     const int lane = threadIdx.x & 31, h = p.group.div(hq);
     const int64_t t = s.first + i;
@@ -153,6 +153,189 @@ __device__ __forceinline__ void attend_row(const AttnParams &p, int b, const Seq
     }
     if (with_lse && p.lse && lane == 0)
         st_f32(p.lse + t * p.out.H + hq, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
+}
+
+// A row's result that is not finite although its sum is: a value that the row
+// does not see may have met its weight 0 in a matrix product (0 inf = NaN).
+// Such a row is worked out again key by key.
+__device__ __forceinline__ bool suspect(float o, float L)
+{
+    return !(fabsf(o) < INFINITY) && L > 0.f && L < INFINITY;
+}
+
+// ------------------------------------------------------------- work split --
+// All tiles (rows that share keys) of a call, each as many units as it has
+// blocks of keys, in one line; CTA c of C takes the units from U c / C to
+// U (c + 1) / C.  So every CTA has the same work whatever the lengths are, and
+// only the tiles at its two ends are shared with others.
+struct Work {
+    int64_t units;               // U
+    int ctas;                    // C
+    int64_t u0, u1;              // this CTA's
+    int b;                       // the sequence of u0,
+    int64_t rest;                // and u0 less the units of those before it
+};
+__device__ __forceinline__ int64_t first_unit(int64_t U, int C, int c) { return U * c / C; }
+// The CTA that takes unit u: the largest c with floor(U c / C) <= u.
+__device__ __forceinline__ int unit_owner(int64_t U, int C, int64_t u) { return (int)(((u + 1) * C - 1) / U); }
+
+struct WorkScratch {
+    int64_t sum[2][32], total[2];
+    int64_t rest;
+    int b;
+};
+
+// count(b, units, tiles): what sequence b has for each key head.  ctas(units,
+// tiles): how many CTAs share them.  All THREADS threads call this; sequences
+// are counted THREADS at a time, and found again by a scan.
+template <int THREADS, typename Count, typename Ctas>
+__device__ __forceinline__ Work share_work(int B, int Hk, WorkScratch &sm, Count count, Ctas ctas)
+{
+    constexpr int W = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t mine = 0, first = 0, tiles = 0;
+    for (int b = tid; b < B; b += THREADS) {
+        int64_t u, t;
+        count(b, u, t);
+        if (b == tid) first = u;
+        mine += u;
+        tiles += t;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    }
+    if (lane == 0) {
+        sm.sum[0][warp] = mine;
+        sm.sum[1][warp] = tiles;
+    }
+    __syncthreads();
+    Work w;
+    w.units = tiles = 0;
+    for (int i = 0; i < W; ++i) {
+        w.units += sm.sum[0][i];
+        tiles += sm.sum[1][i];
+    }
+    w.units *= Hk;
+    w.ctas = ctas(w.units, tiles * Hk);
+    const int c = (int)blockIdx.x;
+    w.u0 = first_unit(w.units, w.ctas, c);
+    w.u1 = first_unit(w.units, w.ctas, c + 1);
+    w.b = 0;
+    w.rest = 0;
+    if (c >= w.ctas) return w;   // the same for all threads
+    // The sequence of u0: the one in which the running sum passes u0 / Hk.
+    const int64_t want = w.u0 / Hk;
+    int64_t before = 0;
+    for (int base = 0; base < B; base += THREADS) {
+        const int b = base + tid;
+        int64_t u = 0, t;
+        if (base == 0) u = first;
+        else if (b < B) count(b, u, t);
+        int64_t incl = u;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        __syncthreads();
+        if (lane == 31) sm.sum[0][warp] = incl;
+        __syncthreads();
+        int64_t chunk = 0;
+        for (int i = 0; i < W; ++i) {
+            if (i < warp) incl += sm.sum[0][i];
+            chunk += sm.sum[0][i];
+        }
+        const int64_t lo = before + incl - u;
+        if (b < B && want >= lo && want < lo + u) {
+            sm.b = b;
+            sm.rest = w.u0 - lo * Hk;
+        }
+        before += chunk;
+        if (want < before) break;
+    }
+    __syncthreads();
+    w.b = sm.b;
+    w.rest = sm.rest;
+    return w;
+}
+
+// Where the parts of CTA c lie.
+__device__ __forceinline__ float *part_of(uint8_t *ws, int c, int which, int rows, int DP)
+{
+    return reinterpret_cast<float *>(ws + kAttnParts) + (int64_t)(2 * c + which) * rows * (2 + DP);
+}
+__device__ __forceinline__ void st_header(uint8_t *ws, int c, const AttnHeader &h)
+{
+    AttnHeader *at = reinterpret_cast<AttnHeader *>(ws) + c;
+    if (dbg_global(at, (int)sizeof(AttnHeader), true)) *at = h;
+}
+__device__ __forceinline__ void st_f32x4(float *p, float a, float b, float c, float d)
+{
+    if (dbg_global(p, 16, true)) *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void st_u32x2(uint16_t *p, uint32_t a, uint32_t b)
+{
+    if (dbg_global(p, 8, true)) *reinterpret_cast<uint2 *>(p) = make_uint2(a, b);
+}
+__device__ __forceinline__ void st_u32x4(uint16_t *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    if (dbg_global(p, 16, true)) *reinterpret_cast<uint4 *>(p) = make_uint4(a, b, c, d);
+}
+
+// ------------------------------------------------------------ shared memory --
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes to shared memory, zeros where `ok` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok)
+{
+    const int n = ok && dbg_global(src, 16, false, 3) ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two FP8 codes in the low half -> packed FP16 pair (exact).
+template <int KIND>
+__device__ __forceinline__ uint32_t f16_fp8(uint32_t codes)
+{
+    uint32_t r;
+    const uint16_t c = (uint16_t)codes;
+    if constexpr (KIND == KV_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+    else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(c));
+    return r;
+}
+// Two floats -> packed FP16 pair (lo in bits 0..15), round to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// FP8 caches: queries in FP16.  A row is scaled by 2^e so that its largest
+// element lies in [2^11, 2^12): the elements down to 2^-28 of it keep all
+// their bits, and smaller ones are off by at most 2^-25, 2^-36 of the largest.
+// A score is below 256 * 2^12 * 2^16 and cannot overflow.
+__device__ __forceinline__ int row_exponent(float amax)
+{
+    if (!(amax > 0.f) || !(amax < INFINITY)) return 0;
+    return 11 - (int)floorf(log2f(amax));
+}
+// x 2^e for |e| up to 160.
+__device__ __forceinline__ float scaled(float x, int e)
+{
+    const int a = e / 2, b = e - a;
+    return x * __int_as_float((127 + a) << 23) * __int_as_float((127 + b) << 23);
 }
 
 }  // namespace crmsn

@@ -55,6 +55,32 @@ struct AttnParams {
 #endif
 };
 
+// Head sizes that the fast forms hold: D rounded up to one of these.
+constexpr int kAttnMaxDim = 256;
+inline int attn_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
+
+// The workspace: a header for each CTA, then two parts for each CTA (the end
+// of the tile that it finds begun, the beginning of the one that it leaves).
+// A part of `rows` rows: their maxima and sums, then rows x DP sums of values.
+struct AttnHeader {
+    int64_t first, last, units;  // units of the tile, of all tiles
+    int ctas, tile;              // CTAs that share them; 1: begins inside this tile
+    int b, h, tok, ntok;         // sequence, key head, first token and tokens of the tile
+    int pad[4];
+};
+static_assert(sizeof(AttnHeader) == 64, "one header");
+constexpr int kAttnMaxCtas = 1024;
+constexpr int64_t kAttnParts = (int64_t)kAttnMaxCtas * (int64_t)sizeof(AttnHeader);
+inline int64_t attn_part_floats(int rows, int DP) { return (int64_t)rows * (2 + DP); }
+
+// Joins the parts of the tiles that several CTAs shared (attn_combine.cu).
+cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int ctas, cudaStream_t s);
+
+// At most 16 rows (tokens times heads of a group) of each sequence, the same
+// number of tokens for all (attn_decode.cu).
+constexpr int kDecodeRows = 16;
+cudaError_t launch_attn_decode(const AttnParams &p, int sms, cudaStream_t s);
+
 // One warp for each row (attn_row.cu): any layout and head size.
 cudaError_t launch_attn_row(const AttnParams &p, int sms, cudaStream_t s);
 

@@ -1,0 +1,505 @@
+// attn_decode.cu -- attention of few rows over many keys: the tokens of a
+// sequence times the query heads of a key head are at most 16 rows, one side
+// of a matrix instruction (mma.m16n8k16).
+//
+// What bounds it is the cache's way from memory: 2 D elements a key and head,
+// read once, for 64 operations an element at 16 rows.  So each warp is a
+// pipeline of its own: it copies its KB keys and their values asynchronously
+// into a ring of slots in shared memory, works through them with its own
+// running maximum, sum and values, and meets the CTA's other warps only at the
+// end of a tile (the keys of one sequence and head), whose parts are then
+// joined.  The ring runs on across the ends of tiles.  The keys are shared out
+// evenly over the CTAs (attn.cuh).
+//
+// Layouts.  Slots hold rows of DP elements with their 16-byte chunks permuted
+// (swz) so that the rows of a matrix fragment lie in different banks.  BF16:
+// ldmatrix for keys, its transposed form for values.  FP8: products in FP16,
+// which holds every code exactly.  A thread's four neighbouring bytes of a key
+// serve as the elements k, k+1, k+8, k+9 of its fragment; the queries are
+// loaded in the same order.  For the values, transposed 16-bit units bring two
+// neighbouring columns of two keys, which go to two products, of the even and
+// of the odd columns.
+#include "attn.cuh"
+
+namespace crmsn {
+namespace {
+
+template <int KIND, int DP>
+struct Shape {
+    static constexpr int ES = KIND == KV_BF16 ? 2 : 1;
+    static constexpr int W = DP > 128 ? 4 : 8;               // warps
+    static constexpr int KB = KIND == KV_BF16 && DP > 64 ? 16 : 32;   // keys of a slot
+    static constexpr int UNIT = W * KB;                      // keys of a unit
+    static constexpr int PITCH = DP * ES, CH = PITCH / 16;   // bytes and chunks of a row
+    static constexpr int SLOT = KB * PITCH;
+    static constexpr int JOIN = W * kDecodeRows * (DP * 4 + 8);   // parts of the warps
+    static constexpr int FIT = (227 * 1024 - 1536 - JOIN) / (W * SLOT);
+    static constexpr int NS = FIT < 12 ? FIT : 12;           // slots of a warp
+    static constexpr int SMEM = JOIN + W * NS * SLOT;
+    static_assert(NS >= 4, "two keys and two values in flight");
+};
+
+template <int CH>
+__device__ __forceinline__ int swz(int row, int chunk)
+{
+    return CH % 8 == 0 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+}
+
+// Column d of a row of the joined parts: groups of eight permuted, so that the
+// rows of a fragment lie in different banks.
+__device__ __forceinline__ int turn(int row, int d) { return d ^ ((row & 7) << 3); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <int KIND>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (KIND == KV_BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Units of sequence s: blocks [k0, k1) of UNIT keys, at least one.
+template <int UNIT>
+__device__ __forceinline__ void units_of(const AttnParams &p, const Seq &s, int &k0, int &k1)
+{
+    k0 = key_lo(p, s, 0) / UNIT;
+    k1 = max((s.m + UNIT - 1) / UNIT, k0 + 1);
+}
+
+// A place in the line of units.
+struct Cursor {
+    int b, h, k, k0, k1;
+    Seq s;
+};
+template <int UNIT>
+__device__ __forceinline__ void step(const AttnParams &p, Cursor &c)
+{
+    if (++c.k < c.k1) return;
+    if (++c.h == p.Hk) {
+        c.h = 0;
+        ++c.b;
+        if (c.b < p.B) {
+            c.s = sequence(p, c.b);
+            units_of<UNIT>(p, c.s, c.k0, c.k1);
+        }
+    }
+    c.k = c.k0;
+}
+
+template <int KIND, int DP>
+__global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(const __grid_constant__ AttnParams p)
+{
+    using S = Shape<KIND, DP>;
+    constexpr int W = S::W, KB = S::KB, NS = S::NS, CH = S::CH, UNIT = S::UNIT;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ WorkScratch scratch;
+    __shared__ uint32_t odd_rows;
+    float *const join_o = reinterpret_cast<float *>(smem);                        // [W][16][DP], permuted (turn)
+    float *const join_ml = join_o + W * kDecodeRows * DP;                 // [W][16][2]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint8_t *const ring = smem + S::JOIN + warp * NS * S::SLOT;
+    const uint32_t ring_at = smem_addr(ring);
+    CRMSN_DEBUG_ENTER(p.dbg);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    const Work work = share_work<W * 32>(
+        p.B, p.Hk, scratch,
+        [&](int b, int64_t &u, int64_t &t) {
+            int k0, k1;
+            units_of<UNIT>(p, sequence(p, b), k0, k1);
+            u = k1 - k0;
+            t = 1;
+        },
+        [&](int64_t units, int64_t) { return (int)min((int64_t)gridDim.x, units); });
+    if ((int)blockIdx.x >= work.ctas) {
+        if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
+        return;
+    }
+    const int G = p.group.d, R = p.n * G, items = (int)(work.u1 - work.u0);
+    Cursor at;                        // of the work
+    at.b = work.b;
+    at.s = sequence(p, at.b);
+    units_of<UNIT>(p, at.s, at.k0, at.k1);
+    at.h = (int)(work.rest / (at.k1 - at.k0));
+    at.k = at.k0 + (int)(work.rest - (int64_t)at.h * (at.k1 - at.k0));
+    int64_t tile_first = work.u0 - (at.k - at.k0);            // unit where the current tile begins
+    if (tid == 0) {
+        AttnHeader hd{};
+        hd.first = tile_first;
+        hd.last = tile_first + (at.k1 - at.k0);
+        hd.units = work.units;
+        hd.ctas = work.ctas;
+        hd.tile = at.k > at.k0;
+        hd.b = at.b;
+        hd.h = at.h;
+        hd.tok = at.s.first;
+        hd.ntok = p.n;
+        st_header(p.ws, blockIdx.x, hd);
+        odd_rows = 0;
+    }
+
+    // ---- copies: slot 2 i holds the keys, slot 2 i + 1 the values of item i
+    Cursor src = at;
+    int copied = 0, slot_in = 0;      // slots copied, and where the next goes
+    int64_t off[2];                   // of this lane's key of the item: keys, values
+    bool ok = false;
+    const auto copy_slot = [&]() {
+        const int which = copied & 1;
+        if (copied < 2 * items) {
+            if (which == 0) {
+                const int j = src.k * UNIT + warp * KB + lane % KB;
+                ok = j < src.s.m && j >= key_lo(p, src.s, 0);
+                off[0] = off[1] = 0;
+                if (ok) {
+                    int page, row;
+                    locate(p, src.b, src.s, j, page, row);
+                    ok = page >= 0;
+                    if (ok) {
+                        off[0] = kv_offset(p.kv[0], page, row, src.h);
+                        off[1] = kv_offset(p.kv[1], page, row, src.h);
+                    }
+                }
+                step<UNIT>(p, src);
+            }
+            const uint8_t *base = p.kv[which].p;
+            const int64_t mine = which ? off[1] : off[0];
+            const uint32_t dst = ring_at + slot_in * S::SLOT;
+            constexpr int ROWS = CH >= 32 ? 1 : 32 / CH;      // rows of an instruction (CH = 12, 24: idle lanes)
+            const int sub = lane / CH, chunk = lane % CH;
+#pragma unroll
+            for (int r = 0; r < KB; r += ROWS) {
+                const int row = r + sub;
+                const bool in = sub < ROWS && row < KB;
+                const int64_t o = __shfl_sync(0xffffffffu, mine, row & 31);
+                const bool good = __shfl_sync(0xffffffffu, ok, row & 31);
+                if (in)
+                    copy16(dst + row * S::PITCH + swz<CH>(row, chunk) * 16, base + o * S::ES + chunk * 16,
+                           good && chunk * 16 < p.D * S::ES);
+            }
+        }
+        copy_commit();
+        ++copied;
+        slot_in = slot_in + 1 == NS ? 0 : slot_in + 1;
+    };
+    for (int i = 0; i < NS - 1; ++i) copy_slot();
+
+    // ---- a tile's state
+    const int g = lane >> 2, q4 = lane & 3;                   // rows g and g + 8, columns 2 q4, 2 q4 + 1
+    const int tok0 = p.group.div(g), tok1 = p.group.div(g + 8);
+    uint32_t qa[DP / 16][4];
+    float o[DP / 8][4], m0, m1, l0, l1, c0, c1, vs = 1.f, ks = 1.f;
+    int hi0, hi1, lo0, lo1, hi_all = 0, lo_all = 0;
+    if (KIND != KV_BF16) {
+        ks = ld_f32_ro(p.scale[0]);
+        vs = ld_f32_ro(p.scale[1]);
+    }
+    const auto load_queries = [&]() {
+        c0 = c1 = p.qk_scale * ks;
+        const bool in0 = g < R, in1 = g + 8 < R;
+        const uint16_t *r0 = p.q.p + (at.s.first + (in0 ? tok0 : 0)) * p.q.ld + (at.h * G + (in0 ? g - tok0 * G : 0)) * p.q.hs;
+        const uint16_t *r1 = p.q.p + (at.s.first + (in1 ? tok1 : 0)) * p.q.ld + (at.h * G + (in1 ? g + 8 - tok1 * G : 0)) * p.q.hs;
+        const auto pair = [&](const uint16_t *r, bool in, int d) -> uint32_t {
+            if (!in || d >= p.D || !dbg_global(r + d, 4, false)) return 0u;
+            return __ldg(reinterpret_cast<const uint32_t *>(r + d));
+        };
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            const int d0 = 16 * k + (KIND == KV_BF16 ? 2 : 4) * q4, d1 = d0 + (KIND == KV_BF16 ? 8 : 2);
+            qa[k][0] = pair(r0, in0, d0);
+            qa[k][1] = pair(r1, in1, d0);
+            qa[k][2] = pair(r0, in0, d1);
+            qa[k][3] = pair(r1, in1, d1);
+        }
+        if constexpr (KIND != KV_BF16) {
+            float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float v = fmaxf(fabsf(bf_lo(qa[k][i])), fabsf(bf_hi(qa[k][i])));
+                    if (i & 1) a1 = fmaxf(a1, v);
+                    else a0 = fmaxf(a0, v);
+                }
+            for (int w = 1; w < 4; w *= 2) {
+                a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, w));
+                a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, w));
+            }
+            const int e0 = row_exponent(a0), e1 = row_exponent(a1);
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = i & 1 ? e1 : e0;
+                    qa[k][i] = pack_f16(scaled(bf_lo(qa[k][i]), e), scaled(bf_hi(qa[k][i]), e));
+                }
+            c0 = scaled(c0, -e0);
+            c1 = scaled(c1, -e1);
+        }
+#pragma unroll
+        for (int k = 0; k < DP / 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+        hi0 = key_hi(p, at.s, tok0);
+        hi1 = key_hi(p, at.s, tok1);
+        lo0 = key_lo(p, at.s, tok0);
+        lo1 = key_lo(p, at.s, tok1);
+        hi_all = key_hi(p, at.s, 0);                          // keys that all rows see
+        lo_all = key_lo(p, at.s, p.n - 1);
+    };
+    load_queries();
+
+    // ---- the items
+    int slot = 0;
+    for (int item = 0; item < items; ++item) {
+        const int j0 = at.k * UNIT + warp * KB;
+        float x[KB / 8][4];
+        copy_wait<NS - 2>();
+        __syncwarp();
+        const uint32_t keys = ring_at + slot * S::SLOT;
+        const uint8_t *keys_p = ring + slot * S::SLOT;
+#pragma unroll
+        for (int b = 0; b < KB / 8; ++b) x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            if constexpr (KIND == KV_BF16) {
+#pragma unroll
+                for (int b = 0; b < KB / 16; ++b) {
+                    const int row = 16 * b + (lane & 7) + ((lane >> 4) << 3), chunk = 2 * k + ((lane >> 3) & 1);
+                    uint32_t f[4];
+                    ldsm4(f, keys + row * S::PITCH + swz<CH>(row, chunk) * 16);
+                    mma<KIND>(x[2 * b], qa[k], f[0], f[1]);
+                    mma<KIND>(x[2 * b + 1], qa[k], f[2], f[3]);
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < KB / 8; ++b) {
+                    const int row = 8 * b + g;
+                    const uint32_t codes = *reinterpret_cast<const uint32_t *>(keys_p + row * S::PITCH + swz<CH>(row, k) * 16 + 4 * q4);
+                    mma<KIND>(x[b], qa[k], f16_fp8<KIND>(codes), f16_fp8<KIND>(codes >> 16));
+                }
+            }
+        }
+        __syncwarp();                 // all lanes have read the slot before the last
+        slot = slot + 1 == NS ? 0 : slot + 1;
+        copy_slot();
+        if (j0 + KB > hi_all || j0 < lo_all) {
+#pragma unroll
+            for (int b = 0; b < KB / 8; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = j0 + 8 * b + 2 * q4 + i;
+                    if (j >= hi0 || j < lo0) x[b][i] = -INFINITY;
+                    if (j >= hi1 || j < lo1) x[b][2 + i] = -INFINITY;
+                }
+        }
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < KB / 8; ++b) {
+            t0 = fmaxf(t0, fmaxf(x[b][0], x[b][1]));
+            t1 = fmaxf(t1, fmaxf(x[b][2], x[b][3]));
+        }
+        for (int w = 1; w < 4; w *= 2) {
+            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
+            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+        }
+        t0 = fmaxf(m0, t0 * c0);
+        t1 = fmaxf(m1, t1 * c1);
+        if (__any_sync(0xffffffffu, t0 > m0 || t1 > m1)) {
+            const float a0 = t0 > m0 ? exp2_fast(m0 - t0) : 1.f, a1 = t1 > m1 ? exp2_fast(m1 - t1) : 1.f;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int k = 0; k < DP / 8; ++k) {
+                o[k][0] *= a0;
+                o[k][1] *= a0;
+                o[k][2] *= a1;
+                o[k][3] *= a1;
+            }
+            m0 = t0;
+            m1 = t1;
+        }
+        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+        uint32_t pa[KB / 16][4];      // the weights: BF16 (FP8 caches: FP16) operands of the product with the values
+#pragma unroll
+        for (int b = 0; b < KB / 8; ++b) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = exp2_fast(fmaf(x[b][i], i < 2 ? c0 : c1, i < 2 ? -z0 : -z1));
+            l0 += w[0] + w[1];
+            l1 += w[2] + w[3];
+            pa[b / 2][(b & 1) * 2] = KIND == KV_BF16 ? pack_bf16(w[0], w[1]) : pack_f16(w[0], w[1]);
+            pa[b / 2][(b & 1) * 2 + 1] = KIND == KV_BF16 ? pack_bf16(w[2], w[3]) : pack_f16(w[2], w[3]);
+        }
+        copy_wait<NS - 2>();
+        __syncwarp();
+        const uint32_t values = ring_at + slot * S::SLOT;
+#pragma unroll
+        for (int b = 0; b < KB / 16; ++b) {
+            if constexpr (KIND == KV_BF16) {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const int row = 16 * b + (lane & 15), chunk = 2 * k + (lane >> 4);
+                    uint32_t f[4];
+                    ldsm4_t(f, values + row * S::PITCH + swz<CH>(row, chunk) * 16);
+                    mma<KIND>(o[2 * k], pa[b], f[0], f[1]);
+                    mma<KIND>(o[2 * k + 1], pa[b], f[2], f[3]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < DP / 32; ++k) {
+                    const int row = 16 * b + (lane & 15), chunk = 2 * k + (lane >> 4);
+                    uint32_t f[4];
+                    ldsm4_t(f, values + row * S::PITCH + swz<CH>(row, chunk) * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = __byte_perm(f[i], 0, 0x3120);   // even column of two keys, odd column
+                    // Products 4 k, 4 k + 1: even and odd columns of chunk 2 k; 4 k + 2, 4 k + 3: of chunk 2 k + 1.
+                    mma<KIND>(o[4 * k], pa[b], f16_fp8<KIND>(f[0]), f16_fp8<KIND>(f[1]));
+                    mma<KIND>(o[4 * k + 1], pa[b], f16_fp8<KIND>(f[0] >> 16), f16_fp8<KIND>(f[1] >> 16));
+                    mma<KIND>(o[4 * k + 2], pa[b], f16_fp8<KIND>(f[2]), f16_fp8<KIND>(f[3]));
+                    mma<KIND>(o[4 * k + 3], pa[b], f16_fp8<KIND>(f[2] >> 16), f16_fp8<KIND>(f[3] >> 16));
+                }
+            }
+        }
+        __syncwarp();
+        slot = slot + 1 == NS ? 0 : slot + 1;
+        copy_slot();
+
+        const bool tile_ends = at.k + 1 == at.k1;
+        if (!tile_ends && item + 1 < items) {
+            ++at.k;
+            continue;
+        }
+        // ---- the tile's end, or this CTA's: join the warps
+        for (int w = 1; w < 4; w *= 2) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = g + 8 * half;
+            if (row >= R) continue;
+            float *dst = join_o + (warp * kDecodeRows + row) * DP;
+#pragma unroll
+            for (int k = 0; k < DP / 8; ++k) {
+                const float a = o[k][2 * half], b = o[k][2 * half + 1];
+                if constexpr (KIND == KV_BF16) {
+                    *reinterpret_cast<float2 *>(dst + turn(row, 8 * k + 2 * q4)) = make_float2(a, b);
+                } else {
+                    const int d = 16 * (k / 2) + 4 * q4 + (k & 1);    // columns 2 n + parity of a chunk
+                    dst[turn(row, d)] = a;
+                    dst[turn(row, d + 2)] = b;
+                }
+            }
+            if (q4 == 0) {
+                float *ml = join_ml + (warp * kDecodeRows + row) * 2;
+                ml[0] = half ? m1 : m0;
+                ml[1] = half ? l1 : l0;
+            }
+        }
+        __syncthreads();
+        const bool whole = tile_first >= work.u0 && tile_ends;
+        float *const part = whole ? nullptr : part_of(p.ws, blockIdx.x, tile_first >= work.u0, kDecodeRows, DP);
+        for (int e = tid; e < R * (DP / 4); e += W * 32) {
+            const int row = e / (DP / 4), d = (e - row * (DP / 4)) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w) M = fmaxf(M, join_ml[(w * kDecodeRows + row) * 2]);
+            const float z = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            F2 a = f2(0.f), b = f2(0.f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float2 ml = *reinterpret_cast<const float2 *>(join_ml + (w * kDecodeRows + row) * 2);
+                const float4 v = *reinterpret_cast<const float4 *>(join_o + (w * kDecodeRows + row) * DP + turn(row, d));
+                const float s = exp2f(ml.x - z);
+                L = fmaf(ml.y, s, L);
+                a = f2_fma(f2(v.x, v.y), f2(s), a);
+                b = f2_fma(f2(v.z, v.w), f2(s), b);
+            }
+            if (whole) {
+                const int i = p.group.div(row), hq = at.h * G + row - i * G;
+                const int64_t t = at.s.first + i;
+                const float inv = L == 0.f ? 0.f : vs / L;
+                a = f2_mul(a, f2(inv));
+                b = f2_mul(b, f2(inv));
+                if (d < p.D) {
+                    if (suspect(a.x, L) || suspect(a.y, L) || suspect(b.x, L) || suspect(b.y, L)) atomicOr(&odd_rows, 1u << row);
+                    st_u32x2(const_cast<uint16_t *>(p.out.p) + t * p.out.ld + hq * p.out.hs + d, bf16_f2(a), bf16_f2(b));
+                }
+                if (d == 0 && p.lse)
+                    st_f32(p.lse + t * p.out.H + hq, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
+            } else {
+                if (d == 0) {
+                    st_f32(part + 2 * row, M);
+                    st_f32(part + 2 * row + 1, L);
+                }
+                st_f32x4(part + 2 * kDecodeRows + row * DP + d, a.x, a.y, b.x, b.y);
+            }
+        }
+        __syncthreads();
+        if (whole && odd_rows) {
+            for (int row = warp; row < R; row += W)
+                if (odd_rows >> row & 1u) {
+                    const int i = p.group.div(row);
+                    attend_row<KIND, DP / 32>(p, at.b, at.s, i, at.h * G + row - i * G, false);
+                }
+            __syncthreads();
+            if (tid == 0) odd_rows = 0;
+            __syncthreads();
+        }
+        if (item + 1 < items) {
+            tile_first += at.k1 - at.k0;
+            step<UNIT>(p, at);
+            load_queries();
+        }
+    }
+    copy_wait<0>();
+}
+
+template <int KIND, int DP>
+cudaError_t run(const AttnParams &p, int sms, cudaStream_t s)
+{
+    using S = Shape<KIND, DP>;
+    static std::atomic<int> opted[kOptInDevices];
+    if (cudaError_t e = opt_in_smem(k_attn_decode<KIND, DP>, S::SMEM, opted)) return e;
+    const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
+    if (cudaError_t e = launch_pdl(k_attn_decode<KIND, DP>, dim3(ctas), dim3(S::W * 32), S::SMEM, s, p)) return e;
+    return launch_attn_combine(p, kDecodeRows, DP, ctas, s);
+}
+
+template <int KIND>
+cudaError_t run(const AttnParams &p, int sms, cudaStream_t s)
+{
+    switch (attn_padded(p.D)) {
+        case 64: return run<KIND, 64>(p, sms, s);
+        case 128: return run<KIND, 128>(p, sms, s);
+        case 192: return run<KIND, 192>(p, sms, s);
+        default: return run<KIND, 256>(p, sms, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnParams &p, int sms, cudaStream_t s)
+{
+    switch (p.kind) {
+        case KV_BF16: return run<KV_BF16>(p, sms, s);
+        case KV_E4M3: return run<KV_E4M3>(p, sms, s);
+        default: return run<KV_E5M2>(p, sms, s);
+    }
+}
+
+}  // namespace crmsn
