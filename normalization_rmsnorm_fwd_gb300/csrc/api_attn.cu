@@ -76,7 +76,11 @@ crmsn_status launch(const AttnParams &p, bool fast, int sms, cudaStream_t stream
 {
     if (!fast) return launched(launch_attn_row(p, sms, stream));
     if (!p.starts && (int64_t)p.n * p.group.d <= kDecodeRows) return launched(launch_attn_decode(p, sms, stream));
-    return launched(launch_attn_row(p, sms, stream));
+    switch (p.kind) {
+        case CRMSN_CACHE_BF16: return launched(launch_attn_tile_bf16(p, sms, stream));
+        case CRMSN_CACHE_E4M3: return launched(launch_attn_tile_e4m3(p, sms, stream));
+        default: return launched(launch_attn_tile_e5m2(p, sms, stream));
+    }
 }
 
 }  // namespace
@@ -90,7 +94,8 @@ size_t attention_workspace_bytes(int64_t D, int device)
     const int sms = sm_count(device);
     if (sms <= 0) return 0;
     const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
-    const int64_t parts = D <= kAttnMaxDim ? 2 * ctas * attn_part_floats(kDecodeRows, attn_padded((int)D)) : 0;
+    const int DP = attn_padded((int)D);
+    const int64_t parts = D <= kAttnMaxDim ? 2 * ctas * attn_part_floats(attn_tile_rows(DP), DP) : 0;
     return (size_t)(kAttnParts + parts * (int64_t)sizeof(float) + 255) / 256 * 256;
 }
 

@@ -219,11 +219,11 @@ __device__ __forceinline__ Work share_work(int B, int Hk, WorkScratch &sm, Count
     w.units *= Hk;
     w.ctas = ctas(w.units, tiles * Hk);
     const int c = (int)blockIdx.x;
+    w.u0 = w.u1 = w.rest = 0;
+    w.b = 0;
+    if (c >= w.ctas) return w;   // the same for all threads (no units: no CTAs)
     w.u0 = first_unit(w.units, w.ctas, c);
     w.u1 = first_unit(w.units, w.ctas, c + 1);
-    w.b = 0;
-    w.rest = 0;
-    if (c >= w.ctas) return w;   // the same for all threads
     // The sequence of u0: the one in which the running sum passes u0 / Hk.
     const int64_t want = w.u0 / Hk;
     int64_t before = 0;

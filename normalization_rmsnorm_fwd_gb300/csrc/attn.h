@@ -81,6 +81,13 @@ cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int ctas,
 constexpr int kDecodeRows = 16;
 cudaError_t launch_attn_decode(const AttnParams &p, int sms, cudaStream_t s);
 
+// Everything else of those head sizes and layouts, on the tensor cores
+// (attn_tile_*.cu): attn_tile_rows() rows of a sequence and key head at once.
+inline int attn_tile_rows(int DP) { return DP > 192 ? 128 : 256; }
+cudaError_t launch_attn_tile_bf16(const AttnParams &p, int sms, cudaStream_t s);
+cudaError_t launch_attn_tile_e4m3(const AttnParams &p, int sms, cudaStream_t s);
+cudaError_t launch_attn_tile_e5m2(const AttnParams &p, int sms, cudaStream_t s);
+
 // One warp for each row (attn_row.cu): any layout and head size.
 cudaError_t launch_attn_row(const AttnParams &p, int sms, cudaStream_t s);
 
