@@ -63,7 +63,7 @@ inline int attn_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 
 // of the tile that it finds begun, the beginning of the one that it leaves).
 // A part of `rows` rows: their maxima and sums, then rows x DP sums of values.
 struct AttnHeader {
-    int64_t first, last, units;  // units of the tile, of all tiles
+    int64_t first, last, units;  // units of the tile's blocks; of all tiles
     int ctas, tile;              // CTAs that share them; 1: begins inside this tile
     int b, h, tok, ntok;         // sequence, key head, first token and tokens of the tile
     int pad[4];

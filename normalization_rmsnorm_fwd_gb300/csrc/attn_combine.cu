@@ -63,11 +63,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_const
     const int i = p.group.div(r), hq = hd.h * p.group.d + (r - i * p.group.d);
     const int64_t t = hd.tok + i;
     const float vs = KIND == KV_BF16 ? 1.f : ld_f32_ro(p.scale[1]);
-    const float inv = L == 0.f ? 0.f : vs / L;
+    const float inv = vs / L;
     uint16_t *out = const_cast<uint16_t *>(p.out.p) + t * p.out.ld + hq * p.out.hs + 2 * lane;
     bool odd = false;
     for (int k = 0; k < NV; ++k) {
-        const F2 y = f2_mul(o[k], f2(inv));
+        const F2 y = L == 0.f ? f2(0.f) : f2_mul(o[k], f2(inv));    // no key: zeros, whatever 0 times the values was
         odd = odd || (2 * lane + 64 * k < p.D && (suspect(y.x, L) || suspect(y.y, L)));
         if (2 * lane + 64 * k < p.D && dbg_global(out + 64 * k, 4, true))
             *reinterpret_cast<uint32_t *>(out + 64 * k) = bf16_f2(y);

@@ -432,9 +432,9 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             if (whole) {
                 const int i = p.group.div(row), hq = at.h * G + row - i * G;
                 const int64_t t = at.s.first + i;
-                const float inv = L == 0.f ? 0.f : vs / L;
-                a = f2_mul(a, f2(inv));
-                b = f2_mul(b, f2(inv));
+                const float inv = vs / L;
+                a = L == 0.f ? f2(0.f) : f2_mul(a, f2(inv));  // no key: zeros, whatever 0 times the values was
+                b = L == 0.f ? f2(0.f) : f2_mul(b, f2(inv));
                 if (d < p.D) {
                     if (suspect(a.x, L) || suspect(a.y, L) || suspect(b.x, L) || suspect(b.y, L)) atomicOr(&odd_rows, 1u << row);
                     st_u32x2(const_cast<uint16_t *>(p.out.p) + t * p.out.ld + hq * p.out.hs + d, bf16_f2(a), bf16_f2(b));

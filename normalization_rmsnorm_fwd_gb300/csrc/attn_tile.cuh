@@ -9,7 +9,8 @@
 //
 // 16 warps: 0-3 and 4-7 work out the weights of the two halves of a tile, one
 // row a thread, so that a row's maximum and sum never leave the thread; 8-11
-// copy keys and values; one thread of warp 12 issues the products.  While one
+// copy keys and values; warp 12 issues the products; warp 13 walks through the
+// CTA's work and hands it to the others piece by piece.  While one  While one
 // half's weights are worked out, the tensor cores run the other half's
 // products: S of the next block follows O of this one at once.  Heads of 256
 // leave no room for two halves in tensor memory (O takes 256 of its 512
@@ -44,10 +45,12 @@ struct TileShape {
     static constexpr int ROWS = NT * 128;
     static constexpr int QBYTES = 128 * DP * 2;              // queries of a half
     static constexpr int STAGE = BN * DP * 2;                // keys or values of a block
-    static constexpr int STAGES = DP == 64 ? (FP8 ? 5 : 8) : (FP8 ? 3 : 5);
+    static constexpr int STAGES = DP == 64 ? (FP8 ? 5 : 8) : (FP8 ? 3 : 4);
     static constexpr int RAW = FP8 ? BN * DP : 0;            // FP8 codes of a block
-    static constexpr int RAWS = FP8 ? (DP == 64 ? 8 : 4) : 0;
-    static constexpr int SMEM = 1024 + NT * QBYTES + STAGES * STAGE + RAWS * RAW;
+    static constexpr int RAWS = FP8 ? (DP == 64 ? 8 : 3) : 0;
+    // Bytes of a row that its result passes through on its way out.
+    static constexpr int OUT = FP8 && (DP == 128 || DP == 192) ? 64 : 128;
+    static constexpr int SMEM = 1024 + NT * QBYTES + STAGES * STAGE + RAWS * RAW + NT * 128 * OUT;
     static constexpr int OCOL = DP == 256 ? 256 : NT * NS * BN;   // columns of S, then of O
     static_assert(OCOL + NT * DP <= 512, "tensor memory");
     static_assert(SMEM + 1600 <= 227 * 1024, "shared memory");
@@ -56,7 +59,7 @@ constexpr int kTileThreads = 512;
 constexpr int kTileColumns = 512;
 // Registers of a thread: of the 128 at launch the copying and the issuing
 // warps give up what the weights' warps need.
-constexpr int kWeightRegs = 184, kOtherRegs = 72;
+constexpr int kWeightRegs = 152, kOtherRegs = 104;
 static_assert(2 * kWeightRegs + 2 * kOtherRegs <= 4 * 128, "registers of the launch");
 
 // sum of floor((a i + b) / m) over 0 <= i < n (the classic Euclid-like
@@ -65,19 +68,24 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 {
     int64_t sum = 0;
     while (n > 0) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
+        const int64_t qa = quotient(a, m), qb = quotient(b, m);
+        sum += n * (n - 1) / 2 * qa + n * qb;
+        a -= qa * m;
+        b -= qb * m;
         const int64_t y = a * n + b;
         if (y < m) break;
-        n = y / m;
-        b = y % m;
+        n = quotient(y, m);
+        b = y - n * m;
         const int64_t t = m;
         m = a;
         a = t;
     }
     return sum;
 }
+
+// What a tile costs beside its blocks (its queries' and results' ways, the
+// first scores that nothing overlaps), in blocks.
+constexpr int kTileCost = 2;
 
 // The tiles of a sequence: TT tokens each.  Tile t takes the blocks [k0, k1),
 // at least one.
@@ -114,23 +122,21 @@ __device__ __forceinline__ int64_t blocks_before(const AttnParams &p, const Seq 
     return sum;
 }
 
-// A piece of a CTA's work: blocks [k, end) of a tile that has [k0, k1).
-struct Piece {
+// A CTA's work is a run of units: a tile is kTileCost units, then one for each
+// block.  A CTA whose units end inside the former has no part of the tile, one
+// whose units begin there has all of its first blocks.  The walk:
+struct Walk {
     int b, h, t, nt;
     Seq s;
-    int k, end, k0, k1;
+    int k, end, k0, k1;              // blocks [k, end) of a tile that has [k0, k1)
     int64_t left;                    // units from block k on
 };
+__device__ __forceinline__ void walk_end(Walk &c) { c.end = (int)min((int64_t)c.k1, c.k + c.left); }
+// To the next tile; false: there is no more work.
 template <int BN>
-__device__ __forceinline__ void piece_ends(Piece &c)
+__device__ __forceinline__ bool walk_on(const AttnParams &p, int TT, Walk &c)
 {
-    c.end = (int)min((int64_t)c.k1, c.k + c.left);
-}
-// The next piece; false: there is none.
-template <int BN>
-__device__ __forceinline__ bool next_piece(const AttnParams &p, int TT, Piece &c)
-{
-    c.left -= c.end - c.k;
+    c.left -= c.end - c.k + kTileCost;
     if (c.left <= 0) return false;
     if (++c.t == c.nt) {
         c.t = 0;
@@ -145,9 +151,18 @@ __device__ __forceinline__ bool next_piece(const AttnParams &p, int TT, Piece &c
     }
     tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
     c.k = c.k0;
-    piece_ends<BN>(c);
+    walk_end(c);
     return true;
 }
+// What the other warps are told of a piece.
+struct __align__(16) Piece {
+    int b, h, tok, ntok;             // sequence, key head, first token and tokens of the tile
+    Seq s;
+    int k;                           // blocks [k, end)
+    int end, flags, hi, lo;          // keys [lo, hi) that the tile's rows see
+};
+enum { PIECE_BEGINS = 1, PIECE_ENDS = 2, PIECE_NONE = 4 };   // the tile's first block, its last; no piece: the end
+constexpr int kPieces = 8;
 
 template <int KIND, int DP>
 struct TileKernel {
@@ -156,15 +171,18 @@ struct TileKernel {
     static constexpr bool FP8 = S::FP8;
 
     struct Shared {
-        WorkScratch scratch;
-        uint64_t full[STAGES], empty[STAGES], q[NT], s[NT * NS], w[NT * NS], o[NT], last;
+        union {
+            WorkScratch scratch;                              // at the start
+            Piece piece[kPieces];
+        };
+        uint64_t full[STAGES], empty[STAGES], landed[STAGES], q[NT], s[NT * NS], w[NT * NS][2], o[NT], last, told[kPieces], heard[kPieces];
         uint32_t tmem;
         volatile int failed;
     };
 
     const AttnParams &p;
     Shared &sm;
-    uint8_t *const base;             // queries, stages, codes
+    uint8_t *const base;             // queries, stages, codes, results
     uint32_t tmem;
     int TT;
 
@@ -175,17 +193,81 @@ struct TileKernel {
     {
         return __all_sync(0xffffffffu, wait(bar, parity));
     }
+    // This warp's writes to shared or to tensor memory are done, for the products.
+    static __device__ __forceinline__ void ready(const uint64_t *bar)
+    {
+        fence_async();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(at(bar));
+    }
+    static __device__ __forceinline__ void ready_tmem(const uint64_t *bar)
+    {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) bar_arrive(at(bar));
+    }
     __device__ __forceinline__ uint8_t *queries(int half) const { return base + half * S::QBYTES; }
     __device__ __forceinline__ uint8_t *stage(int i) const { return base + NT * S::QBYTES + i * S::STAGE; }
-    __device__ __forceinline__ int rows_of(const Piece &c) const
-    {
-        return min(TT, c.s.n - c.t * TT) * p.group.d;
-    }
+    __device__ __forceinline__ int rows_of(const Piece &c) const { return c.ntok * p.group.d; }
     __device__ __forceinline__ bool used(const Piece &c, int half) const { return rows_of(c) > half * 128; }
 
     static __device__ __forceinline__ void put16(uint8_t *at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
     {
         if (dbg_shared(at, 16)) *reinterpret_cast<uint4 *>(at) = make_uint4(a, b, c, d);
+    }
+
+    // ------------------------------------------------------------- pieces --
+    // A reader's place in the pieces.
+    struct Place {
+        int i;
+        uint32_t parity;
+    };
+    // The next piece, read by a whole warp; false: no more, or a wait ran out.
+    // keep: another reader of this warp will follow, which lets the place go.
+    __device__ __forceinline__ bool next(Place &at_, Piece &c, bool keep = false)
+    {
+        if (!wait_all(&sm.told[at_.i], at_.parity)) return false;
+        const int4 *src = reinterpret_cast<const int4 *>(&sm.piece[at_.i]);
+        int4 *dst = reinterpret_cast<int4 *>(&c);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Piece) / 16); ++i) dst[i] = src[i];
+        __syncwarp();
+        if (!keep && (threadIdx.x & 31) == 0) bar_arrive(at(&sm.heard[at_.i]));
+        if (++at_.i == kPieces) {
+            at_.i = 0;
+            at_.parity ^= 1;
+        }
+        return !(c.flags & PIECE_NONE);
+    }
+    // Warp 13.
+    __device__ __forceinline__ void tell_loop(Walk c)
+    {
+        int i = 0;
+        uint32_t parity = 1;
+        for (bool more = true;; more = walk_on<BN>(p, TT, c)) {
+            if (!wait_all(&sm.heard[i], parity)) return;
+            if ((threadIdx.x & 31) == 0) {
+                Piece &d = sm.piece[i];
+                d.b = c.b;
+                d.h = c.h;
+                d.tok = c.t * TT;
+                d.ntok = min(TT, c.s.n - c.t * TT);
+                d.s = c.s;
+                d.k = c.k;
+                d.end = c.end;
+                d.flags = (c.k == c.k0 ? PIECE_BEGINS : 0) | (c.end == c.k1 ? PIECE_ENDS : 0) | (more ? 0 : PIECE_NONE);
+                d.hi = key_hi(p, c.s, d.tok + d.ntok - 1);
+                d.lo = key_lo(p, c.s, d.tok);
+                bar_arrive(at(&sm.told[i]));
+            }
+            __syncwarp();
+            if (!more) return;
+            if (++i == kPieces) {
+                i = 0;
+                parity ^= 1;
+            }
+        }
     }
 
     // ------------------------------------------------------------- copies --
@@ -195,12 +277,12 @@ struct TileKernel {
         int64_t off[2];
         bool ok;
     };
-    __device__ __forceinline__ Rows find_rows(const Piece &c, int k, int hi, int lo) const
+    __device__ __forceinline__ Rows find_rows(const Piece &c) const
     {
         const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
         Rows r{{0, 0}, false};
-        const int j = k * BN + warp * (BN / 4) + lane % (BN / 4);
-        if (j < hi && j >= lo) {
+        const int j = c.k * BN + warp * (BN / 4) + lane % (BN / 4);
+        if (j < c.hi && j >= c.lo) {
             int page, row;
             locate(p, c.b, c.s, j, page, row);
             if (page >= 0) {
@@ -248,102 +330,90 @@ struct TileKernel {
         }
     }
 
-    // BF16: blocks in the order K0 V0 K1 V1 ..., their arrival announced up to
-    // AHEAD blocks later, or as soon as there is no free stage.
-    __device__ __forceinline__ void copy_loop(Piece c)
+    // BF16: blocks in the order K0 V0 K1 V1 ...  Copies and announcements wait
+    // for nothing but their own condition: an empty stage, copies that have
+    // landed.  (Each thread's copies are seen by the products after its own fence
+    // behind their landing.)
+    __device__ __forceinline__ void copy_loop()
     {
-        constexpr int AHEAD = 3;
         int in = 0, out = 0, pending = 0;                     // stages to fill, to announce
-        uint32_t parity = 1;                                  // of `in`'s emptiness: free at first
-        const auto announce = [&]() {
-            fence_async();
-            bar_arrive(at(&sm.full[out]));
-            out = out + 1 == STAGES ? 0 : out + 1;
-            --pending;
-        };
-        do {
-            const int TTt = c.t * TT, last = min(TTt + TT, c.s.n) - 1;
-            const int hi = key_hi(p, c.s, last), lo = key_lo(p, c.s, TTt);
-            for (int k = c.k; k < c.end; ++k) {
-                const Rows r = find_rows(c, k, hi, lo);
-                for (int which = 0; which < 2; ++which) {
-                    if (!__all_sync(0xffffffffu, bar_try(at(&sm.empty[in]), parity))) {
-                        copy_wait<0>();
-                        while (pending) announce();
-                        if (!wait_all(&sm.empty[in], parity)) return;
-                    }
-                    copy_rows(r, which, smem_addr(stage(in)));
-                    copy_commit();
-                    ++pending;
-                    if (++in == STAGES) {
-                        in = 0;
-                        parity ^= 1;
-                    }
-                    if (pending > AHEAD) {
-                        copy_wait<AHEAD>();
-                        announce();
-                    }
+        uint32_t empty = 1, landed = 0;                       // parities: all stages are empty at first
+        Place place{0, 0};
+        Piece c;
+        bool more = next(place, c);
+        int which = 0;
+        Rows r = find_rows(c);
+        for (int idle = 0; more || pending;) {
+            if (more && __all_sync(0xffffffffu, bar_test(at(&sm.empty[in]), empty))) {
+                copy_rows(r, which, smem_addr(stage(in)));
+                bar_arrive_copies(at(&sm.landed[in]));
+                ++pending;
+                if (++in == STAGES) {
+                    in = 0;
+                    empty ^= 1;
                 }
+                which ^= 1;
+                if (which == 0) {
+                    if (++c.k == c.end) more = next(place, c);
+                    if (more) r = find_rows(c);
+                }
+                idle = 0;
             }
-        } while (next_piece<BN>(p, TT, c));
-        copy_wait<0>();
-        while (pending) announce();
+            if (pending && __all_sync(0xffffffffu, bar_test(at(&sm.landed[out]), landed))) {
+                ready(&sm.full[out]);
+                if (++out == STAGES) {
+                    out = 0;
+                    landed ^= 1;
+                }
+                --pending;
+                idle = 0;
+            }
+            if (++idle > 256 && (__any_sync(0xffffffffu, sm.failed) || idle > kWaitTries)) {
+                sm.failed = 1;
+                return;
+            }
+        }
     }
 
     // FP8: the codes run RAWS - 1 blocks ahead.
-    __device__ __forceinline__ void convert_loop(Piece c)
+    __device__ __forceinline__ void convert_loop()
     {
         constexpr int RAWS = S::RAWS > 0 ? S::RAWS : 1;
         uint8_t *const raw = stage(STAGES);
-        Piece src = c;
-        int64_t total = 2 * c.left, copied = 0;
-        int hi = 0, lo = 0, slot_in = 0;
+        Place ahead{0, 0}, place{0, 0};
+        Piece src, c;
+        int slot_in = 0, which = 0;
+        bool more = next(ahead, src, true);
         Rows r{};
-        bool fresh = true;
         const auto copy_next = [&]() {
-            if (copied < total) {
-                const int which = (int)(copied & 1);
-                if (which == 0) {
-                    if (fresh) {
-                        const int first = src.t * TT, last = min(first + TT, src.s.n) - 1;
-                        hi = key_hi(p, src.s, last);
-                        lo = key_lo(p, src.s, first);
-                        fresh = false;
-                    }
-                    r = find_rows(src, src.k, hi, lo);
-                }
+            if (more) {
+                if (which == 0) r = find_rows(src);
                 copy_rows(r, which, smem_addr(raw + slot_in * S::RAW));
-                if (which == 1) {
-                    // One block further: a piece of its own for the cursor.
-                    ++src.k;
-                    --src.left;
-                    if (src.k == src.end && src.left > 0) {
-                        next_piece<BN>(p, TT, src);
-                        fresh = true;
-                    }
-                }
+                if (which == 1 && ++src.k == src.end) more = next(ahead, src, true);
+                which ^= 1;
             }
             copy_commit();
-            ++copied;
             slot_in = slot_in + 1 == RAWS ? 0 : slot_in + 1;
         };
+#pragma unroll 1
         for (int i = 0; i < RAWS - 1; ++i) copy_next();
         int slot = 0, to = 0;
         uint32_t parity = 1;
-        for (int64_t i = 0; i < total; ++i) {
-            copy_next();                                      // into the slot converted last
-            copy_wait<RAWS - 1>();
-            if (!wait_all(&sm.empty[to], parity)) break;
-            convert(raw + slot * S::RAW, stage(to));
-            fence_async();
-            bar_arrive(at(&sm.full[to]));
-            slot = slot + 1 == RAWS ? 0 : slot + 1;
-            if (++to == STAGES) {
-                to = 0;
-                parity ^= 1;
+        while (next(place, c)) {
+#pragma unroll 1
+            for (int i = 2 * (c.end - c.k); i > 0; --i) {
+                copy_next();                                  // into the slot converted last
+                copy_wait<RAWS - 1>();
+                if (!wait_all(&sm.empty[to], parity)) return;
+                convert(raw + slot * S::RAW, stage(to));
+                ready(&sm.full[to]);
+                slot = slot + 1 == RAWS ? 0 : slot + 1;
+                if (++to == STAGES) {
+                    to = 0;
+                    parity ^= 1;
+                }
             }
         }
-        copy_wait<0>();
     }
 
     // ----------------------------------------------------------- products --
@@ -354,22 +424,29 @@ struct TileKernel {
     __device__ __forceinline__ uint32_t o_col(int half) const { return tmem + (uint32_t)(S::OCOL + half * DP); }
     __device__ __forceinline__ void scores(int half, int buf, int st) const
     {
-        const uint32_t q = smem_addr(queries(half)), k = smem_addr(stage(st));
+        const uint32_t q = matrix_low(smem_addr(queries(half)), 16), k = matrix_low(smem_addr(stage(st)), 16);
+        const uint32_t d = s_col(half, buf);
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i)
-            product_ss(s_col(half, buf), matrix_desc(q + (i / 4) * (128 * 128) + (i % 4) * 32, 16),
-                       matrix_desc(k + (i / 4) * (BN * 128) + (i % 4) * 32, 16), kScores, i > 0);
+            product_ss(d, matrix_desc(q + (i / 4) * (128 * 128 / 16) + (i % 4) * 2),
+                       matrix_desc(k + (i / 4) * (BN * 128 / 16) + (i % 4) * 2), kScores, i > 0);
     }
-    __device__ __forceinline__ void values(int half, int buf, int st, bool add) const
+    // The products of the first or second half of a block's keys.
+    __device__ __forceinline__ void values(int half, int buf, int st, int part, bool add) const
     {
-        const uint32_t v = smem_addr(stage(st));
+        constexpr int N = BN / 32;
+        const uint32_t v = matrix_low(smem_addr(stage(st)), BN * 128) + part * N * (2048 / 16);
+        const uint32_t d = o_col(half), w = s_col(half, buf) + part * N * 8;
 #pragma unroll
-        for (int i = 0; i < BN / 16; ++i)
-            product_ts(o_col(half), s_col(half, buf) + i * 8, matrix_desc(v + i * 2048, BN * 128), kValues, add || i > 0);
+        for (int i = 0; i < N; ++i) product_ts(d, w + i * 8, matrix_desc(v + i * (2048 / 16)), kValues, add || part || i > 0);
     }
 
-    __device__ __forceinline__ void issue_loop(Piece c)
+    // Warp 12, all lanes together; one issues.
+    __device__ __forceinline__ void issue_loop()
     {
+        Place place{0, 0};
+        Piece c;
+        const bool one = elect_one();
         int st = 0;                                           // stage of the next block in the stream
         uint32_t full = 0;
         uint32_t q_par[NT], w_cnt[NT];                        // parities; blocks of a half so far
@@ -382,24 +459,24 @@ struct TileKernel {
                 par ^= 1;
             }
         };
-        do {
-            const int blocks = c.end - c.k;
-            bool use[NT];
-            for (int h = 0; h < NT; ++h) use[h] = used(c, h);
-            for (int h = 0; h < NT; ++h)
-                if (use[h]) {
-                    if (!wait(&sm.q[h], q_par[h])) return;
-                    q_par[h] ^= 1;
-                }
-            if (!wait(&sm.full[st], full)) return;
-            tc_fence_after();
-            for (int h = 0; h < NT; ++h)
-                if (use[h]) {
+        while (next(place, c)) {
+            const int blocks = uniform(c.end - c.k);
+            const bool both = NT == 2 && uniform((int)used(c, NT - 1));
+            const int halves = both ? 2 : 1;
+            if (!wait_all(&sm.full[st], full)) return;
+#pragma unroll
+            for (int h = 0; h < NT; ++h) {
+                if (h == 1 && !both) break;
+                if (!wait_all(&sm.q[h], q_par[h])) return;
+                q_par[h] ^= 1;
+                tc_fence_after();
+                if (one) {
                     const int buf = NS == 2 ? w_cnt[h] & 1 : 0;
                     scores(h, buf, st);
                     products_done(at(&sm.s[h * NS + buf]));
+                    if (h + 1 == halves) products_done(at(&sm.empty[st]));
                 }
-            products_done(at(&sm.empty[st]));
+            }
             for (int i = 0; i < blocks; ++i) {
                 int kst, vst;
                 uint32_t kpar, vpar;
@@ -407,45 +484,56 @@ struct TileKernel {
                 later(2, kst, kpar);
                 const bool more = i + 1 < blocks;
                 if (NS == 2) {
-                    if (more) {
-                        if (!wait(&sm.full[kst], kpar)) return;
-                        tc_fence_after();
-                        const int buf = (w_cnt[0] + 1) & 1;
-                        scores(0, buf, kst);
-                        products_done(at(&sm.s[buf]));
-                        products_done(at(&sm.empty[kst]));
-                    }
                     const int buf = w_cnt[0] & 1;
-                    if (!wait(&sm.full[vst], vpar) || !wait(&sm.w[buf], (w_cnt[0] >> 1) & 1)) return;
-                    tc_fence_after();
-                    values(0, buf, vst, i > 0);
-                    products_done(at(&sm.o[0]));
-                    products_done(at(&sm.empty[vst]));
+                    if (more) {
+                        if (!wait_all(&sm.full[kst], kpar)) return;
+                        tc_fence_after();
+                        if (one) {
+                            scores(0, buf ^ 1, kst);
+                            products_done(at(&sm.s[buf ^ 1]));
+                            products_done(at(&sm.empty[kst]));
+                        }
+                    }
+                    if (!wait_all(&sm.full[vst], vpar)) return;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        if (!wait_all(&sm.w[buf][part], (w_cnt[0] >> 1) & 1)) return;
+                        tc_fence_after();
+                        if (one) values(0, buf, vst, part, i > 0);
+                    }
+                    if (one) {
+                        products_done(at(&sm.o[0]));
+                        products_done(at(&sm.empty[vst]));
+                    }
                     ++w_cnt[0];
                 } else {
-                    bool k_here = false;
-                    if (!wait(&sm.full[vst], vpar)) return;
+                    if (!wait_all(&sm.full[vst], vpar)) return;
+#pragma unroll
                     for (int h = 0; h < NT; ++h) {
-                        if (!use[h]) continue;
-                        if (!wait(&sm.w[h], w_cnt[h] & 1)) return;
-                        tc_fence_after();
-                        values(h, 0, vst, i > 0);
-                        products_done(at(&sm.o[h]));
-                        if (h == NT - 1 || !use[NT - 1]) products_done(at(&sm.empty[vst]));
-                        if (more) {
-                            if (!k_here && !wait(&sm.full[kst], kpar)) return;
-                            k_here = true;
+                        if (h == 1 && !both) break;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            if (!wait_all(&sm.w[h][part], w_cnt[h] & 1)) return;
                             tc_fence_after();
-                            scores(h, 0, kst);
-                            products_done(at(&sm.s[h]));
+                            if (one) values(h, 0, vst, part, i > 0);
+                        }
+                        if (more && h == 0 && !wait_all(&sm.full[kst], kpar)) return;
+                        tc_fence_after();
+                        if (one) {
+                            products_done(at(&sm.o[h]));
+                            if (h + 1 == halves) products_done(at(&sm.empty[vst]));
+                            if (more) {
+                                scores(h, 0, kst);
+                                products_done(at(&sm.s[h]));
+                                if (h + 1 == halves) products_done(at(&sm.empty[kst]));
+                            }
                         }
                         ++w_cnt[h];
                     }
-                    if (more) products_done(at(&sm.empty[kst]));
                 }
                 later(2, st, full);
             }
-        } while (next_piece<BN>(p, TT, c));
+        }
     }
 
     // ------------------------------------------------------------ weights --
@@ -461,98 +549,170 @@ struct TileKernel {
         Row w;
         w.valid = r < rows;
         const int rr = w.valid ? r : rows - 1, i = p.group.div(rr);
-        w.tok = c.t * TT + i;
+        w.tok = c.tok + i;
         w.head = c.h * p.group.d + rr - i * p.group.d;
         return w;
     }
-    // The row's queries to shared memory; returns the exponent by which they
-    // were scaled (FP8).
-    __device__ __forceinline__ int load_queries(const Piece &c, int half) const
+
+    // A warp's 32 rows of queries: LANES lanes a row, RPI rows an instruction.
+    static constexpr int CH = DP / 8, LANES = CH <= 8 ? 8 : CH <= 16 ? 16 : 32, RPI = 32 / LANES, NI = 32 / RPI;
+
+    // Asynchronous copies of a tile's queries to their place.
+    __device__ __forceinline__ void copy_queries(const Piece &c, int half) const
     {
         const Row w = row_of(c, half);
-        const uint16_t *src = p.q.p + (int64_t)(c.s.first + w.tok) * p.q.ld + w.head * p.q.hs;
-        uint8_t *dst = queries(half);
-        const int r = threadIdx.x & 127;
-        const auto load = [&](int chunk) {
-            if (!w.valid || chunk * 8 >= p.D || !dbg_global(src + chunk * 8, 16, false)) return make_uint4(0, 0, 0, 0);
-            return __ldg(reinterpret_cast<const uint4 *>(src + chunk * 8));
-        };
-        int e = 0;
+        const int64_t mine = (int64_t)(c.s.first + w.tok) * p.q.ld + w.head * p.q.hs;
+        const int lane = threadIdx.x & 31, first = threadIdx.x & 96, chunk = lane % LANES;
+        const uint32_t dst = smem_addr(queries(half));
+#pragma unroll 2
+        for (int i = 0; i < NI; ++i) {
+            const int row = i * RPI + lane / LANES;
+            const int64_t o = __shfl_sync(0xffffffffu, mine, row);
+            const bool ok = __shfl_sync(0xffffffffu, w.valid, row) && chunk * 8 < p.D;
+            if (chunk < CH) copy16(dst + matrix_at(first + row, chunk, 128 * 128), p.q.p + o + chunk * 8, ok);
+        }
+        copy_commit();
+    }
+    // They have arrived (FP8: and become FP16, each thread what it copied).
+    // Returns the exponent by which this lane's row was scaled.
+    __device__ __forceinline__ int queries_here(int half) const
+    {
+        copy_wait<0>();
+        int mine = 0;
         if constexpr (FP8) {
-            float top = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < DP / 8; ++k) {
-                const uint4 v = load(k);
+            const int lane = threadIdx.x & 31, first = threadIdx.x & 96, chunk = lane % LANES;
+            uint8_t *const base_q = queries(half);
+#pragma unroll 2
+            for (int i = 0; i < NI; ++i) {
+                uint8_t *const at = base_q + matrix_at(first + i * RPI + lane / LANES, chunk < CH ? chunk : 0, 128 * 128);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (chunk < CH && dbg_shared(at, 16)) v = *reinterpret_cast<const uint4 *>(at);
+                float top = 0.f;
                 for (const uint32_t x : {v.x, v.y, v.z, v.w}) top = fmaxf(top, fmaxf(fabsf(bf_lo(x)), fabsf(bf_hi(x))));
+#pragma unroll
+                for (int o = 1; o < LANES; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = row_exponent(top), there = __shfl_sync(0xffffffffu, e, (lane % RPI) * LANES);
+                if (lane / RPI == i) mine = there;
+                const auto f16 = [&](uint32_t x) { return pack_f16(scaled(bf_lo(x), e), scaled(bf_hi(x), e)); };
+                if (chunk < CH) put16(at, f16(v.x), f16(v.y), f16(v.z), f16(v.w));
             }
-            e = row_exponent(top);
         }
-#pragma unroll 8
-        for (int k = 0; k < DP / 8; ++k) {
-            uint4 v = load(k);
-            if constexpr (FP8) {
-                const auto half_of = [&](uint32_t x) { return pack_f16(scaled(bf_lo(x), e), scaled(bf_hi(x), e)); };
-                v = make_uint4(half_of(v.x), half_of(v.y), half_of(v.z), half_of(v.w));
-            }
-            put16(dst + matrix_at(r, k, 128 * 128), v.x, v.y, v.z, v.w);
-        }
-        fence_async();
-        bar_arrive(at(&sm.q[half]));
-        return e;
+        ready(&sm.q[half]);
+        return mine;
     }
 
-    __device__ __forceinline__ void weight_loop(Piece c, int half)
+    // Results leave through a place of OUT bytes a row, so that whole rows of it
+    // reach global memory together.  This lane's row there: chunk c.
+    static constexpr int OC = S::OUT / 16;                    // chunks of a row
+    __device__ __forceinline__ uint8_t *out_chunk(int half, int r, int c) const
+    {
+        return base + NT * S::QBYTES + STAGES * S::STAGE + S::RAWS * S::RAW + (half * 128 + r) * S::OUT +
+               ((c ^ (OC == 8 ? r : r >> 1)) & (OC - 1)) * 16;
+    }
+    // ... to global memory: lane l's row to `to`, the first `have` bytes where `ok`.
+    __device__ __forceinline__ void rows_out(int half, uint8_t *to, bool ok, int have) const
+    {
+        const int lane = threadIdx.x & 31, first = threadIdx.x & 96, chunk = lane % OC;
+        __syncwarp();
+#pragma unroll 2
+        for (int i = 0; i < OC; ++i) {
+            const int row = i * (32 / OC) + lane / OC;
+            uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)to, row)) + chunk * 16;
+            const bool in = __shfl_sync(0xffffffffu, ok, row) && chunk * 16 < have;
+            const uint8_t *from = out_chunk(half, first + row, chunk);
+            if (in && dbg_shared(from, 16) && dbg_global(dst, 16, true))
+                *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(from);
+        }
+        __syncwarp();
+    }
+
+    // Bits [lo, hi) of a word.
+    static __device__ __forceinline__ uint32_t bits(int lo, int hi)
+    {
+        const uint32_t up = hi >= 32 ? ~0u : hi <= 0 ? 0u : (1u << hi) - 1u;
+        return lo <= 0 ? up : lo >= 32 ? 0u : up & ~((1u << lo) - 1u);
+    }
+
+    // The next piece that has rows for this half.
+    __device__ __forceinline__ bool next_used(Place &place, Piece &c, int half)
+    {
+        bool any;
+        while ((any = next(place, c)) && !used(c, half)) {}
+        return any;
+    }
+
+    __device__ __forceinline__ void weight_loop(int half)
     {
         const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;       // lane 32 (warp % 4), in bits 16 up
         const float vs = FP8 ? ld_f32_ro(p.scale[1]) : 1.f;
         const float c_all = FP8 ? p.qk_scale * ld_f32_ro(p.scale[0]) : p.qk_scale;
-        bool any = true;
-        while (!used(c, half) && (any = next_piece<BN>(p, TT, c))) {}
+        Place place{0, 0};
+        Piece c, nx;
+        bool any = next_used(place, c, half);
         if (!any) return;
-        int e = load_queries(c, half);
+        copy_queries(c, half);
+        int e = queries_here(half);
         uint32_t cnt = 0;                                     // blocks so far
         bool good = true;
         while (any) {
             const Row row = row_of(c, half);
-            const int hi = key_hi(p, c.s, row.tok), lo = key_lo(p, c.s, row.tok);
             const float scale = FP8 ? scaled(c_all, -e) : c_all;
             float M = -INFINITY;                              // reference, as a raw score
             float L = 0.f;
-            for (int k = c.k; k < c.end && good; ++k, ++cnt) {
+            int hk = key_hi(p, c.s, row.tok) - c.k * BN, lk = key_lo(p, c.s, row.tok) - c.k * BN;    // seen: [lk, hk) of the block
+            bool begun = false, told = false;
+            for (int n = c.end - c.k; n > 0 && good; --n, ++cnt, hk -= BN, lk -= BN) {
                 const int buf = NS == 2 ? cnt & 1 : 0;
                 const uint32_t sc = s_col(half, buf) + lanes;
+                const bool edge = __any_sync(0xffffffffu, hk < BN || lk > 0);
                 good = wait_all(&sm.s[half * NS + buf], NS == 2 ? (cnt >> 1) & 1 : cnt & 1);
                 if (!good) break;
                 tc_fence_after();
-                uint32_t x[BN];
-#pragma unroll
-                for (int i = 0; i < BN / 32; ++i) tmem_ld32(sc + 32 * i, x + 32 * i);
-                tmem_wait_ld();
-                const int hk = hi - k * BN, lk = lo - k * BN;
-                if (__any_sync(0xffffffffu, hk < BN || lk > 0)) {
-#pragma unroll
-                    for (int j = 0; j < BN; ++j)
-                        if (j >= hk || j < lk) x[j] = 0xff800000u;
+                // The last scores are here: the next tile's queries may take the place of these.
+                if (n == 1) {
+                    // (One piece ahead and no further: later ones may wait for what this half still owes.)
+                    any = next(place, nx);
+                    told = true;
+                    if (any && used(nx, half)) copy_queries(nx, half);
                 }
-                float top = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
+                // Scores that the row does not see leave tensor memory as -infinity.
+                if (edge) {
+#pragma unroll 1
+                    for (int i = 0; i < BN / 32; ++i) {
+                        uint32_t x[32];
+                        tmem_ld32(sc + 32 * i, x);
+                        tmem_wait_ld();
+                        const uint32_t see = bits(lk - 32 * i, hk - 32 * i);
 #pragma unroll
-                for (int j = 0; j < BN; j += 8) {
-                    top = fmaxf(top, fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
-                    top1 = fmaxf(top1, fmaxf(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])));
-                    top2 = fmaxf(top2, fmaxf(__uint_as_float(x[j + 4]), __uint_as_float(x[j + 5])));
-                    top3 = fmaxf(top3, fmaxf(__uint_as_float(x[j + 6]), __uint_as_float(x[j + 7])));
+                        for (int j = 0; j < 32; ++j) x[j] = see >> j & 1u ? x[j] : 0xff800000u;
+                        tmem_st32(sc + 32 * i, x);
+                    }
+                    tmem_wait_st();
                 }
-                top = fmaxf(M, fmaxf(fmaxf(top, top1), fmaxf(top2, top3)));
-                // O of the block before is done; it is what a new reference changes.
-                if (cnt > 0) {
+                // The maximum.  Scores are read twice: tensor memory gives 32 columns in a few tens of cycles, and
+                // a block of them held in registers would leave none.
+                float top[4] = {M, M, M, M};
+#pragma unroll
+                for (int i = 0; i < BN / 32; ++i) {
+                    uint32_t x[32];
+                    tmem_ld32(sc + 32 * i, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2)
+                        top[j / 2 % 4] = fmaxf(top[j / 2 % 4], fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
+                }
+                const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // A new reference changes O, the products of the block before done.  (One S: they were issued before
+                // its products, and are done with them.)
+                if (NS == 2 && cnt > 0) {
                     good = wait_all(&sm.o[half], (cnt - 1) & 1);
                     if (!good) break;
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, (top - M) * scale > 8.f || M == -INFINITY)) {
-                    const float keep = M == -INFINITY || top == M ? 1.f : exp2_fast((M - top) * scale);
+                if (__any_sync(0xffffffffu, (most - M) * scale > 8.f || M == -INFINITY)) {
+                    const float keep = M == -INFINITY || most == M ? 1.f : exp2_fast((M - most) * scale);
                     L *= keep;
-                    if (k > c.k && __any_sync(0xffffffffu, keep != 1.f)) {
+                    if (begun && __any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll 1
                         for (int i = 0; i < DP / 32; ++i) {
                             uint32_t y[32];
@@ -564,74 +724,79 @@ struct TileKernel {
                         }
                         tmem_wait_st();
                     }
-                    M = top;
+                    M = most;
                 }
+                begun = true;
                 const float ref = M == -INFINITY ? 0.f : -M * scale;
                 F2 sum = f2(0.f), sum1 = f2(0.f);
+                // The weights of 32 keys take 16 columns: they replace scores that have been read.
 #pragma unroll
                 for (int i = 0; i < BN / 32; ++i) {
-                    uint32_t w[16];
+                    uint32_t x[32], w[16];
+                    tmem_ld32(sc + 32 * i, x);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const F2 a = f2_fma(f2(__uint_as_float(x[32 * i + 2 * j]), __uint_as_float(x[32 * i + 2 * j + 1])), f2(scale),
-                                            f2(ref));
+                        const F2 a = f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2(scale), f2(ref));
                         const F2 b = f2(exp2_fast(a.x), exp2_fast(a.y));
                         if (j & 1) sum1 = f2_add(sum1, b);
                         else sum = f2_add(sum, b);
                         w[j] = FP8 ? pack_f16(b.x, b.y) : pack_bf16(b.x, b.y);
                     }
                     tmem_st16(sc + 16 * i, w);
+                    if (i == BN / 64 - 1) ready_tmem(&sm.w[half * NS + buf][0]);
                 }
                 sum = f2_add(sum, sum1);
                 L += sum.x + sum.y;
-                tmem_wait_st();
-                tc_fence_before();
-                bar_arrive(at(&sm.w[half * NS + buf]));
+                ready_tmem(&sm.w[half * NS + buf][1]);
             }
-            // The scores are read: the next tile's queries may come.
-            Piece nx = c;
-            int e1 = 0;
-            while ((any = next_piece<BN>(p, TT, nx)) && !used(nx, half)) {}
-            if (any && good) e1 = load_queries(nx, half);
+            // A wait that ran out: this half's rows are NaN from here on, as far as pieces are still told.
+            if (!told) any = next(place, nx);
+            const bool copied = any && good && used(nx, half);
+            int e1 = copied ? queries_here(half) : 0;
             if (good) good = wait_all(&sm.o[half], (cnt - 1) & 1);
             tc_fence_after();
             finish(c, half, row, M * scale, L, vs, lanes, good);
-            c = nx;
+            if (any && !used(nx, half)) any = next_used(place, nx, half);
+            if (any && good && !copied) {
+                copy_queries(nx, half);
+                e1 = queries_here(half);
+            }
             e = e1;
+            c = nx;
         }
     }
 
     // A row's result, or part.  good = false: a wait ran out, and the row is NaN.
     __device__ __forceinline__ void finish(const Piece &c, int half, const Row &row, float M, float L, float vs, uint32_t lanes,
-                                           bool good)
+                                           bool good) const
     {
         const int64_t t = c.s.first + row.tok;
-        const bool whole = c.k == c.k0 && c.end == c.k1;
+        const int r = threadIdx.x & 127;
         if (!good) L = NAN;
-        if (whole) {
-            const float inv = L == 0.f ? 0.f : vs / L;
-            uint16_t *out = const_cast<uint16_t *>(p.out.p) + t * p.out.ld + row.head * p.out.hs;
-            bool odd = false;
+        // This code runs once for each tile, from a cold instruction cache: short loops are faster than long ones unrolled.
+        if ((c.flags & (PIECE_BEGINS | PIECE_ENDS)) == (PIECE_BEGINS | PIECE_ENDS)) {
+            constexpr int COLS = S::OUT / 2;                  // of a passage
+            const float inv = vs / L;
+            uint8_t *out = reinterpret_cast<uint8_t *>(const_cast<uint16_t *>(p.out.p) + t * p.out.ld + row.head * p.out.hs);
+            F2 odd = f2(0.f);                                 // NaN: some value is not finite
 #pragma unroll 1
-            for (int i = 0; i < DP / 32; ++i) {
-                uint32_t y[32];
-                tmem_ld32(o_col(half) + lanes + 32 * i, y);
+            for (int n = 0; n < DP / 8; ++n) {
+                uint32_t y[8], z[4];
+                tmem_ld8(o_col(half) + lanes + 8 * n, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    uint32_t z[4];
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const F2 v = f2_mul(f2(__uint_as_float(y[j + 2 * n]), __uint_as_float(y[j + 2 * n + 1])), f2(inv));
-                        odd = odd || (row.valid && (suspect(v.x, L) || suspect(v.y, L)));
-                        z[n] = bf16_f2(v);
-                    }
-                    if (row.valid && 32 * i + j < p.D) st_u32x4(out + 32 * i + j, z[0], z[1], z[2], z[3]);
+                for (int j = 0; j < 4; ++j) {
+                    F2 v = f2_mul(f2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), f2(inv));
+                    if (L == 0.f) v = f2(0.f);                // whatever 0 times the values was
+                    odd = f2_fma(v, f2(0.f), odd);
+                    z[j] = bf16_f2(v);
                 }
+                put16(out_chunk(half, r, n % OC), z[0], z[1], z[2], z[3]);
+                if (n % OC == OC - 1) rows_out(half, out + n / OC * S::OUT, row.valid, p.D * 2 - n / OC * S::OUT);
             }
             if (row.valid && p.lse) st_f32(p.lse + t * p.out.H + row.head, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
-            uint32_t again = __ballot_sync(0xffffffffu, odd);
-            __syncwarp();
+            uint32_t again = __ballot_sync(0xffffffffu, row.valid && !(odd.x == 0.f && odd.y == 0.f) && L > 0.f && L < INFINITY);
             while (again) {
                 const int l = __ffs(again) - 1;
                 again &= again - 1;
@@ -639,23 +804,20 @@ struct TileKernel {
                                           false);
             }
         } else {
-            float *part = part_of(p.ws, blockIdx.x, c.k == c.k0, S::ROWS, DP);
-            const int r = half * 128 + (threadIdx.x & 127);
+            float *part = part_of(p.ws, blockIdx.x, c.flags & PIECE_BEGINS, S::ROWS, DP);
             if (row.valid) {
-                st_f32(part + 2 * r, good ? M : 0.f);
-                st_f32(part + 2 * r + 1, L);
+                st_f32(part + 2 * (half * 128 + r), good ? M : 0.f);
+                st_f32(part + 2 * (half * 128 + r) + 1, L);
             }
-            part += 2 * S::ROWS + (int64_t)r * DP;
+            part += 2 * S::ROWS + (int64_t)(half * 128 + r) * DP;
 #pragma unroll 1
-            for (int i = 0; i < DP / 32; ++i) {
-                uint32_t y[32];
-                tmem_ld32(o_col(half) + lanes + 32 * i, y);
+            for (int n = 0; n < DP / 8; ++n) {
+                uint32_t y[8];
+                tmem_ld8(o_col(half) + lanes + 8 * n, y);
                 tmem_wait_ld();
-                if (row.valid)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        st_f32x4(part + 32 * i + j, __uint_as_float(y[j]), __uint_as_float(y[j + 1]), __uint_as_float(y[j + 2]),
-                                 __uint_as_float(y[j + 3]));
+                put16(out_chunk(half, r, 2 * n % OC), y[0], y[1], y[2], y[3]);
+                put16(out_chunk(half, r, (2 * n + 1) % OC), y[4], y[5], y[6], y[7]);
+                if (2 * n % OC == OC - 2) rows_out(half, reinterpret_cast<uint8_t *>(part) + 2 * n / OC * S::OUT, row.valid, S::OUT);
             }
         }
         tc_fence_before();
@@ -665,45 +827,85 @@ struct TileKernel {
     __device__ __forceinline__ void go()
     {
         const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+        // What needs no input, before the kernel ahead has ended.
+        if (tid == 0) {
+            for (int i = 0; i < STAGES; ++i) {
+                bar_init(at(&sm.full[i]), 4);
+                bar_init(at(&sm.empty[i]), 1);
+                bar_init(at(&sm.landed[i]), 128);
+            }
+            for (int i = 0; i < NT; ++i) {
+                bar_init(at(&sm.q[i]), 4);
+                bar_init(at(&sm.o[i]), 1);
+            }
+            for (int i = 0; i < NT * NS; ++i) {
+                bar_init(at(&sm.s[i]), 1);
+                bar_init(at(&sm.w[i][0]), 4);
+                bar_init(at(&sm.w[i][1]), 4);
+            }
+            for (int i = 0; i < kPieces; ++i) {
+                bar_init(at(&sm.told[i]), 1);
+                bar_init(at(&sm.heard[i]), 4 * NT + 5);
+            }
+            bar_init(at(&sm.last), 1);
+            sm.failed = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        if (warp == 12) tmem_alloc(smem_addr(&sm.tmem), kTileColumns);
+        tc_fence_before();
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
         TT = S::ROWS / p.group.d;
         const Work work = share_work<kTileThreads>(
             p.B, p.Hk, sm.scratch,
             [&](int b, int64_t &u, int64_t &t) {
                 const Seq s = sequence(p, b);
                 const int nt = (s.n + TT - 1) / TT;
-                u = blocks_before<BN>(p, s, TT, nt, nt);
+                u = blocks_before<BN>(p, s, TT, nt, nt) + (int64_t)nt * kTileCost;
                 t = nt;
             },
-            // A CTA for each tile; tiles are shared out further while that leaves a CTA four blocks.
+            // A CTA for each tile; tiles are shared out further while that leaves a CTA four units (more than
+            // kTileCost: every CTA has a block).
             [&](int64_t units, int64_t tiles) { return (int)min((int64_t)gridDim.x, max(tiles, units / 4)); });
-        if ((int)blockIdx.x >= work.ctas) {
-            if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
-            return;
-        }
-        Piece c;
+        tc_fence_after();                                     // (share_work has met at barriers)
+        tmem = uniform(sm.tmem);
+        if ((int)blockIdx.x < work.ctas) run_work(work, warp, lane);
+        else if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 12) tmem_free(tmem, kTileColumns);
+    }
+
+    __device__ __forceinline__ void run_work(const Work &work, int warp, int lane)
+    {
+        Walk c;
         c.b = work.b;
         c.s = sequence(p, c.b);
         c.nt = (c.s.n + TT - 1) / TT;
-        const int64_t whole = blocks_before<BN>(p, c.s, TT, c.nt, c.nt);
-        c.h = (int)(work.rest / whole);
+        const auto units_before = [&](int t) { return blocks_before<BN>(p, c.s, TT, c.nt, t) + (int64_t)t * kTileCost; };
+        const int64_t whole = units_before(c.nt);
+        c.h = (int)quotient(work.rest, whole);
         const int64_t rest = work.rest - c.h * whole;
-        // The tile of block `rest`: the last with blocks_before(t) <= rest, 32 places at a time.
+        // The tile of unit `rest`: the last with units_before(t) <= rest, 32 places at a time.
         int lo = 0, hi = c.nt;
         while (hi - lo > 1) {
             const int by = (hi - lo + 31) / 32, t = lo + lane * by;
-            const bool before = t < hi && blocks_before<BN>(p, c.s, TT, c.nt, t) <= rest;
+            const bool before = t < hi && units_before(t) <= rest;
             const int n = __popc(__ballot_sync(0xffffffffu, before)) - 1;
             lo += n * by;
             hi = min(hi, lo + by);
         }
         c.t = lo;
         tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
-        c.k = c.k0 + (int)(rest - blocks_before<BN>(p, c.s, TT, c.nt, c.t));
-        c.left = work.u1 - work.u0;
-        piece_ends<BN>(c);
-        if (tid == 0) {
+        const int in = (int)(rest - units_before(c.t)) - kTileCost;      // blocks before u0, or less than none
+        c.k = c.k0 + max(in, 0);
+        c.left = work.u1 - work.u0 + min(in, 0);
+        walk_end(c);
+        __syncthreads();                                      // the scratch becomes pieces
+        if (threadIdx.x == 0) {
             AttnHeader hd{};
-            hd.first = work.u0 - (c.k - c.k0);
+            hd.first = work.u0 - in;                          // the tile's first block
             hd.last = hd.first + (c.k1 - c.k0);
             hd.units = work.units;
             hd.ctas = work.ctas;
@@ -713,51 +915,29 @@ struct TileKernel {
             hd.tok = c.s.first + c.t * TT;
             hd.ntok = min(TT, c.s.n - c.t * TT);
             st_header(p.ws, blockIdx.x, hd);
-            for (int i = 0; i < STAGES; ++i) {
-                bar_init(at(&sm.full[i]), 128);
-                bar_init(at(&sm.empty[i]), 1);
-            }
-            for (int i = 0; i < NT; ++i) {
-                bar_init(at(&sm.q[i]), 128);
-                bar_init(at(&sm.o[i]), 1);
-            }
-            for (int i = 0; i < NT * NS; ++i) {
-                bar_init(at(&sm.s[i]), 1);
-                bar_init(at(&sm.w[i]), 128);
-            }
-            bar_init(at(&sm.last), 1);
-            sm.failed = 0;
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-        if (warp == 12) tmem_alloc(smem_addr(&sm.tmem), kTileColumns);
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        tmem = sm.tmem;
+        __syncwarp();
         if (warp < 8) {
             more_registers<kWeightRegs>();
-            if (warp < 4 * NT) weight_loop(c, warp >> 2);
+            if (warp < 4 * NT) weight_loop(warp >> 2);
         } else {
             fewer_registers<kOtherRegs>();
             if (warp < 12) {
-                if constexpr (FP8) convert_loop(c);
-                else copy_loop(c);
+                if constexpr (FP8) convert_loop();
+                else copy_loop();
                 copy_wait<0>();
             } else if (warp == 12) {
-                if (lane == 0) {
-                    issue_loop(c);
-                    if (sm.failed) {                          // products in flight end before their memory goes
-                        products_done(at(&sm.last));
-                        for (int i = 0; i < kWaitTries && !bar_try(at(&sm.last), 0); ++i) {}
-                    }
+                issue_loop();
+                __syncwarp();
+                if (sm.failed && lane == 0) {                 // products in flight end before their memory goes
+                    products_done(at(&sm.last));
+                    for (int i = 0; i < kWaitTries && !bar_try(at(&sm.last), 0); ++i) {}
                 }
                 __syncwarp();
+            } else if (warp == 13) {
+                tell_loop(c);
             }
         }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (warp == 12) tmem_free(tmem, kTileColumns);
     }
 };
 
@@ -767,8 +947,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const __grid_cons
     extern __shared__ __align__(1024) uint8_t tile_smem[];
     __shared__ typename TileKernel<KIND, DP>::Shared sm;
     CRMSN_DEBUG_ENTER(p.dbg);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;");
     uint8_t *const base = tile_smem + (1024 - (smem_addr(tile_smem) & 1023)) % 1024;
     TileKernel<KIND, DP> k{p, sm, base, 0, 0};
     k.go();

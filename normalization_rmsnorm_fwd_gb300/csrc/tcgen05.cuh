@@ -23,6 +23,19 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
                  : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done;
 }
+// The same without lingering.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done;
+}
+// The barrier receives an arrival when this thread's copies so far have landed.
+__device__ __forceinline__ void bar_arrive_copies(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
 // Waits for the phase of that parity, at most kWaitTries tries (seconds).
 // False: it, or another wait of the CTA (*failed), ran out.
 constexpr int kWaitTries = 1 << 22;
@@ -36,6 +49,19 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     *failed = 1;
     return false;
 }
+// True for one lane of a warp that is together.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one;
+}
+// Lane 0's value, which the compiler then knows to be the warp's: products take
+// their operands from uniform registers, and values that may differ between
+// lanes cost a slow move each (a block's 16 products 1500 cycles to issue
+// instead of the 1024 that they run).
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
 // What this thread wrote to shared memory becomes visible to the tensor cores
 // (with the arrival that follows).
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -68,6 +94,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t *r)
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t *r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(at));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r)
 {
     asm volatile(
@@ -95,11 +126,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r)
 // columns to the next, for operands whose columns are the product's M or N
 // dimension; operands whose columns are summed over are addressed block by
 // block.
-__device__ __forceinline__ uint64_t matrix_desc(uint32_t at, uint32_t block)
+// A descriptor's upper half is the same for all; its lower half counts 16 bytes,
+// so that another place in the matrix is a sum.
+constexpr uint32_t kMatrixHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t matrix_low(uint32_t at, uint32_t block)
 {
-    return (uint64_t)((at & 0x3ffffu) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
+    return ((at & 0x3ffffu) >> 4) | ((block >> 4) << 16);
 }
+__device__ __forceinline__ uint64_t matrix_desc(uint32_t low) { return ((uint64_t)kMatrixHigh << 32) | low; }
 // Where chunk c (16 bytes) of row r of such a matrix lies, `block` as above.
 __device__ __forceinline__ uint32_t matrix_at(int r, int c, uint32_t block)
 {

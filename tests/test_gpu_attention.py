@@ -262,6 +262,19 @@ def test_rows_without_keys(n, dtype):
     check_paged(gen(n), [n, 0, n, n], lens, 4, 2, 128, dtype=dtype, starts=True, window=2)
 
 
+@pytest.mark.parametrize("n", [4, 60])
+@pytest.mark.parametrize("bad", [INF, NAN])
+def test_rows_without_keys_beside_infinite_values(n, bad):
+    # The first rows see nothing; what the others see does not reach them.
+    g = gen(n)
+    for m, lens in ((n // 2, [n // 2]), (n // 2, [n // 2, 5000])):
+        kc, vc, table, _, _ = cache(g, lens, 16, 2, 128)
+        vc[int(table[0, 0]), 0] = bad
+        q = normal(g, len(lens) * n, 8, 128).to(BF16)
+        out = crm.paged_attention(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+        assert (out[:n - m] == 0).all() and not out[n - m:n].isfinite().any()
+
+
 def test_no_pages():
     q = normal(gen(1), 3, 4, 128).to(BF16)
     kc = torch.empty(0, 16, 2, 128, dtype=BF16, device=DEV)
