@@ -45,12 +45,10 @@ struct TileShape {
     static constexpr int ROWS = NT * 128;
     static constexpr int QBYTES = 128 * DP * 2;              // queries of a half
     static constexpr int STAGE = BN * DP * 2;                // keys or values of a block
-    static constexpr int STAGES = DP == 64 ? (FP8 ? 5 : 8) : (FP8 ? 3 : 4);
+    static constexpr int STAGES = DP == 64 ? (FP8 ? 5 : 8) : (FP8 ? 3 : 5);
     static constexpr int RAW = FP8 ? BN * DP : 0;            // FP8 codes of a block
-    static constexpr int RAWS = FP8 ? (DP == 64 ? 8 : 3) : 0;
-    // Bytes of a row that its result passes through on its way out.
-    static constexpr int OUT = FP8 && (DP == 128 || DP == 192) ? 64 : 128;
-    static constexpr int SMEM = 1024 + NT * QBYTES + STAGES * STAGE + RAWS * RAW + NT * 128 * OUT;
+    static constexpr int RAWS = FP8 ? (DP == 64 ? 8 : 4) : 0;
+    static constexpr int SMEM = 1024 + NT * QBYTES + STAGES * STAGE + RAWS * RAW;
     static constexpr int OCOL = DP == 256 ? 256 : NT * NS * BN;   // columns of S, then of O
     static_assert(OCOL + NT * DP <= 512, "tensor memory");
     static_assert(SMEM + 1600 <= 227 * 1024, "shared memory");
@@ -96,28 +94,29 @@ __device__ __forceinline__ void tile_blocks(const AttnParams &p, const Seq &s, i
     k0 = key_lo(p, s, t * TT) / BN;
     k1 = max((key_hi(p, s, last) + BN - 1) / BN, k0 + 1);
 }
-// Blocks of the first t of a sequence's nt tiles, in closed form.
-template <int BN>
-__device__ __forceinline__ int64_t blocks_before(const AttnParams &p, const Seq &s, int TT, int nt, int t)
+// Blocks of BN keys of the first t of a sequence's nt tiles, in closed form.
+// (Not inlined: it is called four times, and the start of a small call is the
+// time that its code takes to arrive.)
+static __device__ __noinline__ int64_t blocks_before(int BN, int n, int m, int causal, int window, int TT, int nt, int t)
 {
     if (t <= 0) return 0;
-    if (!p.causal) return (int64_t)t * max((s.m + BN - 1) / BN, 1);
+    const int all = (m + BN - 1) / BN;
+    if (!causal) return (int64_t)t * max(all, 1);
+    const int64_t off = (int64_t)m - n;
     int64_t sum = 0;
-    if (t == nt) {                   // the last tile may be short
-        int k0, k1;
-        tile_blocks<BN>(p, s, TT, nt - 1, k0, k1);
-        sum = k1 - k0;
-        --t;
-    }
-    const int64_t off = (int64_t)s.m - s.n;
+    const bool last = t == nt;       // that tile may be short: its keys end with the sequence's
+    if (last) --t;
     // Tiles whose tokens all stand before the first key: one block each.
-    const int64_t z = off < 0 ? min(-off / TT, (int64_t)t) : 0;
-    sum += z;
-    sum += floor_sum(t - z, BN, TT, off + (z + 1) * TT + BN - 1);
-    if (p.window) {
-        const int64_t gap = p.window - 1 - off;      // first tiles whose window reaches the first key
-        const int64_t y = max(z, gap > 0 ? (gap + TT - 1) / TT : (int64_t)0);
-        if (y < t) sum -= floor_sum(t - y, BN, TT, off + 1 - p.window + y * TT);
+    const int64_t z = off < 0 ? min(quotient(-off, TT), (int64_t)t) : 0;
+    sum += z + floor_sum(t - z, BN, TT, off + (z + 1) * TT + BN - 1);
+    const int64_t gap = window - 1 - off;            // the first tiles' windows reach the first key
+    if (window) {
+        const int64_t y = max(z, gap > 0 ? quotient(gap + TT - 1, TT) : (int64_t)0);
+        if (y < t) sum -= floor_sum(t - y, BN, TT, off + 1 - window + y * TT);
+    }
+    if (last) {
+        const int64_t lo = window ? max(off + (int64_t)t * TT + 1 - window, (int64_t)0) : 0, k0 = quotient(lo, BN);
+        sum += max((int64_t)all, k0 + 1) - k0;
     }
     return sum;
 }
@@ -182,7 +181,7 @@ struct TileKernel {
 
     const AttnParams &p;
     Shared &sm;
-    uint8_t *const base;             // queries, stages, codes, results
+    uint8_t *const base;             // queries, stages, codes
     uint32_t tmem;
     int TT;
 
@@ -564,7 +563,7 @@ struct TileKernel {
         const int64_t mine = (int64_t)(c.s.first + w.tok) * p.q.ld + w.head * p.q.hs;
         const int lane = threadIdx.x & 31, first = threadIdx.x & 96, chunk = lane % LANES;
         const uint32_t dst = smem_addr(queries(half));
-#pragma unroll 2
+#pragma unroll 8
         for (int i = 0; i < NI; ++i) {
             const int row = i * RPI + lane / LANES;
             const int64_t o = __shfl_sync(0xffffffffu, mine, row);
@@ -601,29 +600,24 @@ struct TileKernel {
         return mine;
     }
 
-    // Results leave through a place of OUT bytes a row, so that whole rows of it
-    // reach global memory together.  This lane's row there: chunk c.
-    static constexpr int OC = S::OUT / 16;                    // chunks of a row
-    __device__ __forceinline__ uint8_t *out_chunk(int half, int r, int c) const
+    // Four lanes, a row each of four chunks (w: 4 words a chunk), exchange them
+    // in two butterfly steps: lane l gets chunk l & 3 of the four rows.  So four
+    // lanes store 64 bytes of a row together: stores of a row a lane occupy the
+    // memory pipe for 32 lines each, four times as long.
+    static __device__ __forceinline__ void turn_quads(uint32_t (&w)[16])
     {
-        return base + NT * S::QBYTES + STAGES * S::STAGE + S::RAWS * S::RAW + (half * 128 + r) * S::OUT +
-               ((c ^ (OC == 8 ? r : r >> 1)) & (OC - 1)) * 16;
-    }
-    // ... to global memory: lane l's row to `to`, the first `have` bytes where `ok`.
-    __device__ __forceinline__ void rows_out(int half, uint8_t *to, bool ok, int have) const
-    {
-        const int lane = threadIdx.x & 31, first = threadIdx.x & 96, chunk = lane % OC;
-        __syncwarp();
-#pragma unroll 2
-        for (int i = 0; i < OC; ++i) {
-            const int row = i * (32 / OC) + lane / OC;
-            uint8_t *dst = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)to, row)) + chunk * 16;
-            const bool in = __shfl_sync(0xffffffffu, ok, row) && chunk * 16 < have;
-            const uint8_t *from = out_chunk(half, first + row, chunk);
-            if (in && dbg_shared(from, 16) && dbg_global(dst, 16, true))
-                *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(from);
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int step = 1; step < 4; step *= 2) {
+            const bool up = lane & step;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int a = step == 1 ? i / 4 * 8 + i % 4 : i, b = a + 4 * step;    // chunks 0, 1 and 2, 3; then 0, 2 and 1, 3
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[a] : w[b], step);
+                if (up) w[a] = got;
+                else w[b] = got;
+            }
         }
-        __syncwarp();
     }
 
     // Bits [lo, hi) of a word.
@@ -633,14 +627,6 @@ struct TileKernel {
         return lo <= 0 ? up : lo >= 32 ? 0u : up & ~((1u << lo) - 1u);
     }
 
-    // The next piece that has rows for this half.
-    __device__ __forceinline__ bool next_used(Place &place, Piece &c, int half)
-    {
-        bool any;
-        while ((any = next(place, c)) && !used(c, half)) {}
-        return any;
-    }
-
     __device__ __forceinline__ void weight_loop(int half)
     {
         const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;       // lane 32 (warp % 4), in bits 16 up
@@ -648,17 +634,31 @@ struct TileKernel {
         const float c_all = FP8 ? p.qk_scale * ld_f32_ro(p.scale[0]) : p.qk_scale;
         Place place{0, 0};
         Piece c, nx;
-        bool any = next_used(place, c, half);
-        if (!any) return;
-        copy_queries(c, half);
-        int e = queries_here(half);
+        bool any = next(place, nx), have = false, copied = false, good = true;
+        Row row;
+        int e = 0;
+        float scale = 0.f, M = 0.f, L = 0.f;                  // M: the reference, a raw score
         uint32_t cnt = 0;                                     // blocks so far
-        bool good = true;
-        while (any) {
-            const Row row = row_of(c, half);
-            const float scale = FP8 ? scaled(c_all, -e) : c_all;
-            float M = -INFINITY;                              // reference, as a raw score
-            float L = 0.f;
+        for (;;) {
+            // The next tile's queries first (its scores are worked out meanwhile), then this one's results.
+            while (any && !used(nx, half)) any = next(place, nx);
+            if (any && good) {
+                if (!copied) copy_queries(nx, half);
+                e = queries_here(half);
+            }
+            if (have) {
+                if (good) good = wait_all(&sm.o[half], (cnt - 1) & 1);
+                tc_fence_after();
+                finish(c, half, row, M * scale, L, vs, lanes, good);
+            }
+            if (!any) return;
+            c = nx;
+            have = true;
+            copied = false;
+            row = row_of(c, half);
+            scale = FP8 ? scaled(c_all, -e) : c_all;
+            M = -INFINITY;
+            L = 0.f;
             int hk = key_hi(p, c.s, row.tok) - c.k * BN, lk = key_lo(p, c.s, row.tok) - c.k * BN;    // seen: [lk, hk) of the block
             bool begun = false, told = false;
             for (int n = c.end - c.k; n > 0 && good; --n, ++cnt, hk -= BN, lk -= BN) {
@@ -673,13 +673,15 @@ struct TileKernel {
                     // (One piece ahead and no further: later ones may wait for what this half still owes.)
                     any = next(place, nx);
                     told = true;
-                    if (any && used(nx, half)) copy_queries(nx, half);
+                    copied = any && used(nx, half);
+                    if (copied) copy_queries(nx, half);
                 }
                 // Scores that the row does not see leave tensor memory as -infinity.
                 if (edge) {
 #pragma unroll 1
                     for (int i = 0; i < BN / 32; ++i) {
                         uint32_t x[32];
+                        if (__all_sync(0xffffffffu, hk >= 32 * i + 32 && lk <= 32 * i)) continue;
                         tmem_ld32(sc + 32 * i, x);
                         tmem_wait_ld();
                         const uint32_t see = bits(lk - 32 * i, hk - 32 * i);
@@ -693,12 +695,13 @@ struct TileKernel {
                 // a block of them held in registers would leave none.
                 float top[4] = {M, M, M, M};
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    uint32_t x[32];
-                    tmem_ld32(sc + 32 * i, x);
+                for (int i = 0; i < BN / 64; ++i) {
+                    uint32_t x[64];
+                    tmem_ld32(sc + 64 * i, x);
+                    tmem_ld32(sc + 64 * i + 32, x + 32);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2)
+                    for (int j = 0; j < 64; j += 2)
                         top[j / 2 % 4] = fmaxf(top[j / 2 % 4], fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
                 }
                 const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
@@ -729,15 +732,19 @@ struct TileKernel {
                 begun = true;
                 const float ref = M == -INFINITY ? 0.f : -M * scale;
                 F2 sum = f2(0.f), sum1 = f2(0.f);
-                // The weights of 32 keys take 16 columns: they replace scores that have been read.
+                // The weights of 32 keys take 16 columns: they replace scores that have been read.  The next 32 scores
+                // are on their way meanwhile.
+                uint32_t x[2][32];
+                tmem_ld32(sc, x[0]);
 #pragma unroll
                 for (int i = 0; i < BN / 32; ++i) {
-                    uint32_t x[32], w[16];
-                    tmem_ld32(sc + 32 * i, x);
+                    uint32_t w[16];
                     tmem_wait_ld();
+                    if (i + 1 < BN / 32) tmem_ld32(sc + 32 * (i + 1), x[(i + 1) & 1]);
+                    const uint32_t *y = x[i & 1];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const F2 a = f2_fma(f2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), f2(scale), f2(ref));
+                        const F2 a = f2_fma(f2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), f2(scale), f2(ref));
                         const F2 b = f2(exp2_fast(a.x), exp2_fast(a.y));
                         if (j & 1) sum1 = f2_add(sum1, b);
                         else sum = f2_add(sum, b);
@@ -752,18 +759,6 @@ struct TileKernel {
             }
             // A wait that ran out: this half's rows are NaN from here on, as far as pieces are still told.
             if (!told) any = next(place, nx);
-            const bool copied = any && good && used(nx, half);
-            int e1 = copied ? queries_here(half) : 0;
-            if (good) good = wait_all(&sm.o[half], (cnt - 1) & 1);
-            tc_fence_after();
-            finish(c, half, row, M * scale, L, vs, lanes, good);
-            if (any && !used(nx, half)) any = next_used(place, nx, half);
-            if (any && good && !copied) {
-                copy_queries(nx, half);
-                e1 = queries_here(half);
-            }
-            e = e1;
-            c = nx;
         }
     }
 
@@ -774,51 +769,62 @@ struct TileKernel {
         const int64_t t = c.s.first + row.tok;
         const int r = threadIdx.x & 127;
         if (!good) L = NAN;
-        // This code runs once for each tile, from a cold instruction cache: short loops are faster than long ones unrolled.
-        if ((c.flags & (PIECE_BEGINS | PIECE_ENDS)) == (PIECE_BEGINS | PIECE_ENDS)) {
-            constexpr int COLS = S::OUT / 2;                  // of a passage
-            const float inv = vs / L;
-            uint8_t *out = reinterpret_cast<uint8_t *>(const_cast<uint16_t *>(p.out.p) + t * p.out.ld + row.head * p.out.hs);
-            F2 odd = f2(0.f);                                 // NaN: some value is not finite
-#pragma unroll 1
-            for (int n = 0; n < DP / 8; ++n) {
-                uint32_t y[8], z[4];
-                tmem_ld8(o_col(half) + lanes + 8 * n, y);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    F2 v = f2_mul(f2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1])), f2(inv));
-                    if (L == 0.f) v = f2(0.f);                // whatever 0 times the values was
-                    odd = f2_fma(v, f2(0.f), odd);
-                    z[j] = bf16_f2(v);
-                }
-                put16(out_chunk(half, r, n % OC), z[0], z[1], z[2], z[3]);
-                if (n % OC == OC - 1) rows_out(half, out + n / OC * S::OUT, row.valid, p.D * 2 - n / OC * S::OUT);
-            }
+        // This code runs once for each tile, from a cold instruction cache: a short loop is faster than a long one
+        // unrolled.  16 columns at a time are two chunks of a result, four of a part.
+        const bool whole = (c.flags & (PIECE_BEGINS | PIECE_ENDS)) == (PIECE_BEGINS | PIECE_ENDS);
+        const float inv = vs / L;
+        F2 odd = f2(0.f);                                     // NaN: some value is not finite
+        uint8_t *to;
+        int have = DP * 4;
+        if (whole) {
+            to = reinterpret_cast<uint8_t *>(const_cast<uint16_t *>(p.out.p) + t * p.out.ld + row.head * p.out.hs);
+            have = p.D * 2;
             if (row.valid && p.lse) st_f32(p.lse + t * p.out.H + row.head, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
-            uint32_t again = __ballot_sync(0xffffffffu, row.valid && !(odd.x == 0.f && odd.y == 0.f) && L > 0.f && L < INFINITY);
-            while (again) {
-                const int l = __ffs(again) - 1;
-                again &= again - 1;
-                attend_row<KIND, DP / 32>(p, c.b, c.s, __shfl_sync(0xffffffffu, row.tok, l), __shfl_sync(0xffffffffu, row.head, l),
-                                          false);
-            }
         } else {
             float *part = part_of(p.ws, blockIdx.x, c.flags & PIECE_BEGINS, S::ROWS, DP);
             if (row.valid) {
                 st_f32(part + 2 * (half * 128 + r), good ? M : 0.f);
                 st_f32(part + 2 * (half * 128 + r) + 1, L);
             }
-            part += 2 * S::ROWS + (int64_t)(half * 128 + r) * DP;
+            to = reinterpret_cast<uint8_t *>(part + 2 * S::ROWS + (int64_t)(half * 128 + r) * DP);
+        }
+        // 64 bytes of the four rows of this lane's quad at a time.
+        uint8_t *quad[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            quad[j] = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)(row.valid ? to : nullptr), (r & 28) + j));
+        int done = (r & 3) * 16;                              // this lane's first byte of them
 #pragma unroll 1
-            for (int n = 0; n < DP / 8; ++n) {
-                uint32_t y[8];
-                tmem_ld8(o_col(half) + lanes + 8 * n, y);
+        for (int n = 0; n < DP / 16; ++n, done += 64) {
+            uint32_t w[16];
+            tmem_ld16(o_col(half) + lanes + 16 * n, w);
+            tmem_wait_ld();
+            if (whole) {
+                // The next 16 columns too: 32 results.
+                uint32_t y[16];
+                tmem_ld16(o_col(half) + lanes + 16 * ++n, y);
                 tmem_wait_ld();
-                put16(out_chunk(half, r, 2 * n % OC), y[0], y[1], y[2], y[3]);
-                put16(out_chunk(half, r, (2 * n + 1) % OC), y[4], y[5], y[6], y[7]);
-                if (2 * n % OC == OC - 2) rows_out(half, reinterpret_cast<uint8_t *>(part) + 2 * n / OC * S::OUT, row.valid, S::OUT);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t *x = j < 8 ? w + 2 * j : y + 2 * (j - 8);
+                    F2 v = f2_mul(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), f2(inv));
+                    if (L == 0.f) v = f2(0.f);                // whatever 0 times the values was
+                    odd = f2_fma(v, f2(0.f), odd);
+                    w[j] = bf16_f2(v);
+                }
             }
+            turn_quads(w);
+            if (done < have)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (quad[j] && dbg_global(quad[j] + done, 16, true))
+                        *reinterpret_cast<uint4 *>(quad[j] + done) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+        uint32_t again = __ballot_sync(0xffffffffu, whole && row.valid && !(odd.x == 0.f && odd.y == 0.f) && L > 0.f && L < INFINITY);
+        while (again) {
+            const int l = __ffs(again) - 1;
+            again &= again - 1;
+            attend_row<KIND, DP / 32>(p, c.b, c.s, __shfl_sync(0xffffffffu, row.tok, l), __shfl_sync(0xffffffffu, row.head, l), false);
         }
         tc_fence_before();
     }
@@ -861,7 +867,7 @@ struct TileKernel {
             [&](int b, int64_t &u, int64_t &t) {
                 const Seq s = sequence(p, b);
                 const int nt = (s.n + TT - 1) / TT;
-                u = blocks_before<BN>(p, s, TT, nt, nt) + (int64_t)nt * kTileCost;
+                u = blocks_before(BN, s.n, s.m, p.causal, p.window, TT, nt, nt) + (int64_t)nt * kTileCost;
                 t = nt;
             },
             // A CTA for each tile; tiles are shared out further while that leaves a CTA four units (more than
@@ -883,7 +889,9 @@ struct TileKernel {
         c.b = work.b;
         c.s = sequence(p, c.b);
         c.nt = (c.s.n + TT - 1) / TT;
-        const auto units_before = [&](int t) { return blocks_before<BN>(p, c.s, TT, c.nt, t) + (int64_t)t * kTileCost; };
+        const auto units_before = [&](int t) {
+            return blocks_before(BN, c.s.n, c.s.m, p.causal, p.window, TT, c.nt, t) + (int64_t)t * kTileCost;
+        };
         const int64_t whole = units_before(c.nt);
         c.h = (int)quotient(work.rest, whole);
         const int64_t rest = work.rest - c.h * whole;
