@@ -106,6 +106,8 @@ enum { CRMSN_CACHE_BF16 = 0, CRMSN_CACHE_E4M3 = 1, CRMSN_CACHE_E5M2 = 2 };
 #define CRMSN_MAX_H 16384
 /* Largest supported head size of the query / key functions. */
 #define CRMSN_MAX_HEAD_DIM 512
+/* Keys of a sequence up to which the attention functions need no workspace. */
+#define CRMSN_ATTENTION_SHORT 640
 
 /*
  * rmsnorm_fwd -- [API] rmsnorm, gemma_rmsnorm, fused_add_rmsnorm,
@@ -566,7 +568,9 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     multiple of 8 elements (FP8 caches: 16) and every base 16-byte aligned.
  *   - workspace: at least attention_workspace_bytes(D, device) bytes, 256-byte
  *     aligned, any content; scratch that a later call on the same stream may
- *     use again (two calls that may run at the same time need two).
+ *     use again (two calls that may run at the same time need two).  Not used,
+ *     and may be NULL, where starts is NULL and no sequence can have more than
+ *     CRMSN_ATTENTION_SHORT keys (T / B; table_pages * page_size).
  *   - The outputs may not overlap any input.
  *   - The order of the sums of a row depends on the lengths of all sequences
  *     of the call and on the SM count, and on nothing else.

@@ -76,6 +76,7 @@ CACHE_BF16, CACHE_E4M3, CACHE_E5M2 = 0, 1, 2
 OUT_BF16, OUT_E4M3 = 0, 1
 MAX_H = 16384
 MAX_HEAD_DIM = 512
+ATTENTION_SHORT = 640
 
 _lock = threading.Lock()
 _lib = None

@@ -766,9 +766,9 @@ def _int32_vector(t, name, n, dev):
     return t.data_ptr()
 
 
-def _attention(q, shape, T, Hq, D, Hk, B, dev, starts, scale, causal, window, out, lse, workspace):
-    """(out, the packed fields of crmsn_attention): what the two attention
-    functions share."""
+def _attention(q, shape, T, Hq, D, Hk, B, keys, dev, starts, scale, causal, window, out, lse, workspace):
+    """(out, workspace, the fields of crmsn_attention): what the two attention
+    functions share.  keys: the most that a sequence can have, without starts."""
     qp = _head_tensor(q, "q", dev, shape)
     if Hk < 1 or Hq % Hk:
         raise ValueError(f"{Hq} query heads are no multiple of {Hk} key heads")
@@ -781,15 +781,17 @@ def _attention(q, shape, T, Hq, D, Hk, B, dev, starts, scale, causal, window, ou
         if lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != shape[:-1] or not lse.is_contiguous():
             raise ValueError(f"lse must be a contiguous float32 {tuple(shape[:-1])} tensor on cuda:{dev}")
         lp = lse.data_ptr()
-    if workspace is None:
+    wsp = wsn = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+        wsp, wsn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif starts is not None or keys > _abi.ATTENTION_SHORT:
         wsn = _lib().attention_workspace_bytes(D, dev)
         workspace = torch.empty(wsn, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
-    else:
-        wsn = workspace.numel() * workspace.element_size()
+        wsp = workspace.data_ptr()
     return out, workspace, (T, D, Hq, Hk, B, *qp, *op, lp, 0 if starts is None else _int32_vector(starts, "starts", B + 1, dev),
-                            D ** -0.5 if scale is None else scale, bool(causal), window, workspace.data_ptr(), wsn)
+                            D ** -0.5 if scale is None else scale, bool(causal), window, wsp, wsn)
 
 
 def prompt_attention(q, k, v, starts=None, scale=None, causal: bool = True, window: int = 0, out=None, lse=None,
@@ -813,7 +815,7 @@ def prompt_attention(q, k, v, starts=None, scale=None, causal: bool = True, wind
         B = starts.shape[0] - 1
     else:
         B = 1 if len(shape) == 3 else math.prod(shape[:-3])
-    out, workspace, packed = _attention(q, shape, T, Hq, D, Hk, B, dev, starts, scale, causal, window, out, lse, workspace)
+    out, workspace, packed = _attention(q, shape, T, Hq, D, Hk, B, T // B if B else 0, dev, starts, scale, causal, window, out, lse, workspace)
     _enqueue("prompt_attention", dev, _abi.PROMPT_ATTENTION_CALL.pack(*packed, *kp, *vp))
     return out
 
@@ -853,8 +855,8 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, starts=None, scale=No
     ldt, t1 = page_table.stride()
     if page_table.shape[1] > 1 and t1 != 1:
         raise ValueError("page_table: a sequence's pages must be contiguous")
-    out, workspace, packed = _attention(q, shape, T, Hq, D, cshape[2], B, dev, starts, scale, causal, window, out, lse,
-                                        workspace)
+    out, workspace, packed = _attention(q, shape, T, Hq, D, cshape[2], B, page_table.shape[1] * cshape[1], dev, starts, scale,
+                                        causal, window, out, lse, workspace)
     fp8 = ck != _abi.CACHE_BF16
     _enqueue("paged_attention", dev,
              _abi.PAGED_ATTENTION_CALL.pack(*packed, k_cache.data_ptr(), kps, kss, khs, v_cache.data_ptr(), vps, vss, vhs,

@@ -29,26 +29,39 @@ crmsn_status check_common(const crmsn_attention &a)
     if (crmsn_status s = check_heads(q, a.T, a.D)) return s;
     if (crmsn_status s = check_heads(out, a.T, a.D)) return s;
     if (!al(a.starts, 4) || !al(a.lse, 4)) return CRMSN_ERR_ALIGNMENT;
-    if (!a.workspace) return CRMSN_ERR_NULL;
-    if (a.workspace_bytes == 0 || a.workspace_bytes > (uint64_t)1 << 40) return CRMSN_ERR_WORKSPACE;
     return CRMSN_OK;
+}
+
+// Calls of at most `keys` keys a sequence that need no workspace.
+bool is_short(const crmsn_attention &a, int64_t keys) { return !a.starts && keys <= kShortKeys; }
+
+crmsn_status check_workspace(const crmsn_attention &a, int64_t keys)
+{
+    if (is_short(a, keys)) return CRMSN_OK;
+    if (!a.workspace) return CRMSN_ERR_NULL;
+    return a.workspace_bytes == 0 || a.workspace_bytes > (uint64_t)1 << 40 ? CRMSN_ERR_WORKSPACE : CRMSN_OK;
 }
 
 Region starts_region(const crmsn_attention &a) { return vec_region(a.starts, a.B + 1, 4); }
 Region lse_region(const crmsn_attention &a) { return vec_region(a.lse, a.T * a.Hq, 4, true); }
-Region ws_region(const crmsn_attention &a) { return vec_region(a.workspace, (int64_t)a.workspace_bytes, 1, true); }
+Region ws_region(const crmsn_attention &a, int64_t keys)
+{
+    return vec_region(is_short(a, keys) ? nullptr : a.workspace, (int64_t)a.workspace_bytes, 1, true);
+}
 
 // The device, its SM count and the workspace, after everything else.
-crmsn_status check_device(const crmsn_attention &a, int &sms)
+crmsn_status check_device(const crmsn_attention &a, int64_t keys, int &sms)
 {
     int dev;
     if (crmsn_status s = device_sms(dev, sms)) return s;
+    if (is_short(a, keys)) return CRMSN_OK;
     if (!al(a.workspace, 256) || a.workspace_bytes < attention_workspace_bytes(a.D, dev)) return CRMSN_ERR_WORKSPACE;
     return CRMSN_OK;
 }
 
-void set_common(AttnParams &p, const crmsn_attention &a)
+void set_common(AttnParams &p, const crmsn_attention &a, int64_t keys)
 {
+    p.whole = is_short(a, keys);
     p.q = view(heads(a.q, a.Hq));
     p.out = view(heads(a.out, a.Hq));
     p.starts = a.starts;
@@ -106,18 +119,20 @@ crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStrea
     if (crmsn_status s = check_common(a)) return s;
     if (a.T == 0 || a.B == 0) return CRMSN_OK;
     const Heads k = heads(call->k, a.Hk), v = heads(call->v, a.Hk);
+    const int64_t keys = a.T / a.B;              // of a sequence, where starts is NULL
+    if (crmsn_status s = check_workspace(a, keys)) return s;
     if (crmsn_status s = check_heads(k, a.T, a.D)) return s;
     if (crmsn_status s = check_heads(v, a.T, a.D)) return s;
     const Region ts[] = {
         heads_region(heads(a.q, a.Hq), a.T, a.D), heads_region(k, a.T, a.D), heads_region(v, a.T, a.D), starts_region(a),
-        heads_region(heads(a.out, a.Hq), a.T, a.D, true), lse_region(a), ws_region(a),
+        heads_region(heads(a.out, a.Hq), a.T, a.D, true), lse_region(a), ws_region(a, keys),
     };
     if (crmsn_status s = check_alias(ts, 7)) return s;
     int sms;
-    if (crmsn_status s = check_device(a, sms)) return s;
+    if (crmsn_status s = check_device(a, keys, sms)) return s;
     AttnParams p{};
     CRMSN_SET_DEBUG(p, ts);
-    set_common(p, a);
+    set_common(p, a, keys);
     p.kv[0] = {static_cast<const uint8_t *>(k.p), 0, k.ld, k.hs};
     p.kv[1] = {static_cast<const uint8_t *>(v.p), 0, v.ld, v.hs};
     p.kind = CRMSN_CACHE_BF16;
@@ -140,6 +155,8 @@ crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_
     if (c.table_pages > 0 && a.B > 1 && (c.ld_table < 0 || c.ld_table > kMaxStride)) return CRMSN_ERR_SHAPE;
     const bool fp8 = c.cache_kind != CRMSN_CACHE_BF16;
     const int es = fp8 ? 1 : 2;
+    const int64_t keys = c.table_pages * c.page_size;
+    if (crmsn_status s = check_workspace(a, keys)) return s;
     if (!c.lens || (c.table_pages > 0 && !c.page_table) || (fp8 && (!c.k_scale || !c.v_scale))) return CRMSN_ERR_NULL;
     if (!al(c.lens, 4) || !al(c.page_table, 4) || (fp8 && (!al(c.k_scale, 4) || !al(c.v_scale, 4))))
         return CRMSN_ERR_ALIGNMENT;
@@ -157,14 +174,14 @@ crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_
         cache_region(P > 0 ? c.v_cache : nullptr, c.vps, c.vss, c.vhs, es, pages, S, a.Hk, a.D, false),
         {c.table_pages > 0 ? c.page_table : nullptr, 4, c.table_pages, {a.B, 1, 1}, {a.B > 1 ? c.ld_table : 0, 0, 0}, false, -1},
         vec_region(c.lens, a.B, 4), vec_region(fp8 ? c.k_scale : nullptr, 1, 4), vec_region(fp8 ? c.v_scale : nullptr, 1, 4),
-        starts_region(a), heads_region(heads(a.out, a.Hq), a.T, a.D, true), lse_region(a), ws_region(a),
+        starts_region(a), heads_region(heads(a.out, a.Hq), a.T, a.D, true), lse_region(a), ws_region(a, keys),
     };
     if (crmsn_status s = check_alias(ts, 11)) return s;
     int sms;
-    if (crmsn_status s = check_device(a, sms)) return s;
+    if (crmsn_status s = check_device(a, keys, sms)) return s;
     AttnParams p{};
     CRMSN_SET_DEBUG(p, ts);
-    set_common(p, a);
+    set_common(p, a, keys);
     p.kv[0] = {static_cast<const uint8_t *>(c.k_cache), c.kps, c.kss, c.khs};
     p.kv[1] = {static_cast<const uint8_t *>(c.v_cache), c.vps, c.vss, c.vhs};
     p.kind = c.cache_kind;
@@ -174,7 +191,7 @@ crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_
     p.ldt = c.ld_table;
     p.num_pages = (int)P;
     p.page = FastDiv((int)S);
-    p.max_keys = (int)(c.table_pages * S);
+    p.max_keys = (int)keys;
     p.lens = c.lens;
     const int v = 16 / es;
     return launch(p, tiled(a, es) && (P == 0 || (cache_vec(c.k_cache, c.kps, c.kss, c.khs, es, P, S, a.Hk, v) &&

@@ -115,40 +115,64 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
 
-    const Work work = share_work<W * 32>(
-        p.B, p.Hk, scratch,
-        [&](int b, int64_t &u, int64_t &t) {
-            int k0, k1;
-            units_of<UNIT>(p, sequence(p, b), k0, k1);
-            u = k1 - k0;
-            t = 1;
-        },
-        [&](int64_t units, int64_t) { return (int)min((int64_t)gridDim.x, units); });
-    if ((int)blockIdx.x >= work.ctas) {
-        if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
-        return;
-    }
-    const int G = p.group.d, R = p.n * G, items = (int)(work.u1 - work.u0);
+    const int G = p.group.d, R = p.n * G;
     Cursor at;                        // of the work
-    at.b = work.b;
-    at.s = sequence(p, at.b);
-    units_of<UNIT>(p, at.s, at.k0, at.k1);
-    at.h = (int)(work.rest / (at.k1 - at.k0));
-    at.k = at.k0 + (int)(work.rest - (int64_t)at.h * (at.k1 - at.k0));
-    int64_t tile_first = work.u0 - (at.k - at.k0);            // unit where the current tile begins
-    if (tid == 0) {
-        AttnHeader hd{};
-        hd.first = tile_first;
-        hd.last = tile_first + (at.k1 - at.k0);
-        hd.units = work.units;
-        hd.ctas = work.ctas;
-        hd.tile = at.k > at.k0;
-        hd.b = at.b;
-        hd.h = at.h;
-        hd.tok = at.s.first;
-        hd.ntok = p.n;
-        st_header(p.ws, blockIdx.x, hd);
-        odd_rows = 0;
+    int items;
+    int64_t tile_first = 0, u0 = 0;   // units where the current tile begins, where this CTA does
+    if (p.whole) {
+        const int64_t tiles = (int64_t)p.B * p.Hk;
+        const int ctas = (int)min((int64_t)gridDim.x, tiles), c = (int)blockIdx.x;
+        if (tid == 0) odd_rows = 0;
+        if (c >= ctas) return;
+        const int64_t first = first_unit(tiles, ctas, c), end = first_unit(tiles, ctas, c + 1);
+        at.b = (int)quotient(first, p.Hk);
+        at.h = (int)(first - (int64_t)at.b * p.Hk);
+        at.s = sequence(p, at.b);
+        units_of<UNIT>(p, at.s, at.k0, at.k1);
+        at.k = at.k0;
+        items = 0;
+        for (int64_t i = first + lane; i < end; i += 32) {
+            int k0, k1;
+            units_of<UNIT>(p, sequence(p, (int)quotient(i, p.Hk)), k0, k1);
+            items += k1 - k0;
+        }
+        for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+    } else {
+        const Work work = share_work<W * 32>(
+            p.B, p.Hk, scratch,
+            [&](int b, int64_t &u, int64_t &t) {
+                int k0, k1;
+                units_of<UNIT>(p, sequence(p, b), k0, k1);
+                u = k1 - k0;
+                t = 1;
+            },
+            [&](int64_t units, int64_t) { return (int)min((int64_t)gridDim.x, units); });
+        if ((int)blockIdx.x >= work.ctas) {
+            if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
+            return;
+        }
+        items = (int)(work.u1 - work.u0);
+        u0 = work.u0;
+        at.b = work.b;
+        at.s = sequence(p, at.b);
+        units_of<UNIT>(p, at.s, at.k0, at.k1);
+        at.h = (int)(work.rest / (at.k1 - at.k0));
+        at.k = at.k0 + (int)(work.rest - (int64_t)at.h * (at.k1 - at.k0));
+        tile_first = u0 - (at.k - at.k0);
+        if (tid == 0) {
+            AttnHeader hd{};
+            hd.first = tile_first;
+            hd.last = tile_first + (at.k1 - at.k0);
+            hd.units = work.units;
+            hd.ctas = work.ctas;
+            hd.tile = at.k > at.k0;
+            hd.b = at.b;
+            hd.h = at.h;
+            hd.tok = at.s.first;
+            hd.ntok = p.n;
+            st_header(p.ws, blockIdx.x, hd);
+            odd_rows = 0;
+        }
     }
 
     // ---- copies: slot 2 i holds the keys, slot 2 i + 1 the values of item i
@@ -410,8 +434,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             }
         }
         __syncthreads();
-        const bool whole = tile_first >= work.u0 && tile_ends;
-        float *const part = whole ? nullptr : part_of(p.ws, blockIdx.x, tile_first >= work.u0, kDecodeRows, DP);
+        const bool whole = tile_first >= u0 && tile_ends;
+        float *const part = whole ? nullptr : part_of(p.ws, blockIdx.x, tile_first >= u0, kDecodeRows, DP);
         for (int e = tid; e < R * (DP / 4); e += W * 32) {
             const int row = e / (DP / 4), d = (e - row * (DP / 4)) * 4;
             float M = -INFINITY;
@@ -477,7 +501,7 @@ cudaError_t run(const AttnParams &p, int sms, cudaStream_t s)
     if (cudaError_t e = opt_in_smem(k_attn_decode<KIND, DP>, S::SMEM, opted)) return e;
     const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
     if (cudaError_t e = launch_pdl(k_attn_decode<KIND, DP>, dim3(ctas), dim3(S::W * 32), S::SMEM, s, p)) return e;
-    return launch_attn_combine(p, kDecodeRows, DP, ctas, s);
+    return p.whole ? cudaSuccess : launch_attn_combine(p, kDecodeRows, DP, ctas, s);
 }
 
 template <int KIND>

@@ -57,7 +57,7 @@ constexpr int kTileThreads = 512;
 constexpr int kTileColumns = 512;
 // Registers of a thread: of the 128 at launch the copying and the issuing
 // warps give up what the weights' warps need.
-constexpr int kWeightRegs = 152, kOtherRegs = 104;
+constexpr int kWeightRegs = 168, kOtherRegs = 88;
 static_assert(2 * kWeightRegs + 2 * kOtherRegs <= 4 * 128, "registers of the launch");
 
 // sum of floor((a i + b) / m) over 0 <= i < n (the classic Euclid-like
@@ -128,14 +128,17 @@ struct Walk {
     int b, h, t, nt;
     Seq s;
     int k, end, k0, k1;              // blocks [k, end) of a tile that has [k0, k1)
-    int64_t left;                    // units from block k on
+    int64_t left;                    // units from block k on; tiles, where they are dealt whole
 };
-__device__ __forceinline__ void walk_end(Walk &c) { c.end = (int)min((int64_t)c.k1, c.k + c.left); }
+__device__ __forceinline__ void walk_end(const AttnParams &p, Walk &c)
+{
+    c.end = p.whole ? c.k1 : (int)min((int64_t)c.k1, c.k + c.left);
+}
 // To the next tile; false: there is no more work.
 template <int BN>
 __device__ __forceinline__ bool walk_on(const AttnParams &p, int TT, Walk &c)
 {
-    c.left -= c.end - c.k + kTileCost;
+    c.left -= p.whole ? 1 : c.end - c.k + kTileCost;
     if (c.left <= 0) return false;
     if (++c.t == c.nt) {
         c.t = 0;
@@ -150,7 +153,7 @@ __device__ __forceinline__ bool walk_on(const AttnParams &p, int TT, Walk &c)
     }
     tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
     c.k = c.k0;
-    walk_end(c);
+    walk_end(p, c);
     return true;
 }
 // What the other warps are told of a piece.
@@ -170,10 +173,8 @@ struct TileKernel {
     static constexpr bool FP8 = S::FP8;
 
     struct Shared {
-        union {
-            WorkScratch scratch;                              // at the start
-            Piece piece[kPieces];
-        };
+        WorkScratch scratch;
+        Piece piece[kPieces];
         uint64_t full[STAGES], empty[STAGES], landed[STAGES], q[NT], s[NT * NS], w[NT * NS][2], o[NT], last, told[kPieces], heard[kPieces];
         uint32_t tmem;
         volatile int failed;
@@ -239,27 +240,30 @@ struct TileKernel {
         }
         return !(c.flags & PIECE_NONE);
     }
-    // Warp 13.
+    __device__ __forceinline__ void tell(int i, const Walk &c, bool more)
+    {
+        Piece &d = sm.piece[i];
+        d.b = c.b;
+        d.h = c.h;
+        d.tok = c.t * TT;
+        d.ntok = min(TT, c.s.n - c.t * TT);
+        d.s = c.s;
+        d.k = c.k;
+        d.end = c.end;
+        d.flags = (c.k == c.k0 ? PIECE_BEGINS : 0) | (c.end == c.k1 ? PIECE_ENDS : 0) | (more ? 0 : PIECE_NONE);
+        d.hi = key_hi(p, c.s, d.tok + d.ntok - 1);
+        d.lo = key_lo(p, c.s, d.tok);
+        bar_arrive(at(&sm.told[i]));
+    }
+    // Warp 13: the pieces behind the first.
     __device__ __forceinline__ void tell_loop(Walk c)
     {
-        int i = 0;
+        int i = 1;
         uint32_t parity = 1;
-        for (bool more = true;; more = walk_on<BN>(p, TT, c)) {
+        for (;;) {
+            const bool more = walk_on<BN>(p, TT, c);
             if (!wait_all(&sm.heard[i], parity)) return;
-            if ((threadIdx.x & 31) == 0) {
-                Piece &d = sm.piece[i];
-                d.b = c.b;
-                d.h = c.h;
-                d.tok = c.t * TT;
-                d.ntok = min(TT, c.s.n - c.t * TT);
-                d.s = c.s;
-                d.k = c.k;
-                d.end = c.end;
-                d.flags = (c.k == c.k0 ? PIECE_BEGINS : 0) | (c.end == c.k1 ? PIECE_ENDS : 0) | (more ? 0 : PIECE_NONE);
-                d.hi = key_hi(p, c.s, d.tok + d.ntok - 1);
-                d.lo = key_lo(p, c.s, d.tok);
-                bar_arrive(at(&sm.told[i]));
-            }
+            if ((threadIdx.x & 31) == 0) tell(i, c, more);
             __syncwarp();
             if (!more) return;
             if (++i == kPieces) {
@@ -669,7 +673,7 @@ struct TileKernel {
                 if (!good) break;
                 tc_fence_after();
                 // The last scores are here: the next tile's queries may take the place of these.
-                if (n == 1) {
+                if (__builtin_expect(n == 1, 0)) {
                     // (One piece ahead and no further: later ones may wait for what this half still owes.)
                     any = next(place, nx);
                     told = true;
@@ -677,7 +681,7 @@ struct TileKernel {
                     if (copied) copy_queries(nx, half);
                 }
                 // Scores that the row does not see leave tensor memory as -infinity.
-                if (edge) {
+                if (__builtin_expect(edge, 0)) {
 #pragma unroll 1
                     for (int i = 0; i < BN / 32; ++i) {
                         uint32_t x[32];
@@ -712,7 +716,7 @@ struct TileKernel {
                     if (!good) break;
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, (most - M) * scale > 8.f || M == -INFINITY)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, (most - M) * scale > 8.f || M == -INFINITY), 0)) {
                     const float keep = M == -INFINITY || most == M ? 1.f : exp2_fast((M - most) * scale);
                     L *= keep;
                     if (begun && __any_sync(0xffffffffu, keep != 1.f)) {
@@ -862,6 +866,37 @@ struct TileKernel {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;");
         TT = S::ROWS / p.group.d;
+        if (p.whole) {
+            const int nt = (p.n + TT - 1) / TT;
+            const int64_t tiles = (int64_t)p.B * p.Hk * nt;
+            const int ctas = (int)min((int64_t)gridDim.x, tiles);
+            __syncthreads();
+            if ((int)blockIdx.x < ctas) {
+                const int64_t first = first_unit(tiles, ctas, blockIdx.x);
+                Walk c;
+                const int64_t bh = quotient(first, nt);
+                c.b = (int)quotient(bh, p.Hk);
+                c.h = (int)(bh - (int64_t)c.b * p.Hk);
+                c.t = (int)(first - bh * nt);
+                c.nt = nt;
+                c.s = sequence(p, c.b);
+                tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
+                c.k = c.k0;
+                c.left = first_unit(tiles, ctas, blockIdx.x + 1) - first;
+                run_work(c, warp, lane);
+            }
+        } else {
+            share(warp, lane);
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 12) tmem_free(tmem, kTileColumns);
+    }
+
+    // By the units of all tiles.
+    __device__ __forceinline__ void share(int warp, int lane)
+    {
         const Work work = share_work<kTileThreads>(
             p.B, p.Hk, sm.scratch,
             [&](int b, int64_t &u, int64_t &t) {
@@ -873,18 +908,10 @@ struct TileKernel {
             // A CTA for each tile; tiles are shared out further while that leaves a CTA four units (more than
             // kTileCost: every CTA has a block).
             [&](int64_t units, int64_t tiles) { return (int)min((int64_t)gridDim.x, max(tiles, units / 4)); });
-        tc_fence_after();                                     // (share_work has met at barriers)
-        tmem = uniform(sm.tmem);
-        if ((int)blockIdx.x < work.ctas) run_work(work, warp, lane);
-        else if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (warp == 12) tmem_free(tmem, kTileColumns);
-    }
-
-    __device__ __forceinline__ void run_work(const Work &work, int warp, int lane)
-    {
+        if ((int)blockIdx.x >= work.ctas) {
+            if (threadIdx.x == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
+            return;
+        }
         Walk c;
         c.b = work.b;
         c.s = sequence(p, c.b);
@@ -909,8 +936,6 @@ struct TileKernel {
         const int in = (int)(rest - units_before(c.t)) - kTileCost;      // blocks before u0, or less than none
         c.k = c.k0 + max(in, 0);
         c.left = work.u1 - work.u0 + min(in, 0);
-        walk_end(c);
-        __syncthreads();                                      // the scratch becomes pieces
         if (threadIdx.x == 0) {
             AttnHeader hd{};
             hd.first = work.u0 - in;                          // the tile's first block
@@ -924,6 +949,16 @@ struct TileKernel {
             hd.ntok = min(TT, c.s.n - c.t * TT);
             st_header(p.ws, blockIdx.x, hd);
         }
+        run_work(c, warp, lane);
+    }
+
+    // All threads, after a barrier behind the start's own work.
+    __device__ __forceinline__ void run_work(Walk &c, int warp, int lane)
+    {
+        tc_fence_after();
+        tmem = uniform(sm.tmem);
+        walk_end(p, c);
+        if (threadIdx.x == 0) tell(0, c, true);
         __syncwarp();
         if (warp < 8) {
             more_registers<kWeightRegs>();
@@ -968,7 +1003,7 @@ cudaError_t run_attn_tile(const AttnParams &p, int sms, cudaStream_t s)
     if (cudaError_t e = opt_in_smem(k_attn_tile<KIND, DP>, S::SMEM, opted)) return e;
     const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
     if (cudaError_t e = launch_pdl(k_attn_tile<KIND, DP>, dim3(ctas), dim3(kTileThreads), S::SMEM, s, p)) return e;
-    return launch_attn_combine(p, S::ROWS, DP, ctas, s);
+    return p.whole ? cudaSuccess : launch_attn_combine(p, S::ROWS, DP, ctas, s);
 }
 
 }  // namespace crmsn
