@@ -866,14 +866,16 @@ struct TileKernel {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;");
         TT = S::ROWS / p.group.d;
+        Walk c;
+        bool work;
         if (p.whole) {
             const int nt = (p.n + TT - 1) / TT;
             const int64_t tiles = (int64_t)p.B * p.Hk * nt;
             const int ctas = (int)min((int64_t)gridDim.x, tiles);
             __syncthreads();
-            if ((int)blockIdx.x < ctas) {
+            work = (int)blockIdx.x < ctas;
+            if (work) {
                 const int64_t first = first_unit(tiles, ctas, blockIdx.x);
-                Walk c;
                 const int64_t bh = quotient(first, nt);
                 c.b = (int)quotient(bh, p.Hk);
                 c.h = (int)(bh - (int64_t)c.b * p.Hk);
@@ -883,19 +885,19 @@ struct TileKernel {
                 tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
                 c.k = c.k0;
                 c.left = first_unit(tiles, ctas, blockIdx.x + 1) - first;
-                run_work(c, warp, lane);
             }
         } else {
-            share(warp, lane);
+            work = share(c, lane);
         }
+        if (work) run_work(c, warp, lane);
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
         if (warp == 12) tmem_free(tmem, kTileColumns);
     }
 
-    // By the units of all tiles.
-    __device__ __forceinline__ void share(int warp, int lane)
+    // By the units of all tiles: where this CTA's begin; false: it has none.
+    __device__ __forceinline__ bool share(Walk &c, int lane)
     {
         const Work work = share_work<kTileThreads>(
             p.B, p.Hk, sm.scratch,
@@ -910,9 +912,8 @@ struct TileKernel {
             [&](int64_t units, int64_t tiles) { return (int)min((int64_t)gridDim.x, max(tiles, units / 4)); });
         if ((int)blockIdx.x >= work.ctas) {
             if (threadIdx.x == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
-            return;
+            return false;
         }
-        Walk c;
         c.b = work.b;
         c.s = sequence(p, c.b);
         c.nt = (c.s.n + TT - 1) / TT;
@@ -949,7 +950,7 @@ struct TileKernel {
             hd.ntok = min(TT, c.s.n - c.t * TT);
             st_header(p.ws, blockIdx.x, hd);
         }
-        run_work(c, warp, lane);
+        return true;
     }
 
     // All threads, after a barrier behind the start's own work.
