@@ -164,14 +164,18 @@ __device__ __forceinline__ bool suspect(float o, float L)
 }
 
 // ------------------------------------------------------------- work split --
-// All tiles (rows that share keys) of a call, each as many units as it has
-// blocks of keys, in one line; CTA c of C takes the units from U c / C to
-// U (c + 1) / C.  So every CTA has the same work whatever the lengths are, and
-// only the tiles at its two ends are shared with others.
+// All tiles (rows that share keys) of one key head, each as many units as it
+// has blocks of keys, in one line; group g of C takes the units from U g / C to
+// U (g + 1) / C.  So every group has the same work whatever the lengths are, and
+// only the tiles at its two ends are shared with others.  A group is Hk CTAs
+// (CTA g Hk + h: head h), which walk through the same keys at the same time: a
+// cache that holds the heads of a slot side by side is read by whole slots.
+// (One head after another reads 128 bytes of each kilobyte: 16 sequences of up
+// to 16384 keys in E4M3 took 75 us.)
 struct Work {
     int64_t units;               // U
-    int ctas;                    // C
-    int64_t u0, u1;              // this CTA's
+    int groups;                  // C
+    int64_t u0, u1;              // this group's
     int b;                       // the sequence of u0,
     int64_t rest;                // and u0 less the units of those before it
 };
@@ -181,8 +185,8 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t d)
     if (((x | d) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)d);
     return x / d;
 }
-__device__ __forceinline__ int64_t first_unit(int64_t U, int C, int c) { return quotient(U * c, C); }
-// The CTA that takes unit u: the largest c with floor(U c / C) <= u.
+__device__ __forceinline__ int64_t first_unit(int64_t U, int C, int g) { return quotient(U * g, C); }
+// The group that takes unit u: the largest g with floor(U g / C) <= u.
 __device__ __forceinline__ int unit_owner(int64_t U, int C, int64_t u) { return (int)quotient((u + 1) * C - 1, U); }
 
 struct WorkScratch {
@@ -191,11 +195,11 @@ struct WorkScratch {
     int b;
 };
 
-// count(b, units, tiles): what sequence b has for each key head.  ctas(units,
-// tiles): how many CTAs share them.  All THREADS threads call this; sequences
-// are counted THREADS at a time, and found again by a scan.
-template <int THREADS, typename Count, typename Ctas>
-__device__ __forceinline__ Work share_work(int B, int Hk, WorkScratch &sm, Count count, Ctas ctas)
+// count(b, units, tiles): what sequence b has for a key head.  groups(units,
+// tiles): how many share them; g: this CTA's.  All THREADS threads call this;
+// sequences are counted THREADS at a time, and found again by a scan.
+template <int THREADS, typename Count, typename Groups>
+__device__ __forceinline__ Work share_work(int B, int g, WorkScratch &sm, Count count, Groups groups)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -223,17 +227,16 @@ __device__ __forceinline__ Work share_work(int B, int Hk, WorkScratch &sm, Count
         w.units += __shfl_xor_sync(0xffffffffu, w.units, o);
         tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
     }
-    w.units = __shfl_sync(0xffffffffu, w.units, 0) * Hk;
+    w.units = __shfl_sync(0xffffffffu, w.units, 0);
     tiles = __shfl_sync(0xffffffffu, tiles, 0);
-    w.ctas = ctas(w.units, tiles * Hk);
-    const int c = (int)blockIdx.x;
+    w.groups = groups(w.units, tiles);
     w.u0 = w.u1 = w.rest = 0;
     w.b = 0;
-    if (c >= w.ctas) return w;   // the same for all threads (no units: no CTAs)
-    w.u0 = first_unit(w.units, w.ctas, c);
-    w.u1 = first_unit(w.units, w.ctas, c + 1);
-    // The sequence of u0: the one in which the running sum passes u0 / Hk.
-    const int64_t want = quotient(w.u0, Hk);
+    if (g >= w.groups) return w; // the same for all threads (no units: no groups)
+    w.u0 = first_unit(w.units, w.groups, g);
+    w.u1 = first_unit(w.units, w.groups, g + 1);
+    // The sequence of u0: the one in which the running sum passes it.
+    const int64_t want = w.u0;
     int64_t before = 0;
     for (int base = 0; base < B; base += THREADS) {
         const int b = base + tid;
@@ -256,7 +259,7 @@ __device__ __forceinline__ Work share_work(int B, int Hk, WorkScratch &sm, Count
         const int64_t lo = before + incl - u;
         if (b < B && want >= lo && want < lo + u) {
             sm.b = b;
-            sm.rest = w.u0 - lo * Hk;
+            sm.rest = w.u0 - lo;
         }
         before += chunk;
         if (want < before) break;
@@ -321,6 +324,19 @@ __device__ __forceinline__ uint32_t f16_fp8(uint32_t codes)
     if constexpr (KIND == KV_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
     else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(c));
     return r;
+}
+// Four FP8 codes -> two packed FP16 pairs.  An E5M2 code is the upper half of its
+// FP16 value.
+template <int KIND>
+__device__ __forceinline__ void f16_codes(uint32_t codes, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (KIND == KV_E5M2) {
+        lo = __byte_perm(codes, 0, 0x1404);
+        hi = __byte_perm(codes, 0, 0x3424);
+    } else {
+        lo = f16_fp8<KIND>(codes);
+        hi = f16_fp8<KIND>(codes >> 16);
+    }
 }
 // Two floats -> packed FP16 pair (lo in bits 0..15), round to nearest even.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)

@@ -64,14 +64,21 @@ inline int attn_padded(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 
 // of the tile that it finds begun, the beginning of the one that it leaves).
 // A part of `rows` rows: their maxima and sums, then rows x DP sums of values.
 struct AttnHeader {
-    int64_t first, last, units;  // units of the tile's blocks; of all tiles
-    int ctas, tile;              // CTAs that share them; 1: begins inside this tile
+    int64_t first, last, units;  // units of the tile's blocks; of all tiles of a head
+    int groups, tile;            // groups that share them; 1: begins inside this tile
     int b, h, tok, ntok;         // sequence, key head, first token and tokens of the tile
     int pad[4];
 };
 static_assert(sizeof(AttnHeader) == 64, "one header");
 constexpr int kAttnMaxCtas = 1024;
 constexpr int64_t kAttnParts = (int64_t)kAttnMaxCtas * (int64_t)sizeof(AttnHeader);
+// Groups of Hk CTAs that a device runs at once.  (One: no tile is shared, and
+// neither headers nor parts are written.)
+inline int attn_groups(int sms, int Hk)
+{
+    const int n = (sms < kAttnMaxCtas ? sms : kAttnMaxCtas) / Hk;
+    return n < 1 ? 1 : n;
+}
 inline int64_t attn_part_floats(int rows, int DP) { return (int64_t)rows * (2 + DP); }
 
 // Sequences of the same number of tokens each and of at most this many keys are
@@ -81,7 +88,7 @@ inline int64_t attn_part_floats(int rows, int DP) { return (int64_t)rows * (2 + 
 constexpr int kShortKeys = CRMSN_ATTENTION_SHORT;
 
 // Joins the parts of the tiles that several CTAs shared (attn_combine.cu).
-cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int ctas, cudaStream_t s);
+cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int groups, cudaStream_t s);
 
 // At most 16 rows (tokens times heads of a group) of each sequence, the same
 // number of tokens for all (attn_decode.cu).

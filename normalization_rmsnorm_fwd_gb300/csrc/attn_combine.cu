@@ -2,9 +2,9 @@
 // with a part's maximum M_i, sum L_i and values O_i (relative to M_i),
 //   M = max M_i,  L = sum L_i 2^(M_i - M),  o = sum O_i 2^(M_i - M) / L.
 //
-// CTA column c looks at the tile in which the work of CTA c of the attention
-// kernel began, and joins it where it is the first such CTA of that tile; one
-// warp for each row.  Parts are added in the order of their keys.
+// CTA column c looks at the tile in which the work of CTA Hk + c of the
+// attention kernel began, and joins it where its group is the first such one;
+// one warp for each row.  Parts are added in the order of their keys.
 #include "attn.cuh"
 
 namespace crmsn {
@@ -18,17 +18,17 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_const
     constexpr int NV = DP / 64;              // pairs of columns of a lane
     CRMSN_DEBUG_ENTER(p.dbg);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = (int)blockIdx.x + 1;
+    const int c = (int)blockIdx.x + p.Hk, g = c / p.Hk;
     AttnHeader *at = reinterpret_cast<AttnHeader *>(p.ws) + c;
     if (!dbg_global(at, (int)sizeof(AttnHeader), false)) return;
     const AttnHeader hd = *at;
-    if (!hd.tile || first_unit(hd.units, hd.ctas, c - 1) > hd.first) return;
+    if (!hd.tile || first_unit(hd.units, hd.groups, g - 1) > hd.first) return;
     const int nrows = hd.ntok * p.group.d;
     const int r = (int)blockIdx.y * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (r >= nrows) return;
-    const int c0 = c - 1, n = unit_owner(hd.units, hd.ctas, hd.last - 1) - c0 + 1;
-    // The part of CTA c0 is its second (the tile begins there), that of the others their first.
-    const auto part = [&](int i) { return part_of(p.ws, c0 + i, i == 0, rows, DP); };
+    const int n = unit_owner(hd.units, hd.groups, hd.last - 1) - g + 2;
+    // The part of the group before is its second (the tile begins there), that of the others their first.
+    const auto part = [&](int i) { return part_of(p.ws, c + (i - 1) * p.Hk, i == 0, rows, DP); };
     float M = -INFINITY, L = 0.f;
     F2 o[NV];
     for (int k = 0; k < NV; ++k) o[k] = f2(0.f);
@@ -94,10 +94,10 @@ cudaError_t run(const AttnParams &p, int rows, int DP, dim3 grid, cudaStream_t s
 
 }  // namespace
 
-cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int ctas, cudaStream_t s)
+cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int groups, cudaStream_t s)
 {
-    if (ctas < 2) return cudaSuccess;
-    const dim3 grid(ctas - 1, (rows + kWarps - 1) / kWarps);
+    if (groups < 2) return cudaSuccess;
+    const dim3 grid((groups - 1) * p.Hk, (rows + kWarps - 1) / kWarps);
     switch (p.kind) {
         case KV_BF16: return run<KV_BF16>(p, rows, DP, grid, s);
         case KV_E4M3: return run<KV_E4M3>(p, rows, DP, grid, s);

@@ -80,20 +80,16 @@ __device__ __forceinline__ void units_of(const AttnParams &p, const Seq &s, int 
 
 // A place in the line of units.
 struct Cursor {
-    int b, h, k, k0, k1;
+    int b, k, k0, k1;
     Seq s;
 };
 template <int UNIT>
 __device__ __forceinline__ void step(const AttnParams &p, Cursor &c)
 {
     if (++c.k < c.k1) return;
-    if (++c.h == p.Hk) {
-        c.h = 0;
-        ++c.b;
-        if (c.b < p.B) {
-            c.s = sequence(p, c.b);
-            units_of<UNIT>(p, c.s, c.k0, c.k1);
-        }
+    if (++c.b < p.B) {
+        c.s = sequence(p, c.b);
+        units_of<UNIT>(p, c.s, c.k0, c.k1);
     }
     c.k = c.k0;
 }
@@ -119,36 +115,35 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
     Cursor at;                        // of the work
     int items;
     int64_t tile_first = 0, u0 = 0;   // units where the current tile begins, where this CTA does
+    const int groups = (int)gridDim.x / p.Hk, group = (int)blockIdx.x / p.Hk, h = (int)blockIdx.x - group * p.Hk;
+    if (tid == 0) odd_rows = 0;
     if (p.whole) {
-        const int64_t tiles = (int64_t)p.B * p.Hk;
-        const int ctas = (int)min((int64_t)gridDim.x, tiles), c = (int)blockIdx.x;
-        if (tid == 0) odd_rows = 0;
-        if (c >= ctas) return;
-        const int64_t first = first_unit(tiles, ctas, c), end = first_unit(tiles, ctas, c + 1);
-        at.b = (int)quotient(first, p.Hk);
-        at.h = (int)(first - (int64_t)at.b * p.Hk);
+        const int n = min(groups, p.B);
+        if (group >= n) return;
+        at.b = (int)first_unit(p.B, n, group);
+        const int end = (int)first_unit(p.B, n, group + 1);
         at.s = sequence(p, at.b);
         units_of<UNIT>(p, at.s, at.k0, at.k1);
         at.k = at.k0;
         items = 0;
-        for (int64_t i = first + lane; i < end; i += 32) {
+        for (int b = at.b + lane; b < end; b += 32) {
             int k0, k1;
-            units_of<UNIT>(p, sequence(p, (int)quotient(i, p.Hk)), k0, k1);
+            units_of<UNIT>(p, sequence(p, b), k0, k1);
             items += k1 - k0;
         }
         for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
     } else {
         const Work work = share_work<W * 32>(
-            p.B, p.Hk, scratch,
+            p.B, group, scratch,
             [&](int b, int64_t &u, int64_t &t) {
                 int k0, k1;
                 units_of<UNIT>(p, sequence(p, b), k0, k1);
                 u = k1 - k0;
                 t = 1;
             },
-            [&](int64_t units, int64_t) { return (int)min((int64_t)gridDim.x, units); });
-        if ((int)blockIdx.x >= work.ctas) {
-            if (tid == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
+            [&](int64_t units, int64_t) { return (int)min((int64_t)groups, units); });
+        if (group >= work.groups) {
+            if (tid == 0 && groups > 1) st_header(p.ws, blockIdx.x, AttnHeader{});
             return;
         }
         items = (int)(work.u1 - work.u0);
@@ -156,22 +151,20 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
         at.b = work.b;
         at.s = sequence(p, at.b);
         units_of<UNIT>(p, at.s, at.k0, at.k1);
-        at.h = (int)(work.rest / (at.k1 - at.k0));
-        at.k = at.k0 + (int)(work.rest - (int64_t)at.h * (at.k1 - at.k0));
+        at.k = at.k0 + (int)work.rest;
         tile_first = u0 - (at.k - at.k0);
-        if (tid == 0) {
+        if (tid == 0 && groups > 1) {
             AttnHeader hd{};
             hd.first = tile_first;
             hd.last = tile_first + (at.k1 - at.k0);
             hd.units = work.units;
-            hd.ctas = work.ctas;
+            hd.groups = work.groups;
             hd.tile = at.k > at.k0;
             hd.b = at.b;
-            hd.h = at.h;
+            hd.h = h;
             hd.tok = at.s.first;
             hd.ntok = p.n;
             st_header(p.ws, blockIdx.x, hd);
-            odd_rows = 0;
         }
     }
 
@@ -192,8 +185,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
                     locate(p, src.b, src.s, j, page, row);
                     ok = page >= 0;
                     if (ok) {
-                        off[0] = kv_offset(p.kv[0], page, row, src.h);
-                        off[1] = kv_offset(p.kv[1], page, row, src.h);
+                        off[0] = kv_offset(p.kv[0], page, row, h);
+                        off[1] = kv_offset(p.kv[1], page, row, h);
                     }
                 }
                 step<UNIT>(p, src);
@@ -223,7 +216,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
     // ---- a tile's state
     const int g = lane >> 2, q4 = lane & 3;                   // rows g and g + 8, columns 2 q4, 2 q4 + 1
     const int tok0 = p.group.div(g), tok1 = p.group.div(g + 8);
-    uint32_t qa[DP / 16][4];
+    // Queries as fragments: in registers, or, where O leaves none, in this warp's place for its part of the join, which
+    // is free until the tile ends.
+    constexpr bool QS = DP >= 192;
+    uint32_t q_regs[QS ? 1 : DP / 16][4];
+    uint4 *const q_place = reinterpret_cast<uint4 *>(join_o + warp * kDecodeRows * DP) + lane;
     float o[DP / 8][4], m0, m1, l0, l1, c0, c1, vs = 1.f, ks = 1.f;
     int hi0, hi1, lo0, lo1, hi_all = 0, lo_all = 0;
     if (KIND != KV_BF16) {
@@ -231,10 +228,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
         vs = ld_f32_ro(p.scale[1]);
     }
     const auto load_queries = [&]() {
+        uint32_t qa[DP / 16][4];
         c0 = c1 = p.qk_scale * ks;
         const bool in0 = g < R, in1 = g + 8 < R;
-        const uint16_t *r0 = p.q.p + (at.s.first + (in0 ? tok0 : 0)) * p.q.ld + (at.h * G + (in0 ? g - tok0 * G : 0)) * p.q.hs;
-        const uint16_t *r1 = p.q.p + (at.s.first + (in1 ? tok1 : 0)) * p.q.ld + (at.h * G + (in1 ? g + 8 - tok1 * G : 0)) * p.q.hs;
+        const uint16_t *r0 = p.q.p + (at.s.first + (in0 ? tok0 : 0)) * p.q.ld + (h * G + (in0 ? g - tok0 * G : 0)) * p.q.hs;
+        const uint16_t *r1 = p.q.p + (at.s.first + (in1 ? tok1 : 0)) * p.q.ld + (h * G + (in1 ? g + 8 - tok1 * G : 0)) * p.q.hs;
         const auto pair = [&](const uint16_t *r, bool in, int d) -> uint32_t {
             if (!in || d >= p.D || !dbg_global(r + d, 4, false)) return 0u;
             return __ldg(reinterpret_cast<const uint32_t *>(r + d));
@@ -273,6 +271,15 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             c1 = scaled(c1, -e1);
         }
 #pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+            if constexpr (QS) {
+                if (dbg_shared(q_place + 32 * k, 16)) q_place[32 * k] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q_regs[k][i] = qa[k][i];
+            }
+        }
+#pragma unroll
         for (int k = 0; k < DP / 8; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
         m0 = m1 = -INFINITY;
         l0 = l1 = 0.f;
@@ -298,21 +305,34 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
         for (int b = 0; b < KB / 8; ++b) x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
+            uint32_t qa[4];
+            if constexpr (QS) {
+                const uint4 v = q_place[32 * k];
+                qa[0] = v.x;
+                qa[1] = v.y;
+                qa[2] = v.z;
+                qa[3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qa[i] = q_regs[k][i];
+            }
             if constexpr (KIND == KV_BF16) {
 #pragma unroll
                 for (int b = 0; b < KB / 16; ++b) {
                     const int row = 16 * b + (lane & 7) + ((lane >> 4) << 3), chunk = 2 * k + ((lane >> 3) & 1);
                     uint32_t f[4];
                     ldsm4(f, keys + row * S::PITCH + swz<CH>(row, chunk) * 16);
-                    mma<KIND>(x[2 * b], qa[k], f[0], f[1]);
-                    mma<KIND>(x[2 * b + 1], qa[k], f[2], f[3]);
+                    mma<KIND>(x[2 * b], qa, f[0], f[1]);
+                    mma<KIND>(x[2 * b + 1], qa, f[2], f[3]);
                 }
             } else {
 #pragma unroll
                 for (int b = 0; b < KB / 8; ++b) {
                     const int row = 8 * b + g;
                     const uint32_t codes = *reinterpret_cast<const uint32_t *>(keys_p + row * S::PITCH + swz<CH>(row, k) * 16 + 4 * q4);
-                    mma<KIND>(x[b], qa[k], f16_fp8<KIND>(codes), f16_fp8<KIND>(codes >> 16));
+                    uint32_t b0, b1;
+                    f16_codes<KIND>(codes, b0, b1);
+                    mma<KIND>(x[b], qa, b0, b1);
                 }
             }
         }
@@ -387,13 +407,14 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
                     const int row = 16 * b + (lane & 15), chunk = 2 * k + (lane >> 4);
                     uint32_t f[4];
                     ldsm4_t(f, values + row * S::PITCH + swz<CH>(row, chunk) * 16);
+                    uint32_t even[4], odd[4];             // columns of two keys
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = __byte_perm(f[i], 0, 0x3120);   // even column of two keys, odd column
+                    for (int i = 0; i < 4; ++i) f16_codes<KIND>(__byte_perm(f[i], 0, 0x3120), even[i], odd[i]);
                     // Products 4 k, 4 k + 1: even and odd columns of chunk 2 k; 4 k + 2, 4 k + 3: of chunk 2 k + 1.
-                    mma<KIND>(o[4 * k], pa[b], f16_fp8<KIND>(f[0]), f16_fp8<KIND>(f[1]));
-                    mma<KIND>(o[4 * k + 1], pa[b], f16_fp8<KIND>(f[0] >> 16), f16_fp8<KIND>(f[1] >> 16));
-                    mma<KIND>(o[4 * k + 2], pa[b], f16_fp8<KIND>(f[2]), f16_fp8<KIND>(f[3]));
-                    mma<KIND>(o[4 * k + 3], pa[b], f16_fp8<KIND>(f[2] >> 16), f16_fp8<KIND>(f[3] >> 16));
+                    mma<KIND>(o[4 * k], pa[b], even[0], even[1]);
+                    mma<KIND>(o[4 * k + 1], pa[b], odd[0], odd[1]);
+                    mma<KIND>(o[4 * k + 2], pa[b], even[2], even[3]);
+                    mma<KIND>(o[4 * k + 3], pa[b], odd[2], odd[3]);
                 }
             }
         }
@@ -454,7 +475,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
                 b = f2_fma(f2(v.z, v.w), f2(s), b);
             }
             if (whole) {
-                const int i = p.group.div(row), hq = at.h * G + row - i * G;
+                const int i = p.group.div(row), hq = h * G + row - i * G;
                 const int64_t t = at.s.first + i;
                 const float inv = vs / L;
                 a = L == 0.f ? f2(0.f) : f2_mul(a, f2(inv));  // no key: zeros, whatever 0 times the values was
@@ -478,7 +499,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             for (int row = warp; row < R; row += W)
                 if (odd_rows >> row & 1u) {
                     const int i = p.group.div(row);
-                    attend_row<KIND, DP / 32>(p, at.b, at.s, i, at.h * G + row - i * G, false);
+                    attend_row<KIND, DP / 32>(p, at.b, at.s, i, h * G + row - i * G, false);
                 }
             __syncthreads();
             if (tid == 0) odd_rows = 0;
@@ -499,9 +520,9 @@ cudaError_t run(const AttnParams &p, int sms, cudaStream_t s)
     using S = Shape<KIND, DP>;
     static std::atomic<int> opted[kOptInDevices];
     if (cudaError_t e = opt_in_smem(k_attn_decode<KIND, DP>, S::SMEM, opted)) return e;
-    const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
-    if (cudaError_t e = launch_pdl(k_attn_decode<KIND, DP>, dim3(ctas), dim3(S::W * 32), S::SMEM, s, p)) return e;
-    return p.whole ? cudaSuccess : launch_attn_combine(p, kDecodeRows, DP, ctas, s);
+    const int groups = attn_groups(sms, p.Hk);
+    if (cudaError_t e = launch_pdl(k_attn_decode<KIND, DP>, dim3(groups * p.Hk), dim3(S::W * 32), S::SMEM, s, p)) return e;
+    return p.whole ? cudaSuccess : launch_attn_combine(p, kDecodeRows, DP, groups, s);
 }
 
 template <int KIND>

@@ -125,7 +125,7 @@ static __device__ __noinline__ int64_t blocks_before(int BN, int n, int m, int c
 // block.  A CTA whose units end inside the former has no part of the tile, one
 // whose units begin there has all of its first blocks.  The walk:
 struct Walk {
-    int b, h, t, nt;
+    int b, t, nt;
     Seq s;
     int k, end, k0, k1;              // blocks [k, end) of a tile that has [k0, k1)
     int64_t left;                    // units from block k on; tiles, where they are dealt whole
@@ -142,14 +142,11 @@ __device__ __forceinline__ bool walk_on(const AttnParams &p, int TT, Walk &c)
     if (c.left <= 0) return false;
     if (++c.t == c.nt) {
         c.t = 0;
-        if (++c.h == p.Hk) {
-            c.h = 0;
-            do {                     // work is left: there is a sequence with tokens
-                ++c.b;
-                c.s = sequence(p, c.b);
-            } while (c.s.n == 0 && c.b + 1 < p.B);
-            c.nt = (c.s.n + TT - 1) / TT;
-        }
+        do {                         // work is left: there is a sequence with tokens
+            ++c.b;
+            c.s = sequence(p, c.b);
+        } while (c.s.n == 0 && c.b + 1 < p.B);
+        c.nt = (c.s.n + TT - 1) / TT;
     }
     tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
     c.k = c.k0;
@@ -158,10 +155,12 @@ __device__ __forceinline__ bool walk_on(const AttnParams &p, int TT, Walk &c)
 }
 // What the other warps are told of a piece.
 struct __align__(16) Piece {
-    int b, h, tok, ntok;             // sequence, key head, first token and tokens of the tile
+    int b, tok, ntok;                // sequence, first token and tokens of the tile
     Seq s;
-    int k;                           // blocks [k, end)
-    int end, flags, hi, lo;          // keys [lo, hi) that the tile's rows see
+    int k, end;                      // blocks [k, end)
+    int flags;
+    int hi, lo;                      // keys [lo, hi) that the tile's rows see
+    int pad;
 };
 enum { PIECE_BEGINS = 1, PIECE_ENDS = 2, PIECE_NONE = 4 };   // the tile's first block, its last; no piece: the end
 constexpr int kPieces = 8;
@@ -175,7 +174,7 @@ struct TileKernel {
     struct Shared {
         WorkScratch scratch;
         Piece piece[kPieces];
-        uint64_t full[STAGES], empty[STAGES], landed[STAGES], q[NT], s[NT * NS], w[NT * NS][2], o[NT], last, told[kPieces], heard[kPieces];
+        uint64_t full[STAGES], empty[STAGES], landed[STAGES], raw_full[S::RAWS + 1], raw_empty[S::RAWS + 1], q[NT], s[NT * NS], w[NT * NS][2], o[NT], last, told[kPieces], heard[kPieces];
         uint32_t tmem;
         volatile int failed;
     };
@@ -185,6 +184,7 @@ struct TileKernel {
     uint8_t *const base;             // queries, stages, codes
     uint32_t tmem;
     int TT;
+    const int groups, group, h;      // of Hk CTAs each, this CTA's, its head
 
     static __device__ __forceinline__ uint32_t at(const uint64_t *bar) { return smem_addr(bar); }
     __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity) { return bar_wait(at(bar), parity, &sm.failed); }
@@ -224,8 +224,7 @@ struct TileKernel {
         uint32_t parity;
     };
     // The next piece, read by a whole warp; false: no more, or a wait ran out.
-    // keep: another reader of this warp will follow, which lets the place go.
-    __device__ __forceinline__ bool next(Place &at_, Piece &c, bool keep = false)
+    __device__ __forceinline__ bool next(Place &at_, Piece &c)
     {
         if (!wait_all(&sm.told[at_.i], at_.parity)) return false;
         const int4 *src = reinterpret_cast<const int4 *>(&sm.piece[at_.i]);
@@ -233,7 +232,7 @@ struct TileKernel {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(Piece) / 16); ++i) dst[i] = src[i];
         __syncwarp();
-        if (!keep && (threadIdx.x & 31) == 0) bar_arrive(at(&sm.heard[at_.i]));
+        if ((threadIdx.x & 31) == 0) bar_arrive(at(&sm.heard[at_.i]));
         if (++at_.i == kPieces) {
             at_.i = 0;
             at_.parity ^= 1;
@@ -244,7 +243,6 @@ struct TileKernel {
     {
         Piece &d = sm.piece[i];
         d.b = c.b;
-        d.h = c.h;
         d.tok = c.t * TT;
         d.ntok = min(TT, c.s.n - c.t * TT);
         d.s = c.s;
@@ -280,29 +278,28 @@ struct TileKernel {
         int64_t off[2];
         bool ok;
     };
-    __device__ __forceinline__ Rows find_rows(const Piece &c) const
+    __device__ __forceinline__ Rows find_rows(const Piece &c, int first) const
     {
-        const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
         Rows r{{0, 0}, false};
-        const int j = c.k * BN + warp * (BN / 4) + lane % (BN / 4);
+        const int j = c.k * BN + first + (int)(threadIdx.x & 31) % (BN / 4);
         if (j < c.hi && j >= c.lo) {
             int page, row;
             locate(p, c.b, c.s, j, page, row);
             if (page >= 0) {
                 r.ok = true;
-                r.off[0] = kv_offset(p.kv[0], page, row, c.h);
-                r.off[1] = kv_offset(p.kv[1], page, row, c.h);
+                r.off[0] = kv_offset(p.kv[0], page, row, h);
+                r.off[1] = kv_offset(p.kv[1], page, row, h);
             }
         }
         return r;
     }
-    // Copies the keys (which = 0) or values of the rows: to their places in a
-    // stage (BF16), or as codes to this thread's slots.
-    __device__ __forceinline__ void copy_rows(const Rows &r, int which, uint32_t dst) const
+    // Copies the keys (which = 0) or values of BN / 4 rows from `first` on: to
+    // their places in a stage (BF16), or as codes, row behind row.
+    __device__ __forceinline__ void copy_rows(const Rows &r, int first, int which, uint32_t dst) const
     {
         constexpr int CH = DP * (FP8 ? 1 : 2) / 16, RW = BN / 4, N = RW * CH / 32;
         static_assert(RW * CH % 32 == 0, "whole instructions");
-        const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+        const int lane = threadIdx.x & 31;
         const uint8_t *src = p.kv[which].p;
         const int64_t mine = which ? r.off[1] : r.off[0];
         const int have = p.D * (FP8 ? 1 : 2);
@@ -311,25 +308,33 @@ struct TileKernel {
             const int e = i * 32 + lane, row = e / CH, chunk = e % CH;
             const int64_t o = __shfl_sync(0xffffffffu, mine, row);
             const bool ok = __shfl_sync(0xffffffffu, r.ok, row) && chunk * 16 < have;
-            const uint32_t to = FP8 ? dst + (uint32_t)(i * 128 + warp * 32 + lane) * 16u
-                                    : dst + matrix_at(warp * RW + row, chunk, BN * 128);
+            const uint32_t to = dst + (FP8 ? (uint32_t)((first + row) * CH + chunk) * 16u : matrix_at(first + row, chunk, BN * 128));
             copy16(to, src + o * (FP8 ? 1 : 2) + chunk * 16, ok);
         }
     }
-    // This thread's codes, arrived, to FP16 in a stage.
+    // A quarter of the codes of a block to FP16 in a stage.  (All loads before the
+    // first store: one after another, each waits for the other's latency.)
     __device__ __forceinline__ void convert(const uint8_t *codes, uint8_t *dst) const
     {
         constexpr int CH = DP / 16, RW = BN / 4, N = RW * CH / 32;
         const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+        uint4 v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint8_t *from = codes + (warp * N + i) * 512 + lane * 16;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (dbg_shared(from, 16)) v[i] = *reinterpret_cast<const uint4 *>(from);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = i * 32 + lane, row = warp * RW + e / CH, chunk = e % CH;
-            const uint8_t *from = codes + (i * 128 + warp * 32 + lane) * 16;
-            const uint4 v = dbg_shared(from, 16) ? *reinterpret_cast<const uint4 *>(from) : make_uint4(0, 0, 0, 0);
-            put16(dst + matrix_at(row, 2 * chunk, BN * 128), f16_fp8<KIND>(v.x), f16_fp8<KIND>(v.x >> 16), f16_fp8<KIND>(v.y),
-                  f16_fp8<KIND>(v.y >> 16));
-            put16(dst + matrix_at(row, 2 * chunk + 1, BN * 128), f16_fp8<KIND>(v.z), f16_fp8<KIND>(v.z >> 16), f16_fp8<KIND>(v.w),
-                  f16_fp8<KIND>(v.w >> 16));
+            uint32_t h[8];
+            f16_codes<KIND>(v[i].x, h[0], h[1]);
+            f16_codes<KIND>(v[i].y, h[2], h[3]);
+            f16_codes<KIND>(v[i].z, h[4], h[5]);
+            f16_codes<KIND>(v[i].w, h[6], h[7]);
+            put16(dst + matrix_at(row, 2 * chunk, BN * 128), h[0], h[1], h[2], h[3]);
+            put16(dst + matrix_at(row, 2 * chunk + 1, BN * 128), h[4], h[5], h[6], h[7]);
         }
     }
 
@@ -345,10 +350,11 @@ struct TileKernel {
         Piece c;
         bool more = next(place, c);
         int which = 0;
-        Rows r = find_rows(c);
+        const int first = (int)((threadIdx.x >> 5) & 3) * (BN / 4);
+        Rows r = find_rows(c, first);
         for (int idle = 0; more || pending;) {
             if (more && __all_sync(0xffffffffu, bar_test(at(&sm.empty[in]), empty))) {
-                copy_rows(r, which, smem_addr(stage(in)));
+                copy_rows(r, first, which, smem_addr(stage(in)));
                 bar_arrive_copies(at(&sm.landed[in]));
                 ++pending;
                 if (++in == STAGES) {
@@ -358,7 +364,7 @@ struct TileKernel {
                 which ^= 1;
                 if (which == 0) {
                     if (++c.k == c.end) more = next(place, c);
-                    if (more) r = find_rows(c);
+                    if (more) r = find_rows(c, first);
                 }
                 idle = 0;
             }
@@ -378,42 +384,59 @@ struct TileKernel {
         }
     }
 
-    // FP8: the codes run RAWS - 1 blocks ahead.
+    // FP8: warps 14 and 15 copy the codes, half of a block each, as far ahead as
+    // there are slots; warps 8-11 turn what has landed into FP16.  (One warp doing
+    // both in turn had neither under way for long: 1500 cycles a block.)
+    __device__ __forceinline__ void code_loop()
+    {
+        constexpr int RAWS = S::RAWS > 0 ? S::RAWS : 1;
+        uint8_t *const raw = stage(STAGES);
+        const int first = (int)((threadIdx.x >> 5) & 1) * (BN / 2);
+        Place place{0, 0};
+        Piece c;
+        int in = 0;
+        uint32_t parity = 1;
+        while (next(place, c)) {
+#pragma unroll 1
+            for (; c.k < c.end; ++c.k) {
+                const Rows r[2] = {find_rows(c, first), find_rows(c, first + BN / 4)};
+#pragma unroll 1
+                for (int which = 0; which < 2; ++which) {
+                    if (!wait_all(&sm.raw_empty[in], parity)) return;
+                    copy_rows(r[0], first, which, smem_addr(raw + in * S::RAW));
+                    copy_rows(r[1], first + BN / 4, which, smem_addr(raw + in * S::RAW));
+                    bar_arrive_copies(at(&sm.raw_full[in]));
+                    if (++in == RAWS) {
+                        in = 0;
+                        parity ^= 1;
+                    }
+                }
+            }
+        }
+    }
     __device__ __forceinline__ void convert_loop()
     {
         constexpr int RAWS = S::RAWS > 0 ? S::RAWS : 1;
         uint8_t *const raw = stage(STAGES);
-        Place ahead{0, 0}, place{0, 0};
-        Piece src, c;
-        int slot_in = 0, which = 0;
-        bool more = next(ahead, src, true);
-        Rows r{};
-        const auto copy_next = [&]() {
-            if (more) {
-                if (which == 0) r = find_rows(src);
-                copy_rows(r, which, smem_addr(raw + slot_in * S::RAW));
-                if (which == 1 && ++src.k == src.end) more = next(ahead, src, true);
-                which ^= 1;
-            }
-            copy_commit();
-            slot_in = slot_in + 1 == RAWS ? 0 : slot_in + 1;
-        };
-#pragma unroll 1
-        for (int i = 0; i < RAWS - 1; ++i) copy_next();
+        Place place{0, 0};
+        Piece c;
         int slot = 0, to = 0;
-        uint32_t parity = 1;
+        uint32_t landed = 0, empty = 1;
         while (next(place, c)) {
 #pragma unroll 1
             for (int i = 2 * (c.end - c.k); i > 0; --i) {
-                copy_next();                                  // into the slot converted last
-                copy_wait<RAWS - 1>();
-                if (!wait_all(&sm.empty[to], parity)) return;
+                if (!wait_all(&sm.raw_full[slot], landed) || !wait_all(&sm.empty[to], empty)) return;
                 convert(raw + slot * S::RAW, stage(to));
+                __syncwarp();
+                if ((threadIdx.x & 31) == 0) bar_arrive(at(&sm.raw_empty[slot]));
                 ready(&sm.full[to]);
-                slot = slot + 1 == RAWS ? 0 : slot + 1;
+                if (++slot == RAWS) {
+                    slot = 0;
+                    landed ^= 1;
+                }
                 if (++to == STAGES) {
                     to = 0;
-                    parity ^= 1;
+                    empty ^= 1;
                 }
             }
         }
@@ -553,7 +576,7 @@ struct TileKernel {
         w.valid = r < rows;
         const int rr = w.valid ? r : rows - 1, i = p.group.div(rr);
         w.tok = c.tok + i;
-        w.head = c.h * p.group.d + rr - i * p.group.d;
+        w.head = h * p.group.d + rr - i * p.group.d;
         return w;
     }
 
@@ -855,7 +878,11 @@ struct TileKernel {
             }
             for (int i = 0; i < kPieces; ++i) {
                 bar_init(at(&sm.told[i]), 1);
-                bar_init(at(&sm.heard[i]), 4 * NT + 5);
+                bar_init(at(&sm.heard[i]), 4 * NT + (FP8 ? 7 : 5));
+            }
+            for (int i = 0; i < S::RAWS; ++i) {
+                bar_init(at(&sm.raw_full[i]), 64);
+                bar_init(at(&sm.raw_empty[i]), 4);
             }
             bar_init(at(&sm.last), 1);
             sm.failed = 0;
@@ -870,21 +897,19 @@ struct TileKernel {
         bool work;
         if (p.whole) {
             const int nt = (p.n + TT - 1) / TT;
-            const int64_t tiles = (int64_t)p.B * p.Hk * nt;
-            const int ctas = (int)min((int64_t)gridDim.x, tiles);
+            const int64_t tiles = (int64_t)p.B * nt;
+            const int n = (int)min((int64_t)groups, tiles);
             __syncthreads();
-            work = (int)blockIdx.x < ctas;
+            work = group < n;
             if (work) {
-                const int64_t first = first_unit(tiles, ctas, blockIdx.x);
-                const int64_t bh = quotient(first, nt);
-                c.b = (int)quotient(bh, p.Hk);
-                c.h = (int)(bh - (int64_t)c.b * p.Hk);
-                c.t = (int)(first - bh * nt);
+                const int64_t first = first_unit(tiles, n, group);
+                c.b = (int)quotient(first, nt);
+                c.t = (int)(first - (int64_t)c.b * nt);
                 c.nt = nt;
                 c.s = sequence(p, c.b);
                 tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
                 c.k = c.k0;
-                c.left = first_unit(tiles, ctas, blockIdx.x + 1) - first;
+                c.left = first_unit(tiles, n, group + 1) - first;
             }
         } else {
             work = share(c, lane);
@@ -900,18 +925,18 @@ struct TileKernel {
     __device__ __forceinline__ bool share(Walk &c, int lane)
     {
         const Work work = share_work<kTileThreads>(
-            p.B, p.Hk, sm.scratch,
+            p.B, group, sm.scratch,
             [&](int b, int64_t &u, int64_t &t) {
                 const Seq s = sequence(p, b);
                 const int nt = (s.n + TT - 1) / TT;
                 u = blocks_before(BN, s.n, s.m, p.causal, p.window, TT, nt, nt) + (int64_t)nt * kTileCost;
                 t = nt;
             },
-            // A CTA for each tile; tiles are shared out further while that leaves a CTA four units (more than
-            // kTileCost: every CTA has a block).
-            [&](int64_t units, int64_t tiles) { return (int)min((int64_t)gridDim.x, max(tiles, units / 4)); });
-        if ((int)blockIdx.x >= work.ctas) {
-            if (threadIdx.x == 0) st_header(p.ws, blockIdx.x, AttnHeader{});
+            // A group for each tile; tiles are shared out further while that leaves a group four units (more than
+            // kTileCost: every group has a block).
+            [&](int64_t units, int64_t tiles) { return (int)min((int64_t)groups, max(tiles, units / 4)); });
+        if (group >= work.groups) {
+            if (threadIdx.x == 0 && groups > 1) st_header(p.ws, blockIdx.x, AttnHeader{});
             return false;
         }
         c.b = work.b;
@@ -920,9 +945,7 @@ struct TileKernel {
         const auto units_before = [&](int t) {
             return blocks_before(BN, c.s.n, c.s.m, p.causal, p.window, TT, c.nt, t) + (int64_t)t * kTileCost;
         };
-        const int64_t whole = units_before(c.nt);
-        c.h = (int)quotient(work.rest, whole);
-        const int64_t rest = work.rest - c.h * whole;
+        const int64_t rest = work.rest;
         // The tile of unit `rest`: the last with units_before(t) <= rest, 32 places at a time.
         int lo = 0, hi = c.nt;
         while (hi - lo > 1) {
@@ -937,15 +960,15 @@ struct TileKernel {
         const int in = (int)(rest - units_before(c.t)) - kTileCost;      // blocks before u0, or less than none
         c.k = c.k0 + max(in, 0);
         c.left = work.u1 - work.u0 + min(in, 0);
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && groups > 1) {
             AttnHeader hd{};
             hd.first = work.u0 - in;                          // the tile's first block
             hd.last = hd.first + (c.k1 - c.k0);
             hd.units = work.units;
-            hd.ctas = work.ctas;
+            hd.groups = work.groups;
             hd.tile = c.k > c.k0;
             hd.b = c.b;
-            hd.h = c.h;
+            hd.h = h;
             hd.tok = c.s.first + c.t * TT;
             hd.ntok = min(TT, c.s.n - c.t * TT);
             st_header(p.ws, blockIdx.x, hd);
@@ -980,6 +1003,9 @@ struct TileKernel {
                 __syncwarp();
             } else if (warp == 13) {
                 tell_loop(c);
+            } else if (FP8) {
+                code_loop();
+                copy_wait<0>();
             }
         }
     }
@@ -992,7 +1018,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attn_tile(const __grid_cons
     __shared__ typename TileKernel<KIND, DP>::Shared sm;
     CRMSN_DEBUG_ENTER(p.dbg);
     uint8_t *const base = tile_smem + (1024 - (smem_addr(tile_smem) & 1023)) % 1024;
-    TileKernel<KIND, DP> k{p, sm, base, 0, 0};
+    const int group = (int)blockIdx.x / p.Hk;
+    TileKernel<KIND, DP> k{p, sm, base, 0, 0, (int)gridDim.x / p.Hk, group, (int)blockIdx.x - group * p.Hk};
     k.go();
 }
 
@@ -1002,9 +1029,9 @@ cudaError_t run_attn_tile(const AttnParams &p, int sms, cudaStream_t s)
     using S = TileShape<KIND, DP>;
     static std::atomic<int> opted[kOptInDevices];
     if (cudaError_t e = opt_in_smem(k_attn_tile<KIND, DP>, S::SMEM, opted)) return e;
-    const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
-    if (cudaError_t e = launch_pdl(k_attn_tile<KIND, DP>, dim3(ctas), dim3(kTileThreads), S::SMEM, s, p)) return e;
-    return p.whole ? cudaSuccess : launch_attn_combine(p, S::ROWS, DP, ctas, s);
+    const int groups = attn_groups(sms, p.Hk);
+    if (cudaError_t e = launch_pdl(k_attn_tile<KIND, DP>, dim3(groups * p.Hk), dim3(kTileThreads), S::SMEM, s, p)) return e;
+    return p.whole ? cudaSuccess : launch_attn_combine(p, S::ROWS, DP, groups, s);
 }
 
 }  // namespace crmsn
