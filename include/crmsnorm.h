@@ -72,7 +72,7 @@ typedef enum crmsn_status {
     CRMSN_ERR_WORKSPACE = 6,      /* backward workspace too small or misaligned */
     CRMSN_ERR_ALIAS = 7,          /* outputs overlap inputs other than as allowed */
     CRMSN_ERR_CUDA = 8,           /* the CUDA runtime reported an error */
-    CRMSN_ERR_DEVICE_TIMEOUT = 9, /* reserved: the kernels have no device-side waits */
+    CRMSN_ERR_DEVICE_TIMEOUT = 9, /* reserved: no entry point returns it */
     CRMSN_ERR_ARG = 10,           /* eps / scale value out of range */
     CRMSN_ERR_SCRATCH_LIMIT = 11, /* rmsnorm_bwd_noalloc: problem needs more than its built-in scratch */
     CRMSN_ERR_NOT_DEBUG_BUILD = 12 /* crmsn_debug_status: the library has no bounds guard */
@@ -573,7 +573,10 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     CRMSN_ATTENTION_SHORT keys (T / B; table_pages * page_size).
  *   - The outputs may not overlap any input.
  *   - The order of the sums of a row depends on the lengths of all sequences
- *     of the call and on the SM count, and on nothing else.
+ *     of the call, the head counts, the form (the alignment rule above) and the
+ *     SM count, and on nothing else.
+ *   - The waits between the parts of a kernel are bounded (seconds); one that
+ *     ran out, which no call is known to bring about, leaves NaN.
  */
 typedef struct crmsn_attention {
     int64_t T, D, Hq, Hk, B;

@@ -44,7 +44,7 @@ __device__ __forceinline__ int key_hi(const AttnParams &p, const Seq &s, int i)
 }
 __device__ __forceinline__ int key_lo(const AttnParams &p, const Seq &s, int i)
 {
-    return p.window ? max(s.m - s.n + i + 1 - p.window, 0) : 0;
+    return p.window ? (int)max((int64_t)s.m - s.n + i + 1 - p.window, (int64_t)0) : 0;
 }
 
 // Page and row of key j of sequence b (page < 0: a page number out of range,

@@ -9,9 +9,9 @@
 //
 // 16 warps: 0-3 and 4-7 work out the weights of the two halves of a tile, one
 // row a thread, so that a row's maximum and sum never leave the thread; 8-11
-// copy keys and values; warp 12 issues the products; warp 13 walks through the
-// CTA's work and hands it to the others piece by piece.  While one  While one
-// half's weights are worked out, the tensor cores run the other half's
+// copy keys and values (FP8: convert what 14 and 15 copy); 12 issues the
+// products; 13 walks through the CTA's work and tells the others piece by piece.
+// While one half's weights are worked out, the tensor cores run the other half's
 // products: S of the next block follows O of this one at once.  Heads of 256
 // leave no room for two halves in tensor memory (O takes 256 of its 512
 // columns); there one half has two S, and S of the next block runs ahead of O
@@ -21,14 +21,27 @@
 // the true one has passed it by 2^8, as moving it means reading and writing O.
 // A weight is then at most 2^8, its rounding relative as ever.
 //
-// Keys and values: 16-byte asynchronous copies by the copying warps (any page
-// size; what lies behind the last key becomes zeros), into the swizzled layout
-// that the products read.  FP8 caches: each thread copies into slots of its own
-// and turns what arrived into FP16.  The blocks of a tile, and the tiles that a
-// CTA works through, form one stream: loads run ahead across the ends of tiles.
+// Keys and values: 16-byte asynchronous copies (any page size; what lies behind
+// the last key becomes zeros), into the swizzled layout that the products read;
+// FP8 codes to slots of their own, from where they become FP16 (exact).  The
+// blocks of a tile, and the tiles that a CTA works through, form one stream:
+// loads run ahead across the ends of tiles, and so do the next tile's queries.
 //
 // Work is shared out by blocks (share_work): CTAs that meet inside a tile write
 // parts, which attn_combine.cu joins.
+//
+// What it takes (GB300, 32 + 8 heads of 128): 16384 tokens 1501 us, 1465
+// TFLOP/s, 75 % of the measured rate of a large BF16 product; 2048 tokens over
+// 32768 keys in pages of 64, 759 us.  What bounds it: a block of 128 keys takes
+// about 3000 cycles for two halves, whose products alone take 2048.  A half's
+// round (scores, 270 for their maximum, 1200 for the weights, products) is
+// longer than the other half's products; with nothing to load the prompt takes
+// 1389 us, and without a single power of two as long as with them.  A piece's
+// end costs some 4000 cycles, mostly instructions that arrive from the L2 cache:
+// this kernel's code is larger than the SM keeps, and shorter loops at a tile's
+// end were faster than unrolled ones.  Tried and left: the halves of a tile of
+// 128 rows taking every other block (no faster: 222 against 215 us for one chunk
+// among single tokens), results staged in shared memory (a stage of keys less).
 #pragma once
 
 #include "attn.cuh"
@@ -50,15 +63,16 @@ struct TileShape {
     static constexpr int RAWS = FP8 ? (DP == 64 ? 8 : 4) : 0;
     static constexpr int SMEM = 1024 + NT * QBYTES + STAGES * STAGE + RAWS * RAW;
     static constexpr int OCOL = DP == 256 ? 256 : NT * NS * BN;   // columns of S, then of O
+    // Registers of a thread: of the 128 at launch the copying and the issuing
+    // warps give up what the weights' warps need.  (BF16: 16384 tokens 1530 us at
+    // 152, 1450 at 168; FP8, whose copying warps convert: a chunk among single
+    // tokens 210 us at 168, 196 at 152.)
+    static constexpr int REGS = FP8 ? 152 : 168, OTHER_REGS = 256 - REGS;
     static_assert(OCOL + NT * DP <= 512, "tensor memory");
     static_assert(SMEM + 1600 <= 227 * 1024, "shared memory");
 };
 constexpr int kTileThreads = 512;
 constexpr int kTileColumns = 512;
-// Registers of a thread: of the 128 at launch the copying and the issuing
-// warps give up what the weights' warps need.
-constexpr int kWeightRegs = 168, kOtherRegs = 88;
-static_assert(2 * kWeightRegs + 2 * kOtherRegs <= 4 * 128, "registers of the launch");
 
 // sum of floor((a i + b) / m) over 0 <= i < n (the classic Euclid-like
 // reduction of a count of lattice points under a line).
@@ -985,10 +999,10 @@ struct TileKernel {
         if (threadIdx.x == 0) tell(0, c, true);
         __syncwarp();
         if (warp < 8) {
-            more_registers<kWeightRegs>();
+            more_registers<S::REGS>();
             if (warp < 4 * NT) weight_loop(warp >> 2);
         } else {
-            fewer_registers<kOtherRegs>();
+            fewer_registers<S::OTHER_REGS>();
             if (warp < 12) {
                 if constexpr (FP8) convert_loop();
                 else copy_loop();

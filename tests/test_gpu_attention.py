@@ -506,3 +506,100 @@ def test_random_shapes():
         ns = [n] * B if r.random() < 0.6 else [r.choice([1, n]) for _ in range(B)]
         check_paged(g, ns, lens, Hk * G, Hk, D, r.choice([1, 5, 16, 32, 128]), r.choice([BF16, E4M3, E5M2]),
                     r.choice(["token", "head"]), window=window)
+
+
+@pytest.mark.parametrize("Hk,G", [(90, 1), (160, 1), (200, 2)])
+def test_more_key_heads_than_processors(Hk, G):
+    # One group of CTAs, or CTAs beyond those that run at once.
+    q, k, v = heads(gen(Hk), 700, Hk * G, Hk, 64)
+    check_prompt(q, k, v, [130, 570], True)
+    check_prompt(q[:70], k[:70], v[:70], [70], False)
+    check_paged(gen(Hk, 1), [1, 1], [900, 5], Hk * G, Hk, 64)
+
+
+@pytest.mark.parametrize("n", [639, 640, 641])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_around_the_short_form(n, D):
+    g = gen(n, D)
+    for B in (1, 3):
+        q, k, v = (normal(g, B, n, H, D).to(BF16) for H in (4, 2, 2))
+        out = crm.prompt_attention(q, k, v)
+        o, tol, _, _ = attn_ref.prompt(q.flatten(0, 1), k.flatten(0, 1), v.flatten(0, 1), [n] * B)
+        attn_ref.check(out.flatten(0, 1), o, tol)
+    check_paged(g, [1, 1, 1], [n, 7, n // 2], 8, 2, D, dtype=E4M3)
+    check_paged(g, [20, 20], [n, 64], 8, 2, D, page=1)
+
+
+def test_short_calls_of_many_sequences():
+    r = random.Random(2)
+    lens = [r.randint(0, 500) for _ in range(700)]
+    check_paged(gen(1), [1] * 700, lens, 4, 2, 64)
+    check_paged(gen(2), [9] * 60, [r.randint(9, 400) for _ in range(60)], 6, 3, 128)
+    q, k, v = (normal(gen(3), 90, 33, H, 64).to(BF16) for H in (6, 3, 3))
+    o, tol, _, _ = attn_ref.prompt(q.flatten(0, 1), k.flatten(0, 1), v.flatten(0, 1), [33] * 90)
+    attn_ref.check(crm.prompt_attention(q, k, v).flatten(0, 1), o, tol)
+
+
+def test_many_pieces_of_one_half_beside_long_ones():
+    # Long tiles of two halves between many short ones, whose halves a CTA works through at their own pace.
+    ns = [300] + [1, 3, 20] * 60 + [500, 2, 2, 2, 700] + [5] * 90
+    q, k, v = heads(gen(6), sum(ns), 5, 1, 128)
+    check_prompt(q, k, v, ns, True)
+    check_paged(gen(7), ns, [n + 200 for n in ns], 5, 1, 128, dtype=E4M3)
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, 1 << 40, 5000])
+def test_windows_beyond_the_sequence(window):
+    q, k, v = heads(gen(window), 300, 4, 2, 128)
+    a, b = crm.prompt_attention(q, k, v, window=window), crm.prompt_attention(q, k, v)
+    assert torch.equal(a, b)
+    check_paged(gen(1), [40, 40], [10, 300], 4, 2, 128, window=window if window < 1 << 31 else 0)
+
+
+def test_refusals():
+    g = gen(1)
+    q, k, v = heads(g, 20, 4, 2, 128)
+    starts = starts_of([20])
+    kc, vc, table, _, _ = cache(g, [20], 16, 2, 128)
+    lens = torch.tensor([20], dtype=torch.int32, device=DEV)
+    for bad in (dict(starts=starts.long()), dict(starts=starts.cpu()), dict(out=torch.empty(20, 4, 128, device=DEV))):
+        with pytest.raises(TypeError):
+            crm.prompt_attention(q, k, v, **bad)
+    for bad in (dict(k=k[:, :, :64], v=v), dict(k=k[:10], v=v[:10]), dict(k=k, v=v[:, :1])):
+        with pytest.raises(ValueError):
+            crm.prompt_attention(q, **bad)
+    with pytest.raises(ValueError):
+        crm.prompt_attention(q[:, :3], k, v)                              # 3 heads over 2
+    with pytest.raises(ValueError):
+        crm.prompt_attention(q, k, v, lse=torch.empty(20, 3, device=DEV))
+    for bad in (dict(scale=-1.0), dict(window=-1), dict(causal=False, window=4), dict(starts=starts, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(crm.CrmsnError):
+            crm.prompt_attention(q, k, v, **bad)
+    with pytest.raises(crm.CrmsnError):
+        crm.prompt_attention(q, k, v, out=q)                              # not in place
+    with pytest.raises(RuntimeError):
+        crm.prompt_attention(q.clone().requires_grad_(), k, v)
+    with torch.no_grad():
+        crm.prompt_attention(q.clone().requires_grad_(), k, v)
+    for bad in (dict(lens=lens.long()), dict(page_table=table.long()), dict(k_cache=kc.float(), v_cache=vc.float()),
+                dict(k_cache=kc.to(E4M3), v_cache=vc.to(E5M2)), dict(k_cache=kc.to(E4M3), v_cache=vc.to(E4M3))):
+        with pytest.raises(TypeError):
+            crm.paged_attention(**{**dict(q=q, k_cache=kc, v_cache=vc, page_table=table, lens=lens), **bad})
+    for bad in (dict(page_table=table[:0]), dict(page_table=table.repeat(2, 1)), dict(lens=lens[:0]), dict(k_cache=kc[..., :64], v_cache=vc[..., :64]),
+                dict(k_scale=torch.ones(1, device=DEV))):
+        with pytest.raises(ValueError):
+            crm.paged_attention(**{**dict(q=q, k_cache=kc, v_cache=vc, page_table=table, lens=lens), **bad})
+    with pytest.raises(ValueError):
+        crm.paged_attention(q[:19], kc, vc, table.repeat(2, 1), lens.repeat(2))   # 19 tokens over 2 sequences
+
+
+def test_empty_calls():
+    q, k, v = heads(gen(1), 0, 4, 2, 128)
+    assert crm.prompt_attention(q, k, v).shape == (0, 4, 128)
+    q, k, v = heads(gen(1), 9, 4, 2, 128)
+    out = torch.full_like(q.contiguous(), 3.0)
+    crm.prompt_attention(q, k, v, starts=starts_of([]), out=out)              # no sequence
+    assert (out == 3).all()
+    kc = torch.zeros(3, 16, 2, 128, dtype=BF16, device=DEV)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    assert crm.paged_attention(q[:0], kc, kc, none.view(0, 4), none).shape == (0, 4, 128)
