@@ -4,7 +4,9 @@
  * Row-wise RMSNorm forward (plain, fused residual add, Gemma w+1, FP32
  * zero-centred weight), its FP8 epilogues (static scale, 1x128 blocks), the
  * AdaRMSNorm style epilogues, RMSNorm + SiLU, LayerNorm (BF16 and FP8
- * output), and the training backward (dx and a deterministic FP32 dw).
+ * output), the training backward (dx and a deterministic FP32 dw), and what
+ * stands behind the norms in attention: rotary positions, normed queries and
+ * keys, a paged cache, and the attention itself.
  *
  * Sources cited below:
  *   [API]   "flashinfer.norm" API index (docs.flashinfer.ai/api/norm.html)

@@ -3,17 +3,21 @@
 //   M = max M_i,  L = sum L_i 2^(M_i - M),  o = sum O_i 2^(M_i - M) / L.
 //
 // CTA column c looks at the tile in which the work of CTA Hk + c of the
-// attention kernel began, and joins it where its group is the first such one;
-// one warp for each row.  Parts are added in the order of their keys.
+// attention kernel began, and joins it where its group is the first such one.
+// Parts are added in the order of their keys.  A warp takes one row of the few
+// of a decode step, whose many parts bound it, and four of a larger tile, where
+// finding the parts costs as much as a row (8192 tokens, 32 + 8 heads of 128:
+// 21 us with one).
 #include "attn.cuh"
 
 namespace crmsn {
 namespace {
 
 constexpr int kWarps = 8;
+inline int rows_of_warp(int rows) { return rows > kDecodeRows ? 4 : 1; }
 
 template <int KIND, int DP>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_constant__ AttnParams p, int rows)
+__global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_constant__ AttnParams p, int rows, int per)
 {
     constexpr int NV = DP / 64;              // pairs of columns of a lane
     CRMSN_DEBUG_ENTER(p.dbg);
@@ -23,60 +27,63 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_const
     if (!dbg_global(at, (int)sizeof(AttnHeader), false)) return;
     const AttnHeader hd = *at;
     if (!hd.tile || first_unit(hd.units, hd.groups, g - 1) > hd.first) return;
-    const int nrows = hd.ntok * p.group.d;
-    const int r = (int)blockIdx.y * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= nrows) return;
+    const int nrows = hd.ntok * p.group.d, lane = threadIdx.x & 31;
+    const int first = ((int)blockIdx.y * kWarps + (int)(threadIdx.x >> 5)) * per;
+    if (first >= nrows) return;
     const int n = unit_owner(hd.units, hd.groups, hd.last - 1) - g + 2;
+    const float vs = KIND == KV_BF16 ? 1.f : ld_f32_ro(p.scale[1]);
     // The part of the group before is its second (the tile begins there), that of the others their first.
     const auto part = [&](int i) { return part_of(p.ws, c + (i - 1) * p.Hk, i == 0, rows, DP); };
-    float M = -INFINITY, L = 0.f;
-    F2 o[NV];
-    for (int k = 0; k < NV; ++k) o[k] = f2(0.f);
-    for (int base = 0; base < n; base += 32) {
-        float m = -INFINITY, l = 0.f;
-        if (base + lane < n) {
-            const float *ml = part(base + lane) + 2 * r;
-            if (dbg_global(ml, 8, false)) {
-                m = ml[0];
-                l = ml[1];
+#pragma unroll 1
+    for (int r = first; r < min(first + per, nrows); ++r) {
+        float M = -INFINITY, L = 0.f;
+        F2 o[NV];
+        for (int k = 0; k < NV; ++k) o[k] = f2(0.f);
+        for (int base = 0; base < n; base += 32) {
+            float m = -INFINITY, l = 0.f;
+            if (base + lane < n) {
+                const float *ml = part(base + lane) + 2 * r;
+                if (dbg_global(ml, 8, false)) {
+                    m = ml[0];
+                    l = ml[1];
+                }
+            }
+            float top = m;
+            for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            top = fmaxf(top, M);
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float keep = exp2f(M - ref), mine = exp2f(m - ref);
+            M = top;
+            L *= keep;
+            for (int k = 0; k < NV; ++k) o[k] = f2_mul(o[k], f2(keep));
+            const int here = min(32, n - base);
+#pragma unroll 4
+            for (int i = 0; i < here; ++i) {
+                const float w = __shfl_sync(0xffffffffu, mine, i);
+                L = fmaf(__shfl_sync(0xffffffffu, l, i), w, L);
+                const float *v = part(base + i) + 2 * rows + (int64_t)r * DP + 2 * lane;
+                for (int k = 0; k < NV; ++k)
+                    if (dbg_global(v + 64 * k, 8, false))
+                        o[k] = f2_fma(*reinterpret_cast<const float2 *>(v + 64 * k), f2(w), o[k]);
             }
         }
-        float top = m;
-        for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        top = fmaxf(top, M);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float keep = exp2f(M - ref), mine = exp2f(m - ref);
-        M = top;
-        L *= keep;
-        for (int k = 0; k < NV; ++k) o[k] = f2_mul(o[k], f2(keep));
-        const int here = min(32, n - base);
-#pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float w = __shfl_sync(0xffffffffu, mine, i);
-            L = fmaf(__shfl_sync(0xffffffffu, l, i), w, L);
-            const float *v = part(base + i) + 2 * rows + (int64_t)r * DP + 2 * lane;
-            for (int k = 0; k < NV; ++k)
-                if (dbg_global(v + 64 * k, 8, false))
-                    o[k] = f2_fma(*reinterpret_cast<const float2 *>(v + 64 * k), f2(w), o[k]);
+        const int i = p.group.div(r), hq = hd.h * p.group.d + (r - i * p.group.d);
+        const int64_t t = hd.tok + i;
+        const float inv = vs / L;
+        uint16_t *out = const_cast<uint16_t *>(p.out.p) + t * p.out.ld + hq * p.out.hs + 2 * lane;
+        bool odd = false;
+        for (int k = 0; k < NV; ++k) {
+            const F2 y = L == 0.f ? f2(0.f) : f2_mul(o[k], f2(inv));    // no key: zeros, whatever 0 times the values was
+            odd = odd || (2 * lane + 64 * k < p.D && (suspect(y.x, L) || suspect(y.y, L)));
+            if (2 * lane + 64 * k < p.D && dbg_global(out + 64 * k, 4, true))
+                *reinterpret_cast<uint32_t *>(out + 64 * k) = bf16_f2(y);
         }
-    }
-    const int i = p.group.div(r), hq = hd.h * p.group.d + (r - i * p.group.d);
-    const int64_t t = hd.tok + i;
-    const float vs = KIND == KV_BF16 ? 1.f : ld_f32_ro(p.scale[1]);
-    const float inv = vs / L;
-    uint16_t *out = const_cast<uint16_t *>(p.out.p) + t * p.out.ld + hq * p.out.hs + 2 * lane;
-    bool odd = false;
-    for (int k = 0; k < NV; ++k) {
-        const F2 y = L == 0.f ? f2(0.f) : f2_mul(o[k], f2(inv));    // no key: zeros, whatever 0 times the values was
-        odd = odd || (2 * lane + 64 * k < p.D && (suspect(y.x, L) || suspect(y.y, L)));
-        if (2 * lane + 64 * k < p.D && dbg_global(out + 64 * k, 4, true))
-            *reinterpret_cast<uint32_t *>(out + 64 * k) = bf16_f2(y);
-    }
-    if (p.lse && lane == 0) st_f32(p.lse + t * p.out.H + hq, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
-    if (__any_sync(0xffffffffu, odd)) {
-        __syncwarp();                        // the row is written once more, by other lanes
-        const Seq s = sequence(p, hd.b);
-        attend_row<KIND, DP / 32>(p, hd.b, s, (int)(t - s.first), hq, false);
+        if (p.lse && lane == 0) st_f32(p.lse + t * p.out.H + hq, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
+        if (__any_sync(0xffffffffu, odd)) {
+            __syncwarp();                        // the row is written once more, by other lanes
+            const Seq s = sequence(p, hd.b);
+            attend_row<KIND, DP / 32>(p, hd.b, s, (int)(t - s.first), hq, false);
+        }
     }
 }
 
@@ -85,10 +92,10 @@ cudaError_t run(const AttnParams &p, int rows, int DP, dim3 grid, cudaStream_t s
 {
     const dim3 block(kWarps * 32);
     switch (DP) {
-        case 64: return launch_pdl(k_attn_combine<KIND, 64>, grid, block, 0, s, p, rows);
-        case 128: return launch_pdl(k_attn_combine<KIND, 128>, grid, block, 0, s, p, rows);
-        case 192: return launch_pdl(k_attn_combine<KIND, 192>, grid, block, 0, s, p, rows);
-        default: return launch_pdl(k_attn_combine<KIND, 256>, grid, block, 0, s, p, rows);
+        case 64: return launch_pdl(k_attn_combine<KIND, 64>, grid, block, 0, s, p, rows, rows_of_warp(rows));
+        case 128: return launch_pdl(k_attn_combine<KIND, 128>, grid, block, 0, s, p, rows, rows_of_warp(rows));
+        case 192: return launch_pdl(k_attn_combine<KIND, 192>, grid, block, 0, s, p, rows, rows_of_warp(rows));
+        default: return launch_pdl(k_attn_combine<KIND, 256>, grid, block, 0, s, p, rows, rows_of_warp(rows));
     }
 }
 
@@ -97,7 +104,8 @@ cudaError_t run(const AttnParams &p, int rows, int DP, dim3 grid, cudaStream_t s
 cudaError_t launch_attn_combine(const AttnParams &p, int rows, int DP, int groups, cudaStream_t s)
 {
     if (groups < 2) return cudaSuccess;
-    const dim3 grid((groups - 1) * p.Hk, (rows + kWarps - 1) / kWarps);
+    const int rows_of_cta = kWarps * rows_of_warp(rows);
+    const dim3 grid((groups - 1) * p.Hk, (rows + rows_of_cta - 1) / rows_of_cta);
     switch (p.kind) {
         case KV_BF16: return run<KV_BF16>(p, rows, DP, grid, s);
         case KV_E4M3: return run<KV_E4M3>(p, rows, DP, grid, s);
