@@ -98,6 +98,9 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
 // What a tile costs beside its blocks (its queries' and results' ways, the
 // first scores that nothing overlaps), in blocks.
 constexpr int kTileCost = 2;
+// Tiles of a sequence up to which their blocks are added one by one: shorter
+// than the closed form, whose code must arrive first.
+constexpr int kFewTiles = 4;
 
 // The tiles of a sequence: TT tokens each.  Tile t takes the blocks [k0, k1),
 // at least one.
@@ -109,8 +112,8 @@ __device__ __forceinline__ void tile_blocks(const AttnParams &p, const Seq &s, i
     k1 = max((key_hi(p, s, last) + BN - 1) / BN, k0 + 1);
 }
 // Blocks of BN keys of the first t of a sequence's nt tiles, in closed form.
-// (Not inlined: it is called four times, and the start of a small call is the
-// time that its code takes to arrive.)
+// (Not inlined: it is called three times, and the start of a small call is
+// the time that its code takes to arrive.)
 static __device__ __noinline__ int64_t blocks_before(int BN, int n, int m, int causal, int window, int TT, int nt, int t)
 {
     if (t <= 0) return 0;
@@ -943,8 +946,17 @@ struct TileKernel {
             [&](int b, int64_t &u, int64_t &t) {
                 const Seq s = sequence(p, b);
                 const int nt = (s.n + TT - 1) / TT;
-                u = blocks_before(BN, s.n, s.m, p.causal, p.window, TT, nt, nt) + (int64_t)nt * kTileCost;
+                u = (int64_t)nt * kTileCost;
                 t = nt;
+                if (nt > kFewTiles) {
+                    u += blocks_before(BN, s.n, s.m, p.causal, p.window, TT, nt, nt);
+                } else {
+                    for (int i = 0; i < nt; ++i) {
+                        int k0, k1;
+                        tile_blocks<BN>(p, s, TT, i, k0, k1);
+                        u += k1 - k0;
+                    }
+                }
             },
             // A group for each tile; tiles are shared out further while that leaves a group four units (more than
             // kTileCost: every group has a block).
@@ -956,22 +968,38 @@ struct TileKernel {
         c.b = work.b;
         c.s = sequence(p, c.b);
         c.nt = (c.s.n + TT - 1) / TT;
-        const auto units_before = [&](int t) {
-            return blocks_before(BN, c.s.n, c.s.m, p.causal, p.window, TT, c.nt, t) + (int64_t)t * kTileCost;
-        };
+        // The tile of unit `rest`: the last with no more units before it.
         const int64_t rest = work.rest;
-        // The tile of unit `rest`: the last with units_before(t) <= rest, 32 places at a time.
-        int lo = 0, hi = c.nt;
-        while (hi - lo > 1) {
-            const int by = (hi - lo + 31) / 32, t = lo + lane * by;
-            const bool before = t < hi && units_before(t) <= rest;
-            const int n = __popc(__ballot_sync(0xffffffffu, before)) - 1;
-            lo += n * by;
-            hi = min(hi, lo + by);
+        int64_t before;
+        if (c.nt <= 32) {
+            // A lane for each tile.
+            int k0 = 0, k1 = -kTileCost;
+            if (lane < c.nt) tile_blocks<BN>(p, c.s, TT, lane, k0, k1);
+            const int64_t mine = k1 - k0 + kTileCost;
+            int64_t upto = mine;
+            for (int o = 1; o < 32; o *= 2) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            c.t = min(__popc(__ballot_sync(0xffffffffu, upto <= rest)), c.nt - 1);
+            before = __shfl_sync(0xffffffffu, upto - mine, c.t);
+        } else {
+            const auto units_before = [&](int t) {
+                return blocks_before(BN, c.s.n, c.s.m, p.causal, p.window, TT, c.nt, t) + (int64_t)t * kTileCost;
+            };
+            int lo = 0, hi = c.nt;               // 32 places at a time
+            while (hi - lo > 1) {
+                const int by = (hi - lo + 31) / 32, t = lo + lane * by;
+                const bool in = t < hi && units_before(t) <= rest;
+                const int n = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+                lo += n * by;
+                hi = min(hi, lo + by);
+            }
+            c.t = lo;
+            before = units_before(lo);
         }
-        c.t = lo;
         tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
-        const int in = (int)(rest - units_before(c.t)) - kTileCost;      // blocks before u0, or less than none
+        const int in = (int)(rest - before) - kTileCost;      // blocks before u0, or less than none
         c.k = c.k0 + max(in, 0);
         c.left = work.u1 - work.u0 + min(in, 0);
         if (threadIdx.x == 0 && groups > 1) {
