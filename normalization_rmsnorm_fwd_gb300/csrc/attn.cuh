@@ -99,7 +99,9 @@ __device__ __forceinline__ void st_out(uint16_t *p, float v)
 // key by key: lane l holds the elements l, l + 32, ...; masked keys and values
 // are never read.  Running maximum M and sum L in FP32:
 //   M' = max(M, s_j),  L = L 2^(M-M') + 2^(s_j-M'),  o = o 2^(M-M') + 2^(s_j-M') v_j
-template <int KIND, int NE>
+// U keys' loads are under way together (1 where this is a rare call inside
+// another kernel, whose registers it would take).
+template <int KIND, int NE, int U>
 __device__ __noinline__ void attend_row(const AttnParams &p, int b, const Seq &s, int i, int hq, bool with_lse)
 {
     const int lane = threadIdx.x & 31, h = p.group.div(hq);
@@ -120,29 +122,43 @@ __device__ __noinline__ void attend_row(const AttnParams &p, int b, const Seq &s
     }
     const int hi = key_hi(p, s, i);
     float M = -INFINITY, L = 0.f;
-    for (int j = key_lo(p, s, i); j < hi; ++j) {
-        int page, row;
-        locate(p, b, s, j, page, row);
-        const int64_t ko = kv_offset(p.kv[0], page, row, h), vo = kv_offset(p.kv[1], page, row, h);
-        float k[NE], v[NE];
+    for (int j = key_lo(p, s, i); j < hi; j += U) {
+        float k[U][NE], v[U][NE], x[U];
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const int d = lane + 32 * e;
-            const bool in = d < p.D && page >= 0;
-            k[e] = in ? ld_kv<KIND>(p.kv[0], ko + d) : 0.f;
-            v[e] = in ? ld_kv<KIND>(p.kv[1], vo + d) : 0.f;
+        for (int u = 0; u < U; ++u) {
+            int page = -1, row = 0;
+            if (j + u < hi) locate(p, b, s, j + u, page, row);
+            const int64_t ko = kv_offset(p.kv[0], page, row, h), vo = kv_offset(p.kv[1], page, row, h);
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                const int d = lane + 32 * e;
+                const bool in = d < p.D && page >= 0;
+                k[u][e] = in ? ld_kv<KIND>(p.kv[0], ko + d) : 0.f;
+                v[u][e] = in ? ld_kv<KIND>(p.kv[1], vo + d) : 0.f;
+            }
         }
-        float x = 0.f;
+        float M1 = M;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) x = fmaf(q[e], k[e], x);
+        for (int u = 0; u < U; ++u) {
+            x[u] = 0.f;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-        x *= c;
-        const float M1 = fmaxf(M, x), base = M1 == -INFINITY ? 0.f : M1;
-        const float keep = exp2f(M - base), w = exp2f(x - base);
-        L = fmaf(L, keep, w);
+            for (int e = 0; e < NE; ++e) x[u] = fmaf(q[e], k[u][e], x[u]);
 #pragma unroll
-        for (int e = 0; e < NE; ++e) o[e] = fmaf(o[e], keep, w * v[e]);
+            for (int w = 16; w > 0; w >>= 1) x[u] += __shfl_xor_sync(0xffffffffu, x[u], w);
+            x[u] = j + u < hi ? x[u] * c : -INFINITY;
+            M1 = fmaxf(M1, x[u]);
+        }
+        const float base = M1 == -INFINITY ? 0.f : M1, keep = exp2f(M - base);
+        L *= keep;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) o[e] *= keep;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float w = exp2f(x[u] - base);
+            L += w;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) o[e] = fmaf(w, v[u][e], o[e]);
+        }
         M = M1;
     }
     const float r = L == 0.f ? 0.f : vs / L;

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_const
         if (__any_sync(0xffffffffu, odd)) {
             __syncwarp();                        // the row is written once more, by other lanes
             const Seq s = sequence(p, hd.b);
-            attend_row<KIND, DP / 32>(p, hd.b, s, (int)(t - s.first), hq, false);
+            attend_row<KIND, DP / 32, 1>(p, hd.b, s, (int)(t - s.first), hq, false);
         }
     }
 }

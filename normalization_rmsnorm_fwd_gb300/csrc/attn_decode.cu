@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             for (int row = warp; row < R; row += W)
                 if (odd_rows >> row & 1u) {
                     const int i = p.group.div(row);
-                    attend_row<KIND, DP / 32>(p, at.b, at.s, i, h * G + row - i * G, false);
+                    attend_row<KIND, DP / 32, 1>(p, at.b, at.s, i, h * G + row - i * G, false);
                 }
             __syncthreads();
             if (tid == 0) odd_rows = 0;

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_row(const __grid_constant_
         }
         const Seq s = sequence(p, b);
         if (t < s.first || t - s.first >= s.n) continue;       // a row of no sequence stays as it is
-        attend_row<KIND, NE>(p, b, s, t - s.first, hq, true);
+        attend_row<KIND, NE, NE <= 8 ? 4 : 2>(p, b, s, t - s.first, hq, true);
     }
 }
 

@@ -868,7 +868,7 @@ struct TileKernel {
         while (again) {
             const int l = __ffs(again) - 1;
             again &= again - 1;
-            attend_row<KIND, DP / 32>(p, c.b, c.s, __shfl_sync(0xffffffffu, row.tok, l), __shfl_sync(0xffffffffu, row.head, l), false);
+            attend_row<KIND, DP / 32, 1>(p, c.b, c.s, __shfl_sync(0xffffffffu, row.tok, l), __shfl_sync(0xffffffffu, row.head, l), false);
         }
         tc_fence_before();
     }

@@ -150,6 +150,24 @@ def test_prompt_masked_values_do_not_matter(D, bad):
         attn_ref.check(win[rows], o[rows], tol[rows])
 
 
+def test_later_values_do_not_matter_over_many_keys():
+    # Rows worked out again key by key, over a long cache, split among CTAs or not.
+    g = gen(12)
+    kc, vc, table, _, _ = cache(g, [30000], 64, 1, 128)
+    page, row = int(table[0, 29990 // 64]), 29990 % 64
+    vc[page, row] = NAN
+    for n in (4, 100):
+        q = normal(g, n, 4, 128).to(BF16)
+        out = crm.paged_attention(q, kc, vc, table, torch.tensor([30000], dtype=torch.int32, device=DEV))
+        k0, v0 = kc.clone(), vc.clone()
+        v0[page, row] = 0
+        seen = 29990 - (30000 - n)               # tokens that stand before it
+        if seen > 0:
+            o, tol, _, _ = attn_ref.paged(q, k0, v0, table, [30000], [n])
+            attn_ref.check(out[:seen], o[:seen], tol[:seen])
+        assert out[max(seen, 0):].isnan().all()
+
+
 def test_prompt_infinite_values_that_are_seen():
     q, k, v = (t.clone() for t in heads(gen(5), 200, 2, 1, 128))
     v[50, :, 3] = INF
