@@ -571,8 +571,9 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *   - workspace: at least attention_workspace_bytes(D, device) bytes, 256-byte
  *     aligned, any content; scratch that a later call on the same stream may
  *     use again (two calls that may run at the same time need two).  Not used,
- *     and may be NULL, where starts is NULL and no sequence can have more than
- *     CRMSN_ATTENTION_SHORT keys (T / B; table_pages * page_size).
+ *     and may be NULL, where no sequence can have more than
+ *     CRMSN_ATTENTION_SHORT keys (prompt_attention: T, without starts T / B;
+ *     paged_attention: table_pages * page_size).
  *   - The outputs may not overlap any input.
  *   - The order of the sums of a row depends on the lengths of all sequences
  *     of the call, the head counts, the form (the alignment rule above) and the

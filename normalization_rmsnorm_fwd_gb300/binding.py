@@ -768,7 +768,7 @@ def _int32_vector(t, name, n, dev):
 
 def _attention(q, shape, T, Hq, D, Hk, B, keys, dev, starts, scale, causal, window, out, lse, workspace):
     """(out, workspace, the fields of crmsn_attention): what the two attention
-    functions share.  keys: the most that a sequence can have, without starts."""
+    functions share.  keys: the most that a sequence can have."""
     qp = _head_tensor(q, "q", dev, shape)
     if Hk < 1 or Hq % Hk:
         raise ValueError(f"{Hq} query heads are no multiple of {Hk} key heads")
@@ -786,7 +786,7 @@ def _attention(q, shape, T, Hq, D, Hk, B, keys, dev, starts, scale, causal, wind
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous on cuda:{dev}")
         wsp, wsn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif starts is not None or keys > _abi.ATTENTION_SHORT:
+    elif keys > _abi.ATTENTION_SHORT:
         wsn = _lib().attention_workspace_bytes(D, dev)
         workspace = torch.empty(wsn, dtype=torch.uint8, device=q.device)
         wsp = workspace.data_ptr()
@@ -815,7 +815,7 @@ def prompt_attention(q, k, v, starts=None, scale=None, causal: bool = True, wind
         B = starts.shape[0] - 1
     else:
         B = 1 if len(shape) == 3 else math.prod(shape[:-3])
-    out, workspace, packed = _attention(q, shape, T, Hq, D, Hk, B, T // B if B else 0, dev, starts, scale, causal, window, out, lse, workspace)
+    out, workspace, packed = _attention(q, shape, T, Hq, D, Hk, B, T // B if starts is None and B else T, dev, starts, scale, causal, window, out, lse, workspace)
     _enqueue("prompt_attention", dev, _abi.PROMPT_ATTENTION_CALL.pack(*packed, *kp, *vp))
     return out
 

@@ -32,12 +32,12 @@ crmsn_status check_common(const crmsn_attention &a)
     return CRMSN_OK;
 }
 
-// Calls of at most `keys` keys a sequence that need no workspace.
-bool is_short(const crmsn_attention &a, int64_t keys) { return !a.starts && keys <= kShortKeys; }
+// Whether a call whose sequences can have at most `keys` keys needs no workspace.
+bool is_short(int64_t keys) { return keys <= kShortKeys; }
 
 crmsn_status check_workspace(const crmsn_attention &a, int64_t keys)
 {
-    if (is_short(a, keys)) return CRMSN_OK;
+    if (is_short(keys)) return CRMSN_OK;
     if (!a.workspace) return CRMSN_ERR_NULL;
     return a.workspace_bytes == 0 || a.workspace_bytes > (uint64_t)1 << 40 ? CRMSN_ERR_WORKSPACE : CRMSN_OK;
 }
@@ -46,7 +46,7 @@ Region starts_region(const crmsn_attention &a) { return vec_region(a.starts, a.B
 Region lse_region(const crmsn_attention &a) { return vec_region(a.lse, a.T * a.Hq, 4, true); }
 Region ws_region(const crmsn_attention &a, int64_t keys)
 {
-    return vec_region(is_short(a, keys) ? nullptr : a.workspace, (int64_t)a.workspace_bytes, 1, true);
+    return vec_region(is_short(keys) ? nullptr : a.workspace, (int64_t)a.workspace_bytes, 1, true);
 }
 
 // The device, its SM count and the workspace, after everything else.
@@ -54,14 +54,14 @@ crmsn_status check_device(const crmsn_attention &a, int64_t keys, int &sms)
 {
     int dev;
     if (crmsn_status s = device_sms(dev, sms)) return s;
-    if (is_short(a, keys)) return CRMSN_OK;
+    if (is_short(keys)) return CRMSN_OK;
     if (!al(a.workspace, 256) || a.workspace_bytes < attention_workspace_bytes(a.D, dev)) return CRMSN_ERR_WORKSPACE;
     return CRMSN_OK;
 }
 
 void set_common(AttnParams &p, const crmsn_attention &a, int64_t keys)
 {
-    p.whole = is_short(a, keys);
+    p.whole = is_short(keys);
     p.q = view(heads(a.q, a.Hq));
     p.out = view(heads(a.out, a.Hq));
     p.starts = a.starts;
@@ -119,7 +119,7 @@ crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStrea
     if (crmsn_status s = check_common(a)) return s;
     if (a.T == 0 || a.B == 0) return CRMSN_OK;
     const Heads k = heads(call->k, a.Hk), v = heads(call->v, a.Hk);
-    const int64_t keys = a.T / a.B;              // of a sequence, where starts is NULL
+    const int64_t keys = a.starts ? a.T : a.T / a.B;
     if (crmsn_status s = check_workspace(a, keys)) return s;
     if (crmsn_status s = check_heads(k, a.T, a.D)) return s;
     if (crmsn_status s = check_heads(v, a.T, a.D)) return s;

@@ -81,9 +81,8 @@ inline int attn_groups(int sms, int Hk)
 }
 inline int64_t attn_part_floats(int rows, int DP) { return (int64_t)rows * (2 + DP); }
 
-// Sequences of the same number of tokens each and of at most this many keys are
-// dealt out by whole tiles, without a count of the work and without a second
-// kernel.  (A call of 77 tokens 9.0 us instead of 16.2; one token over 517 keys, 8
+// Sequences of at most this many keys are dealt out by whole tiles, without a
+// count of their blocks and without a second kernel.  (A call of 77 tokens 9.0 us instead of 16.2; one token over 517 keys, 8
 // key heads, 9.8 instead of 7.2, but the host's 13.4 instead of 20.3 for one
 // launch and one allocation less.  Each further 128 keys cost 0.6 us.)
 constexpr int kShortKeys = CRMSN_ATTENTION_SHORT;

@@ -912,7 +912,22 @@ struct TileKernel {
         TT = S::ROWS / p.group.d;
         Walk c;
         bool work;
-        if (p.whole) {
+        if (p.whole && p.starts) {
+            // Tiles as units.
+            const Work w = share_work<kTileThreads>(
+                p.B, group, sm.scratch, [&](int b, int64_t &u, int64_t &t) { u = t = (sequence(p, b).n + TT - 1) / TT; },
+                [&](int64_t tiles, int64_t) { return (int)min((int64_t)groups, tiles); });
+            work = group < w.groups;
+            if (work) {
+                c.b = w.b;
+                c.t = (int)w.rest;
+                c.s = sequence(p, c.b);
+                c.nt = (c.s.n + TT - 1) / TT;
+                tile_blocks<BN>(p, c.s, TT, c.t, c.k0, c.k1);
+                c.k = c.k0;
+                c.left = w.u1 - w.u0;
+            }
+        } else if (p.whole) {
             const int nt = (p.n + TT - 1) / TT;
             const int64_t tiles = (int64_t)p.B * nt;
             const int n = (int)min((int64_t)groups, tiles);

@@ -56,11 +56,11 @@ def test_structs_are_the_headers(tmp_path):
                                                   getattr(struct, end).offset]
 
 
-BASE = dict(T=64, D=128, Hq=8, Hk=2, B=4, q=A, ldq=1024, hsq=128, o=A + G, ldo=1024, hso=128, lse=A + 2 * G, starts=A + 3 * G,
+BASE = dict(T=6404, D=128, Hq=8, Hk=2, B=4, q=A, ldq=1024, hsq=128, o=A + G, ldo=1024, hso=128, lse=A + 2 * G, starts=A + 3 * G,
             scale=0.1, causal=1, window=0, ws=A + 4 * G, wsn=1 << 29)
 PROMPT = dict(BASE, k=A + 5 * G, ldk=256, hsk=128, v=A + 6 * G, ldv=256, hsv=128)
 PAGED = dict(BASE, kc=A + 5 * G, kps=4096, kss=256, khs=128, vc=A + 6 * G, vps=4096, vss=256, vhs=128, pages=100, page=16,
-             table=A + 7 * G, ldt=30, tp=30, lens=A + 8 * G, ks=None, vs=None, kind=0, zero=0)
+             table=A + 7 * G, ldt=100, tp=100, lens=A + 8 * G, ks=None, vs=None, kind=0, zero=0)
 
 
 def prompt(L, **kw):
@@ -92,6 +92,14 @@ def test_shared_refusals(L, f):
     assert f(L, o=A, ldo=1024) == ALIAS                                              # not in place
     assert f(L, lse=A + G) == ALIAS and f(L, ws=A + G) == ALIAS and f(L, starts=A + G) == ALIAS and f(L, ws=A) == ALIAS
     assert f(L, D=126) == CUDA and f(L, q=A + 2) == CUDA                             # any layout
+
+
+def test_short_calls_need_no_workspace(L):
+    assert prompt(L, T=640, ws=None, wsn=0) == CUDA and prompt(L, T=641, ws=None) == NULL
+    assert prompt(L, T=2560, starts=None, ws=None) == CUDA and prompt(L, T=2564, starts=None, ws=None) == NULL
+    assert paged(L, tp=40, ws=None, wsn=0) == CUDA and paged(L, tp=41, ws=None) == NULL
+    assert paged(L, tp=40, starts=None, ws=None) == CUDA
+    assert prompt(L, T=640, o=A + G, ws=A + G) == CUDA            # not used: not looked at
 
 
 def test_prompt_refusals(L):

@@ -590,11 +590,12 @@ def test_refusals():
         crm.prompt_attention(q[:, :3], k, v)                              # 3 heads over 2
     with pytest.raises(ValueError):
         crm.prompt_attention(q, k, v, lse=torch.empty(20, 3, device=DEV))
-    for bad in (dict(scale=-1.0), dict(window=-1), dict(causal=False, window=4), dict(starts=starts, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))):
+    for bad in (dict(scale=-1.0), dict(window=-1), dict(causal=False, window=4), dict(out=q)):
         with pytest.raises(crm.CrmsnError):
             crm.prompt_attention(q, k, v, **bad)
+    long = heads(g, 700, 4, 2, 128)
     with pytest.raises(crm.CrmsnError):
-        crm.prompt_attention(q, k, v, out=q)                              # not in place
+        crm.prompt_attention(*long, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(RuntimeError):
         crm.prompt_attention(q.clone().requires_grad_(), k, v)
     with torch.no_grad():
@@ -621,3 +622,17 @@ def test_empty_calls():
     kc = torch.zeros(3, 16, 2, 128, dtype=BF16, device=DEV)
     none = torch.empty(0, dtype=torch.int32, device=DEV)
     assert crm.paged_attention(q[:0], kc, kc, none.view(0, 4), none).shape == (0, 4, 128)
+
+
+@pytest.mark.parametrize("G", [1, 5])
+def test_short_ragged_calls(G):
+    r = random.Random(G)
+    for i in range(8):
+        ns = [r.choice([0, 0, 1, 2, 30, 90]) for _ in range(r.choice([1, 5, 40, 700]))]
+        while sum(ns) > 640:
+            ns[r.randrange(len(ns))] = 0
+        q, k, v = heads(gen(i, G), sum(ns), 2 * G, 2, 64)
+        if sum(ns):
+            check_prompt(q, k, v, ns, True, window=r.choice([0, 20]))
+        ns = [r.choice([0, 1, 1, 7, 60]) for _ in range(r.choice([3, 50]))]
+        check_paged(gen(i, G), ns, [n + r.randint(0, 400) for n in ns], 2 * G, 2, 128, dtype=r.choice([BF16, E4M3]))
