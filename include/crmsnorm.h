@@ -628,8 +628,8 @@ crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStrea
  * Entries behind a sequence's last key are not read.  A page number outside
  * [0, num_pages) reads as keys and values of zeros; a length is taken as
  * within [0, table_pages * page_size].  An FP8 element stands for its value
- * times k_scale or v_scale.  num_pages * page_size and table_pages * page_size
- * are below 2^31 - 2^20.
+ * times k_scale or v_scale (any finite numbers).  num_pages * page_size and
+ * table_pages * page_size are below 2^31 - 2^20.
  */
 crmsn_status paged_attention(const crmsn_paged_attention_call *call, cudaStream_t stream);
 

@@ -4,6 +4,8 @@
 // Scores are kept times log2(e), so that every exponential is a power of two.
 #pragma once
 
+#include <cfloat>
+
 #include "attn.h"
 
 namespace crmsn {
@@ -377,5 +379,17 @@ __device__ __forceinline__ float scaled(float x, int e)
     const int a = e / 2, b = e - a;
     return x * __int_as_float((127 + a) << 23) * __int_as_float((127 + b) << 23);
 }
+// Such a row's factor from products of queries and codes to scores: |c| 2^-e,
+// c = scale * k_scale; c's sign goes into the queries (score_sign), so that
+// masked places stay -infinity.  At least FLT_MIN, for the same reason: 0 times
+// -infinity is NaN.  (Products are below 2^36: with a factor at or below FLT_MIN
+// all scores are nothing beside 1.)
+__device__ __forceinline__ float score_factor(float c, int e)
+{
+    const float f = fabsf(scaled(c, -e));
+    return f < FLT_MIN ? FLT_MIN : f;
+}
+// What turns the signs of a packed FP16 pair.
+__device__ __forceinline__ uint32_t score_sign(float c) { return c < 0.f ? 0x80008000u : 0u; }
 
 }  // namespace crmsn

@@ -264,15 +264,16 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
                 a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, w));
             }
             const int e0 = row_exponent(a0), e1 = row_exponent(a1);
+            const uint32_t sign = score_sign(c0);
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = i & 1 ? e1 : e0;
-                    qa[k][i] = pack_f16(scaled(bf_lo(qa[k][i]), e), scaled(bf_hi(qa[k][i]), e));
+                    qa[k][i] = pack_f16(scaled(bf_lo(qa[k][i]), e), scaled(bf_hi(qa[k][i]), e)) ^ sign;
                 }
-            c0 = scaled(c0, -e0);
-            c1 = scaled(c1, -e1);
+            c0 = score_factor(c0, e0);
+            c1 = score_factor(c1, e1);
         }
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {

@@ -617,8 +617,8 @@ struct TileKernel {
         copy_commit();
     }
     // They have arrived (FP8: and become FP16, each thread what it copied).
-    // Returns the exponent by which this lane's row was scaled.
-    __device__ __forceinline__ int queries_here(int half) const
+    // Returns the exponent by which this lane's row was scaled.  sign: score_sign.
+    __device__ __forceinline__ int queries_here(int half, uint32_t sign) const
     {
         copy_wait<0>();
         int mine = 0;
@@ -636,7 +636,7 @@ struct TileKernel {
                 for (int o = 1; o < LANES; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const int e = row_exponent(top), there = __shfl_sync(0xffffffffu, e, (lane % RPI) * LANES);
                 if (lane / RPI == i) mine = there;
-                const auto f16 = [&](uint32_t x) { return pack_f16(scaled(bf_lo(x), e), scaled(bf_hi(x), e)); };
+                const auto f16 = [&](uint32_t x) { return pack_f16(scaled(bf_lo(x), e), scaled(bf_hi(x), e)) ^ sign; };
                 if (chunk < CH) put16(at, f16(v.x), f16(v.y), f16(v.z), f16(v.w));
             }
         }
@@ -688,7 +688,7 @@ struct TileKernel {
             while (any && !used(nx, half)) any = next(place, nx);
             if (any && good) {
                 if (!copied) copy_queries(nx, half);
-                e = queries_here(half);
+                e = queries_here(half, FP8 ? score_sign(c_all) : 0u);
             }
             if (have) {
                 if (good) good = wait_all(&sm.o[half], (cnt - 1) & 1);
@@ -700,7 +700,7 @@ struct TileKernel {
             have = true;
             copied = false;
             row = row_of(c, half);
-            scale = FP8 ? scaled(c_all, -e) : c_all;
+            scale = FP8 ? score_factor(c_all, e) : c_all;
             M = -INFINITY;
             L = 0.f;
             int hk = key_hi(p, c.s, row.tok) - c.k * BN, lk = key_lo(p, c.s, row.tok) - c.k * BN;    // seen: [lk, hk) of the block
