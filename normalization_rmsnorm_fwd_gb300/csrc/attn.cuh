@@ -364,6 +364,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 
+// FP8 caches: weights in FP16, whose smallest number is 2^-24.  They are held
+// times a power of two, so that they reach 2^12: a small one is off by at most
+// 2^-37 of the largest (2^-29 where the reference may lag by 2^8), and what
+// many small ones add up to is kept.  (Up to 2^15 would fit; the rest is room
+// for the exponent's rounding, 4 at scores of 2^26.)  The factor is part of the
+// reference, and so of the sums.
+constexpr int kWeightTop = 12;
+
 // FP8 caches: queries in FP16.  A row is scaled by 2^e so that its largest
 // element lies in [2^11, 2^12): the elements down to 2^-28 of it keep all
 // their bits, and smaller ones are off by at most 2^-25, 2^-36 of the largest.

@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
     constexpr bool QS = DP >= 192;
     uint32_t q_regs[QS ? 1 : DP / 16][4];
     uint4 *const q_place = reinterpret_cast<uint4 *>(join_o + warp * kDecodeRows * DP) + lane;
+    constexpr float UP = KIND == KV_BF16 ? 0.f : kWeightTop;  // weights are 2^(x - (m - UP))
     float o[DP / 8][4], m0, m1, l0, l1, c0, c1, vs = 1.f, ks = 1.f;
     int hi0, hi1, lo0, lo1, hi_all = 0, lo_all = 0;
     if (KIND != KV_BF16) {
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             m0 = t0;
             m1 = t1;
         }
-        const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+        const float z0 = m0 == -INFINITY ? 0.f : m0 - UP, z1 = m1 == -INFINITY ? 0.f : m1 - UP;
         uint32_t pa[KB / 16][4];      // the weights: BF16 (FP8 caches: FP16) operands of the product with the values
 #pragma unroll
         for (int b = 0; b < KB / 8; ++b) {
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             }
             if (q4 == 0) {
                 float *ml = join_ml + (warp * kDecodeRows + row) * 2;
-                ml[0] = half ? m1 : m0;
+                ml[0] = (half ? m1 : m0) - UP;
                 ml[1] = half ? l1 : l0;
             }
         }

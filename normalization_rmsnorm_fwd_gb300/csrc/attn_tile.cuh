@@ -18,8 +18,8 @@
 // of this one.
 //
 // The reference M of a row's weights is a maximum of before; it moves only when
-// the true one has passed it by 2^8, as moving it means reading and writing O.
-// A weight is then at most 2^8, its rounding relative as ever.
+// the true one has passed it by 2^kLag, as moving it means reading and writing O.
+// A weight is then at most 2^8 (FP16: 2^kWeightTop), its rounding relative as ever.
 //
 // Keys and values: 16-byte asynchronous copies (any page size; what lies behind
 // the last key becomes zeros), into the swizzled layout that the products read;
@@ -71,6 +71,7 @@ struct TileShape {
     static_assert(OCOL + NT * DP <= 512, "tensor memory");
     static_assert(SMEM + 1600 <= 227 * 1024, "shared memory");
 };
+constexpr int kLag = 8;              // binary digits by which a row's reference may lag behind its maximum
 constexpr int kTileThreads = 512;
 constexpr int kTileColumns = 512;
 
@@ -671,6 +672,12 @@ struct TileKernel {
         return lo <= 0 ? up : lo >= 32 ? 0u : up & ~((1u << lo) - 1u);
     }
 
+    // What weights are relative to (kWeightTop), with M a raw score.
+    static __device__ __forceinline__ float reference(float M, float scale)
+    {
+        return FP8 ? fmaf(M, scale, (float)(kLag - kWeightTop)) : M * scale;
+    }
+
     __device__ __forceinline__ void weight_loop(int half)
     {
         const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;       // lane 32 (warp % 4), in bits 16 up
@@ -693,7 +700,7 @@ struct TileKernel {
             if (have) {
                 if (good) good = wait_all(&sm.o[half], (cnt - 1) & 1);
                 tc_fence_after();
-                finish(c, half, row, M * scale, L, vs, lanes, good);
+                finish(c, half, row, reference(M, scale), L, vs, lanes, good);
             }
             if (!any) return;
             c = nx;
@@ -756,7 +763,7 @@ struct TileKernel {
                     if (!good) break;
                     tc_fence_after();
                 }
-                if (__builtin_expect(__any_sync(0xffffffffu, (most - M) * scale > 8.f || M == -INFINITY), 0)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, (most - M) * scale > kLag || M == -INFINITY), 0)) {
                     const float keep = M == -INFINITY || most == M ? 1.f : exp2_fast((M - most) * scale);
                     L *= keep;
                     if (begun && __any_sync(0xffffffffu, keep != 1.f)) {
@@ -774,7 +781,7 @@ struct TileKernel {
                     M = most;
                 }
                 begun = true;
-                const float ref = M == -INFINITY ? 0.f : -M * scale;
+                const float ref = M == -INFINITY ? 0.f : -reference(M, scale);
                 F2 sum = f2(0.f), sum1 = f2(0.f);
                 // The weights of 32 keys take 16 columns: they replace scores that have been read.  The next 32 scores
                 // are on their way meanwhile.

@@ -53,3 +53,31 @@ def test_negative_scales(dtype, D, n):
         o, tol, l, ltol = attn_ref.paged(q, kc, vc, table, lens, [n] * 3, k_scale, v_scale)
         attn_ref.check(out, o, tol)
         attn_ref.check(lse, l, ltol, "lse")
+
+
+# ---------------------------------------------------------------- weights --
+
+@pytest.mark.parametrize("dtype", [E4M3, E5M2])
+@pytest.mark.parametrize("D", [64, 100, 128, 192, 256])
+@pytest.mark.parametrize("n,m", [(1, 600), (1, 100001), (40, 100001)])
+def test_small_weights_add_up_over_fp8(dtype, D, n, m):
+    # One key that takes nearly all, of value 0, before keys of weight exp(-18) = 2^-25.97 and value 1.
+    page = 64
+    pages = -(-m // page)
+    kc = torch.zeros(pages, page, 1, D, device=DEV)
+    vc = torch.ones(pages, page, 1, D, device=DEV)
+    kc[0, 0], vc[0, 0] = 1.0, 0.0
+    q = torch.full((n, 2, D), 16.0 / D, dtype=BF16, device=DEV)
+    scale = 18.0 / float((q[0, 0].double()).sum())
+    one = torch.ones(1, device=DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    out = crm.paged_attention(q, kc.to(dtype), vc.to(dtype), table, int32(m), scale=scale, k_scale=one, v_scale=one)
+    # Weights relative to the largest: w = exp(-18), their FP16 rounding off by at most 2^-29 (half a step of FP16's
+    # smallest numbers, 2^-25, where the largest weight is 2^4 or more) or by 2^-11 of w, the exponential by 2^-17 (scores
+    # of 18 in FP32, exponents of 26); sums of m terms by m 2^-24 of themselves; the result by 2^-8.
+    w = math.exp(-18.0)
+    for i in range(n):
+        seen = m - n + i                       # of value 1
+        want = seen * w / (1 + seen * w)
+        tol = seen * max(2.0 ** -29, 2.0 ** -11 * w) + want * (2.0 ** -16 + seen * 2.0 ** -23 + 2.0 ** -8)
+        assert ((out[i].double() - want).abs() <= tol).all(), (i, out[i, 0, 0].item(), want, tol)
