@@ -578,9 +578,12 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *   - The order of the sums of a row depends on the lengths of all sequences
  *     of the call, the head counts, the form (the alignment rule above) and the
  *     SM count, and on nothing else.
- *   - A row whose result is not finite although its sum is (an infinite or NaN
- *     value beside its keys) is worked out again key by key, about 11 us for
- *     each key of 32 such rows.
+ *   - Infinite and NaN values that a row sees reach its result as they are
+ *     (times a weight that FP32 rounds to 0: NaN) and cost no time worth
+ *     mentioning.  A row that does not see one which a neighbour does (a later
+ *     token's, or one before its window; up to 256 rows share their keys) is
+ *     worked out again key by key, about 11 us for each key of 32 such rows;
+ *     over an E5M2 cache with infinities, a row that sees one as well.
  *   - The waits between the parts of a kernel are bounded (about 6 s); one that
  *     ran out leaves NaN.  Only such rows over more than some 500,000 keys can
  *     keep a kernel that long.

@@ -164,6 +164,7 @@ __device__ __noinline__ void attend_row(const AttnParams &p, int b, const Seq &s
         M = M1;
     }
     const float r = L == 0.f ? 0.f : vs / L;
+    __syncwarp();                                 // behind what other lanes have stored of the row before
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
         const int d = lane + 32 * e;
@@ -175,10 +176,91 @@ __device__ __noinline__ void attend_row(const AttnParams &p, int b, const Seq &s
 
 // A row's result that is not finite although its sum is: a value that the row
 // does not see may have met its weight 0 in a matrix product (0 inf = NaN).
-// Such a row is worked out again key by key.
 __device__ __forceinline__ bool suspect(float o, float L)
 {
     return !(fabsf(o) < INFINITY) && L > 0.f && L < INFINITY;
+}
+
+// The first and the last of the keys [from, to) of sequence b whose values for
+// key head h are not all finite, or (INFINITE) some infinite; x > y: none, and
+// none too once a key of [all_from, all_to) has nothing but NaN.  By a whole
+// warp, in the forms whose rows are whole 16-byte pieces.
+template <int KIND, bool INFINITE>
+__device__ __noinline__ int2 bad_values(const AttnParams &p, int b, const Seq &s, int h, int from, int to, int all_from, int all_to)
+{
+    constexpr int U = INFINITE ? 1 : 2;           // loads under way together
+    const int lane = threadIdx.x & 31, chunks = p.D * (KIND == KV_BF16 ? 2 : 1) / 16;
+    const int rows = 32 / chunks, sub = lane / chunks;
+    const uint32_t row_lanes = chunks == 32 ? ~0u : ((1u << chunks) - 1u) << (sub * chunks & 31);
+    int first = 0x7fffffff, last = -1;
+#pragma unroll 1
+    for (int64_t j0 = from; j0 < to; j0 += U * rows) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t j = j0 + u * rows + sub;
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (sub >= rows || j >= to) continue;
+            int page, row;
+            locate(p, b, s, (int)j, page, row);
+            if (page < 0) continue;
+            const uint8_t *at = p.kv[1].p + kv_offset(p.kv[1], page, row, h) * (KIND == KV_BF16 ? 2 : 1) + (lane - sub * chunks) * 16;
+            if (dbg_global(at, 16, false)) v[u] = __ldg(reinterpret_cast<const uint4 *>(at));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = (int)(j0 + u * rows + sub);
+            uint32_t bad = 0, nan = ~0u;
+            for (const uint32_t x : {v[u].x, v[u].y, v[u].z, v[u].w}) {
+                if constexpr (KIND == KV_BF16) bad |= __vcmpeq2(x & 0x7f807f80u, 0x7f807f80u);
+                else if constexpr (KIND == KV_E4M3) bad |= __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                else if constexpr (INFINITE) bad |= __vcmpeq4(x & 0x7f7f7f7fu, 0x7c7c7c7cu);
+                else bad |= __vcmpgeu4(x & 0x7f7f7f7fu, 0x7c7c7c7cu);
+                if constexpr (INFINITE) nan &= __vcmpgtu4(x & 0x7f7f7f7fu, 0x7c7c7c7cu);
+            }
+            if (bad) {
+                first = min(first, j);
+                last = max(last, j);
+            }
+            if constexpr (INFINITE) {
+                const uint32_t full = __ballot_sync(0xffffffffu, nan == ~0u && j >= all_from && j < all_to);
+                if (__any_sync(0xffffffffu, sub < rows && (full & row_lanes) == row_lanes)) return make_int2(0x7fffffff, -1);
+            }
+        }
+    }
+    return make_int2(__reduce_min_sync(0xffffffffu, first), __reduce_max_sync(0xffffffffu, last));
+}
+
+// Each lane's row (token t of sequence b, query head hq of key head h), where it
+// is suspect, is worked out again key by key if it has to be.  The tile of the
+// tokens [tok, tok + ntok) loaded the keys that any of them sees: a result stands
+// if no value among those that the row does not see, at most ntok - 1 on either
+// side, is bad.  (Without this look, one bad value that all rows see would have
+// all of them worked out again: 1.2 s for a prompt of 16384 tokens.)  Over E5M2 a
+// weight that FP16 rounds to 0 turns an infinite value that the row does see
+// into NaN as well; there the seen values are looked through too, up to one of
+// nothing but NaN.  (No other kind needs that: E4M3 has no infinity, and BF16
+// weights reach down to 2^-126.)
+template <int KIND, int NE>
+__device__ __noinline__ void work_out_again(const AttnParams &p, int b, int h, int tok, int ntok, int t, int hq, bool suspect)
+{
+    constexpr int kNone = 0x7fffffff;
+    const Seq s = sequence(p, b);
+    const int i = t - s.first;
+    const int lo = key_lo(p, s, i), hi = key_hi(p, s, i);
+    const int first_hi = __reduce_min_sync(0xffffffffu, suspect ? hi : kNone), last_lo = __reduce_max_sync(0xffffffffu, suspect ? lo : 0);
+    const int above = bad_values<KIND, false>(p, b, s, h, first_hi, key_hi(p, s, tok - s.first + ntok - 1), 0, 0).y;
+    const int below = bad_values<KIND, false>(p, b, s, h, key_lo(p, s, tok - s.first), last_lo, 0, 0).x;
+    bool again = above >= hi || below < lo;
+    if (KIND == KV_E5M2) {
+        const int first_lo = __reduce_min_sync(0xffffffffu, suspect ? lo : kNone), last_hi = __reduce_max_sync(0xffffffffu, suspect ? hi : 0);
+        const int2 at = bad_values<KIND, true>(p, b, s, h, first_lo, last_hi, last_lo, first_hi);
+        again = again || (at.x < hi && at.y >= lo);
+    }
+    for (uint32_t rows = __ballot_sync(0xffffffffu, again && suspect); rows; rows &= rows - 1) {
+        const int l = __ffs(rows) - 1;
+        attend_row<KIND, NE, 1>(p, b, s, __shfl_sync(0xffffffffu, i, l), __shfl_sync(0xffffffffu, hq, l), false);
+    }
 }
 
 // ------------------------------------------------------------- work split --

@@ -16,8 +16,12 @@ namespace {
 constexpr int kWarps = 8;
 inline int rows_of_warp(int rows) { return rows > kDecodeRows ? 2 : 1; }
 
+// CTAs of an SM, which the rare calls' registers would cost (a small chunk in
+// E5M2 with heads of 64: 46.3 us instead of 42.0).
+constexpr int ctas(int DP) { return DP == 64 ? 5 : DP <= 192 ? 4 : 3; }
+
 template <int KIND, int DP>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_constant__ AttnParams p, int rows, int per)
+__global__ void __launch_bounds__(kWarps * 32, ctas(DP)) k_attn_combine(const __grid_constant__ AttnParams p, int rows, int per)
 {
     constexpr int NV = DP / 64;              // pairs of columns of a lane
     CRMSN_DEBUG_ENTER(p.dbg);
@@ -79,11 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_combine(const __grid_const
                 *reinterpret_cast<uint32_t *>(out + 64 * k) = bf16_f2(y);
         }
         if (p.lse && lane == 0) st_f32(p.lse + t * p.out.H + hq, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
-        if (__any_sync(0xffffffffu, odd)) {
-            __syncwarp();                        // the row is written once more, by other lanes
-            const Seq s = sequence(p, hd.b);
-            attend_row<KIND, DP / 32, 1>(p, hd.b, s, (int)(t - s.first), hq, false);
-        }
+        if (__any_sync(0xffffffffu, odd)) work_out_again<KIND, DP / 32>(p, hd.b, hd.h, hd.tok, hd.ntok, (int)t, hq, lane == 0);
     }
 }
 

@@ -502,11 +502,11 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
         }
         __syncthreads();
         if (whole && odd_rows) {
-            for (int row = warp; row < R; row += W)
-                if (odd_rows >> row & 1u) {
-                    const int i = p.group.div(row);
-                    attend_row<KIND, DP / 32, 1>(p, at.b, at.s, i, h * G + row - i * G, false);
-                }
+            // A warp takes every W-th row.
+            const bool mine = lane % W == warp && (odd_rows >> lane & 1u);
+            const int i = p.group.div(lane);
+            if (__any_sync(0xffffffffu, mine))
+                work_out_again<KIND, DP / 32>(p, at.b, h, at.s.first, p.n, at.s.first + i, h * G + lane - i * G, mine);
             __syncthreads();
             if (tid == 0) odd_rows = 0;
             __syncthreads();

@@ -871,12 +871,8 @@ struct TileKernel {
                     if (quad[j] && dbg_global(quad[j] + done, 16, true))
                         *reinterpret_cast<uint4 *>(quad[j] + done) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
-        uint32_t again = __ballot_sync(0xffffffffu, whole && row.valid && !(odd.x == 0.f && odd.y == 0.f) && L > 0.f && L < INFINITY);
-        while (again) {
-            const int l = __ffs(again) - 1;
-            again &= again - 1;
-            attend_row<KIND, DP / 32, 1>(p, c.b, c.s, __shfl_sync(0xffffffffu, row.tok, l), __shfl_sync(0xffffffffu, row.head, l), false);
-        }
+        const bool again = whole && row.valid && !(odd.x == 0.f && odd.y == 0.f) && L > 0.f && L < INFINITY;
+        if (__any_sync(0xffffffffu, again)) work_out_again<KIND, DP / 32>(p, c.b, h, c.s.first + c.tok, c.ntok, (int)t, row.head, again);
         tc_fence_before();
     }
 

@@ -81,3 +81,95 @@ def test_small_weights_add_up_over_fp8(dtype, D, n, m):
         want = seen * w / (1 + seen * w)
         tol = seen * max(2.0 ** -29, 2.0 ** -11 * w) + want * (2.0 ** -16 + seen * 2.0 ** -23 + 2.0 ** -8)
         assert ((out[i].double() - want).abs() <= tol).all(), (i, out[i, 0, 0].item(), want, tol)
+
+
+# ------------------------------------------------------ values not finite --
+
+def microseconds(f, n):
+    f()
+    best = math.inf
+    for _ in range(3):
+        torch.cuda.synchronize()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(n):
+            f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1000 / n)
+    return best
+
+
+@pytest.mark.parametrize("D,Hq,Hk", [(128, 32, 8), (64, 8, 8), (256, 8, 4)])
+@pytest.mark.parametrize("window", [0, 500])
+def test_a_value_that_rows_see_costs_no_time(D, Hq, Hk, window):
+    # Rows that see it cannot be anything but not finite: nothing is worked out again for them.
+    q, k, v = heads(gen(D), 2048, Hq, Hk, D)
+    bad = v.clone()
+    bad[0] = NAN
+    clean = microseconds(lambda: crm.prompt_attention(q, k, v, window=window), 5)
+    out = crm.prompt_attention(q, k, bad, window=window)
+    last = window or 2048
+    assert out[:last].isnan().all() and not out[last:].isnan().any()
+    # (Twice the time, not the hundredfold of rows worked out one by one; rows beside a window's edge are.)
+    if not window:
+        assert microseconds(lambda: crm.prompt_attention(q, k, bad), 5) < 2 * clean + 100
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, E5M2])
+@pytest.mark.parametrize("n", [1, 4])
+def test_a_bad_slot_of_a_long_cache_costs_no_time(dtype, n):
+    g = gen(n)
+    kc, vc, table, ks, vs = cache(g, [20000], 64, 8, 128, dtype)
+    q = normal(g, n, 32, 128).to(BF16)
+    bad = vc.clone()
+    bad[int(table[0, 3]), 5] = NAN
+    f = lambda c: crm.paged_attention(q, kc, c, table, int32(20000), k_scale=ks, v_scale=vs)
+    assert f(bad).isnan().all() and f(vc).isfinite().all()
+    assert microseconds(lambda: f(bad), 5) < 2 * microseconds(lambda: f(vc), 5) + 100
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, E5M2])
+@pytest.mark.parametrize("D,G,causal,window", [(128, 4, True, 0), (128, 4, True, 40), (64, 1, True, 0), (64, 1, True, 300), (256, 2, True, 40),
+                                               (192, 3, True, 0), (128, 4, False, 0)])
+@pytest.mark.parametrize("n,m", [(4, 200), (4, 3000), (100, 700), (300, 3000), (300, 200)])
+def test_columns_are_finite_where_no_seen_value_is_bad(dtype, D, G, causal, window, n, m):
+    # Bad values here and there, also among the new tokens: a result is NaN exactly where a key that the row sees has one
+    # in its column.
+    g = gen(D, G, n, m, window)
+    Hk = 2
+    kc, vc, table, ks, vs = cache(g, [m], 16, Hk, D, dtype)
+    for j in (0, m // 3, m - n // 2 - 1, m - 2, m - 1):
+        vc[int(table[0, j // 16]), j % 16, j % Hk, (7 * j) % D] = NAN
+    q = normal(g, n, G * Hk, D).to(BF16)
+    how = dict(causal=causal, window=window)
+    out = crm.paged_attention(q, kc, vc, table, int32(m), k_scale=ks, v_scale=vs, **how)
+    values = attn_ref.cached(vc, table[0], m, vs)                             # [m, Hk, D]
+    see = attn_ref.visible(n, m, causal, window, DEV).to(torch.float64)
+    has = torch.einsum("nm,mhd->nhd", see, values.isnan().to(torch.float64)) > 0
+    assert torch.equal(out.isnan(), has.repeat_interleave(G, 1))
+    o, tol, _, _ = attn_ref.sequence(q, attn_ref.cached(kc, table[0], m, ks), torch.nan_to_num(values, 0.0),
+                                     half=2.0 ** -8 if dtype == BF16 else 2.0 ** -11, **how)
+    keep = ~out.isnan()
+    attn_ref.check(out[keep], o[keep], tol[keep])
+
+
+@pytest.mark.parametrize("n", [1, 4, 60])
+@pytest.mark.parametrize("m", [300, 5000])
+@pytest.mark.parametrize("dtype", [BF16, E5M2])
+def test_infinite_values_of_small_weight(dtype, n, m):
+    # exp(-25) = 2^-36 of the largest weight, and 2^-50: below what a 16-bit weight may hold, and still infinite.
+    D, page = 128, 16
+    pages = -(-m // page)
+    kc, vc = torch.zeros(pages, page, 1, D, device=DEV), torch.ones(pages, page, 1, D, device=DEV)
+    kc[0, 0] = 1.0
+    vc[0, 1, 0, 3], vc[0, 2, 0, 4], vc[1, 0, 0, 5] = INF, -INF, NAN
+    vc[2, 0, 0, 6], vc[2, 1, 0, 6] = INF, -INF
+    q = torch.full((n, 2, D), 1.0, dtype=BF16, device=DEV)
+    one = torch.ones(1, device=DEV) if dtype != BF16 else None
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    for s in (25.0, 35.0):
+        out = crm.paged_attention(q, kc.to(dtype), vc.to(dtype), table, int32(m), scale=s / D, k_scale=one, v_scale=one)
+        assert (out[..., 3] == INF).all() and (out[..., 4] == -INF).all() and out[..., 5:7].isnan().all()
+        rest = [d for d in range(D) if not 3 <= d <= 6]
+        assert ((out[..., rest].double() - 1).abs() <= 2.0 ** -7).all()
