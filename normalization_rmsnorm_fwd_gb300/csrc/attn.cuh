@@ -181,66 +181,104 @@ __device__ __forceinline__ bool suspect(float o, float L)
     return !(fabsf(o) < INFINITY) && L > 0.f && L < INFINITY;
 }
 
-// The first and the last of the keys [from, to) of sequence b whose values for
-// key head h are not all finite, or (INFINITE) some infinite; x > y: none, and
-// none too once a key of [all_from, all_to) has nothing but NaN.  By a whole
-// warp, in the forms whose rows are whole 16-byte pieces.
-template <int KIND, bool INFINITE>
-__device__ __noinline__ int2 bad_values(const AttnParams &p, int b, const Seq &s, int h, int from, int to, int all_from, int all_to)
+// Elements of four 16-byte words' worth of values that are not finite, infinite,
+// or NaN: ones in their place.
+enum { V_BAD, V_INFINITE, V_NAN };
+template <int KIND, int WHAT>
+__device__ __forceinline__ uint32_t flags_of(uint32_t x)
 {
-    constexpr int U = INFINITE ? 1 : 2;           // loads under way together
-    const int lane = threadIdx.x & 31, chunks = p.D * (KIND == KV_BF16 ? 2 : 1) / 16;
-    const int rows = 32 / chunks, sub = lane / chunks;
-    const uint32_t row_lanes = chunks == 32 ? ~0u : ((1u << chunks) - 1u) << (sub * chunks & 31);
-    int first = 0x7fffffff, last = -1;
+    if constexpr (KIND == KV_BF16) {
+        x &= 0x7fff7fffu;
+        return WHAT == V_BAD ? __vcmpgeu2(x, 0x7f807f80u) : WHAT == V_NAN ? __vcmpgtu2(x, 0x7f807f80u) : __vcmpeq2(x, 0x7f807f80u);
+    } else if constexpr (KIND == KV_E4M3) {
+        return WHAT == V_INFINITE ? 0u : __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    } else {
+        x &= 0x7f7f7f7fu;
+        return WHAT == V_BAD ? __vcmpgeu4(x, 0x7c7c7c7cu) : WHAT == V_NAN ? __vcmpgtu4(x, 0x7c7c7c7cu) : __vcmpeq4(x, 0x7c7c7c7cu);
+    }
+}
+template <int KIND, int WHAT>
+__device__ __forceinline__ uint4 flags_of(uint4 v)
+{
+    return make_uint4(flags_of<KIND, WHAT>(v.x), flags_of<KIND, WHAT>(v.y), flags_of<KIND, WHAT>(v.z), flags_of<KIND, WHAT>(v.w));
+}
+// 16 bytes of the values of key j, from byte `at` on (the forms whose rows are
+// whole 16-byte pieces); zeros if its page is out of range.
+template <int KIND>
+__device__ __forceinline__ uint4 values_of(const AttnParams &p, int b, const Seq &s, int h, int j, int at)
+{
+    int page, row;
+    locate(p, b, s, j, page, row);
+    if (page < 0) return make_uint4(0, 0, 0, 0);
+    const uint8_t *v = p.kv[1].p + kv_offset(p.kv[1], page, row, h) * (KIND == KV_BF16 ? 2 : 1) + at;
+    return dbg_global(v, 16, false) ? __ldg(reinterpret_cast<const uint4 *>(v)) : make_uint4(0, 0, 0, 0);
+}
+
+// The first and the last of the keys [from, to) of sequence b whose values for
+// key head h are not all finite, or (V_INFINITE) some infinite; first > last:
+// none.  columns: their columns, in lane l those of piece l modulo the pieces of
+// a row.  V_INFINITE: none, too, once a key of [all_from, all_to) has nothing
+// but NaN.  By a whole warp.
+struct BadValues {
+    int first, last;
+    uint4 columns;
+};
+template <int KIND, int WHAT>
+__device__ __noinline__ BadValues bad_values(const AttnParams &p, int b, const Seq &s, int h, int from, int to, int all_from, int all_to)
+{
+    constexpr int U = WHAT == V_INFINITE ? 1 : 2; // loads under way together
+    const int lane = threadIdx.x & 31, pieces = p.D * (KIND == KV_BF16 ? 2 : 1) / 16;
+    const int rows = 32 / pieces, sub = lane / pieces, piece = lane - sub * pieces;
+    const uint32_t row_lanes = pieces == 32 ? ~0u : ((1u << pieces) - 1u) << (sub * pieces & 31);
+    BadValues r{0x7fffffff, -1, {0, 0, 0, 0}};
 #pragma unroll 1
     for (int64_t j0 = from; j0 < to; j0 += U * rows) {
         uint4 v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t j = j0 + u * rows + sub;
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (sub >= rows || j >= to) continue;
-            int page, row;
-            locate(p, b, s, (int)j, page, row);
-            if (page < 0) continue;
-            const uint8_t *at = p.kv[1].p + kv_offset(p.kv[1], page, row, h) * (KIND == KV_BF16 ? 2 : 1) + (lane - sub * chunks) * 16;
-            if (dbg_global(at, 16, false)) v[u] = __ldg(reinterpret_cast<const uint4 *>(at));
+            v[u] = sub < rows && j < to ? values_of<KIND>(p, b, s, h, (int)j, piece * 16) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = (int)(j0 + u * rows + sub);
-            uint32_t bad = 0, nan = ~0u;
-            for (const uint32_t x : {v[u].x, v[u].y, v[u].z, v[u].w}) {
-                if constexpr (KIND == KV_BF16) bad |= __vcmpeq2(x & 0x7f807f80u, 0x7f807f80u);
-                else if constexpr (KIND == KV_E4M3) bad |= __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                else if constexpr (INFINITE) bad |= __vcmpeq4(x & 0x7f7f7f7fu, 0x7c7c7c7cu);
-                else bad |= __vcmpgeu4(x & 0x7f7f7f7fu, 0x7c7c7c7cu);
-                if constexpr (INFINITE) nan &= __vcmpgtu4(x & 0x7f7f7f7fu, 0x7c7c7c7cu);
+            const uint4 f = flags_of<KIND, WHAT>(v[u]);
+            if (f.x | f.y | f.z | f.w) {
+                r.first = min(r.first, j);
+                r.last = max(r.last, j);
+                r.columns = make_uint4(r.columns.x | f.x, r.columns.y | f.y, r.columns.z | f.z, r.columns.w | f.w);
             }
-            if (bad) {
-                first = min(first, j);
-                last = max(last, j);
-            }
-            if constexpr (INFINITE) {
-                const uint32_t full = __ballot_sync(0xffffffffu, nan == ~0u && j >= all_from && j < all_to);
-                if (__any_sync(0xffffffffu, sub < rows && (full & row_lanes) == row_lanes)) return make_int2(0x7fffffff, -1);
+            if constexpr (WHAT == V_INFINITE) {
+                const uint4 n = flags_of<KIND, V_NAN>(v[u]);
+                const uint32_t full = __ballot_sync(0xffffffffu, (n.x & n.y & n.z & n.w) == ~0u && j >= all_from && j < all_to);
+                if (__any_sync(0xffffffffu, sub < rows && (full & row_lanes) == row_lanes)) return {0x7fffffff, -1, {0, 0, 0, 0}};
             }
         }
     }
-    return make_int2(__reduce_min_sync(0xffffffffu, first), __reduce_max_sync(0xffffffffu, last));
+    r.first = __reduce_min_sync(0xffffffffu, r.first);
+    r.last = __reduce_max_sync(0xffffffffu, r.last);
+    const uint4 mine = r.columns;
+    for (int i = 0; i < rows; ++i) {
+        const int l = i * pieces + piece;
+        r.columns.x |= __shfl_sync(0xffffffffu, mine.x, l);
+        r.columns.y |= __shfl_sync(0xffffffffu, mine.y, l);
+        r.columns.z |= __shfl_sync(0xffffffffu, mine.z, l);
+        r.columns.w |= __shfl_sync(0xffffffffu, mine.w, l);
+    }
+    return r;
 }
 
 // Each lane's row (token t of sequence b, query head hq of key head h), where it
 // is suspect, is worked out again key by key if it has to be.  The tile of the
 // tokens [tok, tok + ntok) loaded the keys that any of them sees: a result stands
 // if no value among those that the row does not see, at most ntok - 1 on either
-// side, is bad.  (Without this look, one bad value that all rows see would have
-// all of them worked out again: 1.2 s for a prompt of 16384 tokens.)  Over E5M2 a
-// weight that FP16 rounds to 0 turns an infinite value that the row does see
-// into NaN as well; there the seen values are looked through too, up to one of
-// nothing but NaN.  (No other kind needs that: E4M3 has no infinity, and BF16
-// weights reach down to 2^-126.)
+// side, is bad, or if the last key that it does see has NaN in all columns of
+// such values.  (So a bad value that all rows see, and values that are NaN
+// throughout, cost this look and no more; worked out again, a prompt of 16384
+// tokens takes 1.2 s.)  Over E5M2 a weight that FP16 rounds to 0 turns an
+// infinite value that the row does see into NaN as well; there the seen values
+// are looked through too, up to one of nothing but NaN.  (No other kind needs
+// that: E4M3 has no infinity, and BF16 weights reach down to 2^-126.)
 template <int KIND, int NE>
 __device__ __noinline__ void work_out_again(const AttnParams &p, int b, int h, int tok, int ntok, int t, int hq, bool suspect)
 {
@@ -249,16 +287,29 @@ __device__ __noinline__ void work_out_again(const AttnParams &p, int b, int h, i
     const int i = t - s.first;
     const int lo = key_lo(p, s, i), hi = key_hi(p, s, i);
     const int first_hi = __reduce_min_sync(0xffffffffu, suspect ? hi : kNone), last_lo = __reduce_max_sync(0xffffffffu, suspect ? lo : 0);
-    const int above = bad_values<KIND, false>(p, b, s, h, first_hi, key_hi(p, s, tok - s.first + ntok - 1), 0, 0).y;
-    const int below = bad_values<KIND, false>(p, b, s, h, key_lo(p, s, tok - s.first), last_lo, 0, 0).x;
-    bool again = above >= hi || below < lo;
+    const BadValues above = bad_values<KIND, V_BAD>(p, b, s, h, first_hi, key_hi(p, s, tok - s.first + ntok - 1), 0, 0);
+    const BadValues below = bad_values<KIND, V_BAD>(p, b, s, h, key_lo(p, s, tok - s.first), last_lo, 0, 0);
+    bool seen = false;
     if (KIND == KV_E5M2) {
         const int first_lo = __reduce_min_sync(0xffffffffu, suspect ? lo : kNone), last_hi = __reduce_max_sync(0xffffffffu, suspect ? hi : 0);
-        const int2 at = bad_values<KIND, true>(p, b, s, h, first_lo, last_hi, last_lo, first_hi);
-        again = again || (at.x < hi && at.y >= lo);
+        const BadValues at = bad_values<KIND, V_INFINITE>(p, b, s, h, first_lo, last_hi, last_lo, first_hi);
+        seen = at.first < hi && at.last >= lo;
     }
-    for (uint32_t rows = __ballot_sync(0xffffffffu, again && suspect); rows; rows &= rows - 1) {
-        const int l = __ffs(rows) - 1;
+    const bool unseen = above.last >= hi || below.first < lo;
+    const int lane = threadIdx.x & 31;
+    const bool piece = lane < p.D * (KIND == KV_BF16 ? 2 : 1) / 16;
+    int looked = -1;
+    bool covered = false;
+    for (uint32_t rows = __ballot_sync(0xffffffffu, (seen || unseen) && suspect); rows; rows &= rows - 1) {
+        const int l = __ffs(rows) - 1, last = __shfl_sync(0xffffffffu, hi, l) - 1;
+        if (last != looked) {
+            uint4 n = make_uint4(0, 0, 0, 0);
+            if (piece) n = flags_of<KIND, V_NAN>(values_of<KIND>(p, b, s, h, last, lane * 16));
+            covered = __all_sync(0xffffffffu, !piece || (((above.columns.x | below.columns.x) & ~n.x) | ((above.columns.y | below.columns.y) & ~n.y) |
+                                                         ((above.columns.z | below.columns.z) & ~n.z) | ((above.columns.w | below.columns.w) & ~n.w)) == 0);
+            looked = last;
+        }
+        if (covered && !__shfl_sync(0xffffffffu, seen, l)) continue;
         attend_row<KIND, NE, 1>(p, b, s, __shfl_sync(0xffffffffu, i, l), __shfl_sync(0xffffffffu, hq, l), false);
     }
 }

@@ -173,3 +173,30 @@ def test_infinite_values_of_small_weight(dtype, n, m):
         assert (out[..., 3] == INF).all() and (out[..., 4] == -INF).all() and out[..., 5:7].isnan().all()
         rest = [d for d in range(D) if not 3 <= d <= 6]
         assert ((out[..., rest].double() - 1).abs() <= 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hk", [(128, 32, 8), (64, 8, 8), (256, 8, 4)])
+@pytest.mark.parametrize("columns", [slice(None), slice(5, 6)])
+def test_values_that_are_nan_throughout_cost_no_time(D, Hq, Hk, columns):
+    # A row sees its own key: what is NaN in all keys is NaN in all results, whatever lies beside.
+    q, k, v = heads(gen(D), 2048, Hq, Hk, D)
+    bad = v.clone()
+    bad[..., columns] = NAN
+    out, clean = crm.prompt_attention(q, k, bad), crm.prompt_attention(q, k, v)
+    has = torch.zeros(D, dtype=torch.bool, device=DEV)
+    has[columns] = True
+    assert torch.equal(out.isnan(), has.expand_as(out))
+    assert torch.equal(out[..., ~has], clean[..., ~has])
+    assert microseconds(lambda: crm.prompt_attention(q, k, bad), 5) < 2 * microseconds(lambda: crm.prompt_attention(q, k, v), 5) + 100
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, E5M2])
+@pytest.mark.parametrize("n", [1, 4, 60])
+def test_a_cache_of_nan_costs_no_time(dtype, n):
+    g = gen(n)
+    kc, vc, table, ks, vs = cache(g, [20000], 64, 8, 128, dtype)
+    q = normal(g, n, 32, 128).to(BF16)
+    bad = torch.full_like(vc.float(), NAN).to(dtype)
+    f = lambda c: crm.paged_attention(q, kc, c, table, int32(20000), k_scale=ks, v_scale=vs)
+    assert f(bad).isnan().all() and f(vc).isfinite().all()
+    assert microseconds(lambda: f(bad), 5) < 2 * microseconds(lambda: f(vc), 5) + 100
