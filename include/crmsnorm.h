@@ -585,8 +585,7 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     worked out again key by key, about 11 us for each key of 32 such rows;
  *     over an E5M2 cache with infinities, a row that sees one as well.
  *   - The waits between the parts of a kernel are bounded (about 6 s); one that
- *     ran out leaves NaN.  Only such rows over more than some 500,000 keys can
- *     keep a kernel that long.
+ *     ran out leaves NaN.  Rows are worked out again where nothing waits.
  */
 typedef struct crmsn_attention {
     int64_t T, D, Hq, Hk, B;

@@ -4,6 +4,7 @@
 // launch.
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "api_tensors.h"
 #include "attn.h"
@@ -76,6 +77,10 @@ void set_common(AttnParams &p, const crmsn_attention &a, int64_t keys)
     p.qk_scale = a.scale * 1.44269504f;
     p.lse = a.lse;
     p.ws = static_cast<uint8_t *>(a.workspace);
+#ifdef CRMSN_DEBUG
+    const char *tries = std::getenv("CRMSN_DEBUG_WAIT_TRIES");
+    p.wait_tries = tries ? std::atoi(tries) : 0;
+#endif
 }
 
 // What the tiled kernels want: 16-byte accesses and a head that they hold.

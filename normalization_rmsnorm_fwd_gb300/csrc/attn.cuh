@@ -181,8 +181,7 @@ __device__ __forceinline__ bool suspect(float o, float L)
     return !(fabsf(o) < INFINITY) && L > 0.f && L < INFINITY;
 }
 
-// Elements of four 16-byte words' worth of values that are not finite, infinite,
-// or NaN: ones in their place.
+// Elements of a word that are not finite, infinite, or NaN: ones in their place.
 enum { V_BAD, V_INFINITE, V_NAN };
 template <int KIND, int WHAT>
 __device__ __forceinline__ uint32_t flags_of(uint32_t x)
@@ -268,6 +267,19 @@ __device__ __noinline__ BadValues bad_values(const AttnParams &p, int b, const S
     return r;
 }
 
+// Whether a row of results, written by this CTA before a barrier, holds a value
+// that is not finite.
+__device__ __forceinline__ bool not_finite(const uint16_t *out, int D)
+{
+    uint32_t bad = 0;
+    for (int d = 0; d < D; d += 8) {
+        if (!dbg_global(out + d, 16, false)) continue;
+        const uint4 f = flags_of<KV_BF16, V_BAD>(*reinterpret_cast<const uint4 *>(out + d));
+        bad |= f.x | f.y | f.z | f.w;
+    }
+    return bad != 0;
+}
+
 // Each lane's row (token t of sequence b, query head hq of key head h), where it
 // is suspect, is worked out again key by key if it has to be.  The tile of the
 // tokens [tok, tok + ntok) loaded the keys that any of them sees: a result stands
@@ -279,6 +291,8 @@ __device__ __noinline__ BadValues bad_values(const AttnParams &p, int b, const S
 // infinite value that the row does see into NaN as well; there the seen values
 // are looked through too, up to one of nothing but NaN.  (No other kind needs
 // that: E4M3 has no infinity, and BF16 weights reach down to 2^-126.)
+// Kernels call this last: nothing waits for its warps, and no register is live
+// across it.
 template <int KIND, int NE>
 __device__ __noinline__ void work_out_again(const AttnParams &p, int b, int h, int tok, int ntok, int t, int hq, bool suspect)
 {

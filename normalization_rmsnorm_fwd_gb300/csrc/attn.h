@@ -53,6 +53,7 @@ struct AttnParams {
     uint8_t *ws;
 #ifdef CRMSN_DEBUG
     DebugRanges dbg;
+    int wait_tries;              // of a wait inside a kernel (0: as ever)
 #endif
 };
 

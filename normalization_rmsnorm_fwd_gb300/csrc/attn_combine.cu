@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas(DP)) k_attn_combine(const __
     const float vs = KIND == KV_BF16 ? 1.f : ld_f32_ro(p.scale[1]);
     // The part of the group before is its second (the tile begins there), that of the others their first.
     const auto part = [&](int i) { return part_of(p.ws, c + (i - 1) * p.Hk, i == 0, rows, DP); };
+    uint32_t odd_rows = 0;
 #pragma unroll 1
     for (int r = first; r < min(first + per, nrows); ++r) {
         float M = -INFINITY, L = 0.f;
@@ -83,7 +84,11 @@ __global__ void __launch_bounds__(kWarps * 32, ctas(DP)) k_attn_combine(const __
                 *reinterpret_cast<uint32_t *>(out + 64 * k) = bf16_f2(y);
         }
         if (p.lse && lane == 0) st_f32(p.lse + t * p.out.H + hq, L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718f);
-        if (__any_sync(0xffffffffu, odd)) work_out_again<KIND, DP / 32>(p, hd.b, hd.h, hd.tok, hd.ntok, (int)t, hq, lane == 0);
+        if (__any_sync(0xffffffffu, odd)) odd_rows |= 1u << (r - first);
+    }
+    if (odd_rows) {
+        const int r = first + lane, i = p.group.div(r);
+        work_out_again<KIND, DP / 32>(p, hd.b, hd.h, hd.tok, hd.ntok, hd.tok + i, hd.h * p.group.d + r - i * p.group.d, odd_rows >> lane & 1u);
     }
 }
 

@@ -87,6 +87,10 @@ struct Cursor {
     int b, k, k0, k1;
     Seq s;
 };
+struct Begin {
+    Cursor at;
+    int items;
+};
 template <int UNIT>
 __device__ __forceinline__ void step(const AttnParams &p, Cursor &c)
 {
@@ -98,6 +102,29 @@ __device__ __forceinline__ void step(const AttnParams &p, Cursor &c)
     c.k = c.k0;
 }
 
+// The rows of the tiles that the CTA had whole, once more where a result is not
+// finite: a warp for each tile.
+template <int KIND, int DP>
+__device__ __noinline__ void look_again(const AttnParams &p, const Begin &begin)
+{
+    using S = Shape<KIND, DP>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.group.d, R = p.n * G, h = (int)blockIdx.x % p.Hk;
+    Cursor c = begin.at;
+    int items = begin.items;
+    for (int tile = 0;; ++tile) {
+        const int n = min(c.k1 - c.k, items);
+        if (n == c.k1 - c.k0 && tile % S::W == warp) {
+            const int row = lane < R ? lane : 0, i = p.group.div(row), t = c.s.first + i, hq = h * G + row - i * G;
+            const bool suspect = lane < R && not_finite(p.out.p + (int64_t)t * p.out.ld + hq * p.out.hs, p.D);
+            if (__any_sync(0xffffffffu, suspect)) work_out_again<KIND, DP / 32>(p, c.b, h, c.s.first, p.n, t, hq, suspect);
+        }
+        items -= n;
+        if (items <= 0) return;
+        c.k = c.k1 - 1;
+        step<S::UNIT>(p, c);
+    }
+}
+
 template <int KIND, int DP>
 __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(const __grid_constant__ AttnParams p)
 {
@@ -105,7 +132,8 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
     constexpr int W = S::W, KB = S::KB, NS = S::NS, CH = S::CH, UNIT = S::UNIT;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ WorkScratch scratch;
-    __shared__ uint32_t odd_rows;
+    __shared__ int odd;                                       // some result is not finite
+    __shared__ Begin begin;
     float *const join_o = reinterpret_cast<float *>(smem);                        // [W][16][DP], permuted (turn)
     float *const join_ml = join_o + W * kDecodeRows * DP;                 // [W][16][2]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -120,7 +148,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
     int items;
     int64_t tile_first = 0, u0 = 0;   // units where the current tile begins, where this CTA does
     const int groups = (int)gridDim.x / p.Hk, group = (int)blockIdx.x / p.Hk, h = (int)blockIdx.x - group * p.Hk;
-    if (tid == 0) odd_rows = 0;
+    if (tid == 0) odd = 0;
     if (p.whole) {
         const int n = min(groups, p.B);
         if (group >= n) return;
@@ -172,6 +200,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
         }
     }
 
+    if (tid == 0) begin = {at, items};
     // ---- copies: slot 2 i holds the keys, slot 2 i + 1 the values of item i
     Cursor src = at;
     int copied = 0, slot_in = 0;      // slots copied, and where the next goes
@@ -487,7 +516,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
                 a = L == 0.f ? f2(0.f) : f2_mul(a, f2(inv));  // no key: zeros, whatever 0 times the values was
                 b = L == 0.f ? f2(0.f) : f2_mul(b, f2(inv));
                 if (d < p.D) {
-                    if (suspect(a.x, L) || suspect(a.y, L) || suspect(b.x, L) || suspect(b.y, L)) atomicOr(&odd_rows, 1u << row);
+                    if (suspect(a.x, L) || suspect(a.y, L) || suspect(b.x, L) || suspect(b.y, L)) odd = 1;
                     st_u32x2(const_cast<uint16_t *>(p.out.p) + t * p.out.ld + hq * p.out.hs + d, bf16_f2(a), bf16_f2(b));
                 }
                 if (d == 0 && p.lse)
@@ -501,16 +530,6 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
             }
         }
         __syncthreads();
-        if (whole && odd_rows) {
-            // A warp takes every W-th row.
-            const bool mine = lane % W == warp && (odd_rows >> lane & 1u);
-            const int i = p.group.div(lane);
-            if (__any_sync(0xffffffffu, mine))
-                work_out_again<KIND, DP / 32>(p, at.b, h, at.s.first, p.n, at.s.first + i, h * G + lane - i * G, mine);
-            __syncthreads();
-            if (tid == 0) odd_rows = 0;
-            __syncthreads();
-        }
         if (item + 1 < items) {
             tile_first += at.k1 - at.k0;
             step<UNIT>(p, at);
@@ -518,6 +537,7 @@ __global__ void __launch_bounds__(Shape<KIND, DP>::W * 32, 1) k_attn_decode(cons
         }
     }
     copy_wait<0>();
+    if (odd) look_again<KIND, DP>(p, begin);                  // (the barrier behind the last tile's results)
 }
 
 template <int KIND, int DP>

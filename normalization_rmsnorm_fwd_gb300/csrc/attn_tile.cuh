@@ -69,7 +69,8 @@ struct TileShape {
     // tokens 210 us at 168, 196 at 152.)
     static constexpr int REGS = FP8 ? 152 : 168, OTHER_REGS = 256 - REGS;
     static_assert(OCOL + NT * DP <= 512, "tensor memory");
-    static_assert(SMEM + 1600 <= 227 * 1024, "shared memory");
+    static constexpr int STATIC = 2048;                      // for what is not dynamic
+    static_assert(SMEM + STATIC <= 227 * 1024, "shared memory");
 };
 constexpr int kLag = 8;              // binary digits by which a row's reference may lag behind its maximum
 constexpr int kTileThreads = 512;
@@ -183,6 +184,24 @@ struct __align__(16) Piece {
 enum { PIECE_BEGINS = 1, PIECE_ENDS = 2, PIECE_NONE = 4 };   // the tile's first block, its last; no piece: the end
 constexpr int kPieces = 8;
 
+// The rows of the pieces that are whole tiles, once more where a result is not
+// finite: 32 rows a warp.
+template <int KIND, int DP>
+__device__ __noinline__ void look_again(const AttnParams &p, const Walk &begin)
+{
+    using S = TileShape<KIND, DP>;
+    const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * 32, G = p.group.d, TT = S::ROWS / G, h = (int)blockIdx.x % p.Hk;
+    Walk c = begin;
+    do {
+        const int tok = c.s.first + c.t * TT, ntok = min(TT, c.s.n - c.t * TT), rows = ntok * G;
+        if (c.k == c.k0 && c.end == c.k1 && first < rows) {
+            const int row = min(first + lane, rows - 1), i = p.group.div(row), t = tok + i, hq = h * G + row - i * G;
+            const bool suspect = first + lane < rows && not_finite(p.out.p + (int64_t)t * p.out.ld + hq * p.out.hs, p.D);
+            if (__any_sync(0xffffffffu, suspect)) work_out_again<KIND, DP / 32>(p, c.b, h, tok, ntok, t, hq, suspect);
+        }
+    } while (walk_on<S::BN>(p, TT, c));
+}
+
 template <int KIND, int DP>
 struct TileKernel {
     using S = TileShape<KIND, DP>;
@@ -194,8 +213,10 @@ struct TileKernel {
         Piece piece[kPieces];
         uint64_t full[STAGES], empty[STAGES], landed[STAGES], raw_full[S::RAWS + 1], raw_empty[S::RAWS + 1], q[NT], s[NT * NS], w[NT * NS][2], o[NT], last, told[kPieces], heard[kPieces];
         uint32_t tmem;
-        volatile int failed;
+        volatile int failed, odd;    // a wait ran out; some result is not finite
+        Walk begin;
     };
+    static_assert(sizeof(Shared) <= S::STATIC, "shared memory");
 
     const AttnParams &p;
     Shared &sm;
@@ -205,7 +226,18 @@ struct TileKernel {
     const int groups, group, h;      // of Hk CTAs each, this CTA's, its head
 
     static __device__ __forceinline__ uint32_t at(const uint64_t *bar) { return smem_addr(bar); }
-    __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity) { return bar_wait(at(bar), parity, &sm.failed); }
+    // How often a wait tries.  (The debug build can be told to give up early.)
+    __device__ __forceinline__ int tries() const
+    {
+#ifdef CRMSN_DEBUG
+        if (p.wait_tries > 0) return p.wait_tries;
+#endif
+        return kWaitTries;
+    }
+    __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity)
+    {
+        return bar_wait(at(bar), parity, &sm.failed, tries());
+    }
     // The same for a whole warp that goes on together.
     __device__ __forceinline__ bool wait_all(const uint64_t *bar, uint32_t parity)
     {
@@ -395,7 +427,7 @@ struct TileKernel {
                 --pending;
                 idle = 0;
             }
-            if (++idle > 256 && (__any_sync(0xffffffffu, sm.failed) || idle > kWaitTries)) {
+            if (++idle > 256 && (__any_sync(0xffffffffu, sm.failed) || idle > tries())) {
                 sm.failed = 1;
                 return;
             }
@@ -872,7 +904,7 @@ struct TileKernel {
                         *reinterpret_cast<uint4 *>(quad[j] + done) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
         const bool again = whole && row.valid && !(odd.x == 0.f && odd.y == 0.f) && L > 0.f && L < INFINITY;
-        if (__any_sync(0xffffffffu, again)) work_out_again<KIND, DP / 32>(p, c.b, h, c.s.first + c.tok, c.ntok, (int)t, row.head, again);
+        if (again) sm.odd = 1;
         tc_fence_before();
     }
 
@@ -905,7 +937,7 @@ struct TileKernel {
                 bar_init(at(&sm.raw_empty[i]), 4);
             }
             bar_init(at(&sm.last), 1);
-            sm.failed = 0;
+            sm.failed = sm.odd = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         if (warp == 12) tmem_alloc(smem_addr(&sm.tmem), kTileColumns);
@@ -1042,11 +1074,16 @@ struct TileKernel {
         tc_fence_after();
         tmem = uniform(sm.tmem);
         walk_end(p, c);
-        if (threadIdx.x == 0) tell(0, c, true);
+        if (threadIdx.x == 0) {
+            sm.begin = c;
+            tell(0, c, true);
+        }
         __syncwarp();
         if (warp < 8) {
             more_registers<S::REGS>();
             if (warp < 4 * NT) weight_loop(warp >> 2);
+            asm volatile("bar.sync 1, 256;" ::: "memory");    // all results are written
+            if (sm.odd) look_again<KIND, DP>(p, sm.begin);
         } else {
             fewer_registers<S::OTHER_REGS>();
             if (warp < 12) {

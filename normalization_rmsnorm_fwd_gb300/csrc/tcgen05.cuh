@@ -36,15 +36,13 @@ __device__ __forceinline__ void bar_arrive_copies(uint32_t bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
 }
-// Waits for the phase of that parity, at most kWaitTries tries (about 6 s: a
-// warp that works 32 rows of a long sequence out again key by key keeps the
-// others waiting: 11 us for each key).  False: it, or another wait of the CTA
-// (*failed), ran out.
+// Waits for the phase of that parity, at most `tries` tries (kWaitTries took
+// about 6 s).  False: it, or another wait of the CTA (*failed), ran out.
 constexpr int kWaitTries = 1 << 25;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed, int tries)
 {
     if (bar_try(bar, parity)) return true;
-    for (int i = 1; i < kWaitTries; ++i) {
+    for (int i = 1; i < tries; ++i) {
         if (bar_try(bar, parity)) return true;
         if ((i & 255) == 0 && *failed) return false;
     }
