@@ -74,7 +74,7 @@ typedef enum crmsn_status {
     CRMSN_ERR_WORKSPACE = 6,      /* backward workspace too small or misaligned */
     CRMSN_ERR_ALIAS = 7,          /* outputs overlap inputs other than as allowed */
     CRMSN_ERR_CUDA = 8,           /* the CUDA runtime reported an error */
-    CRMSN_ERR_DEVICE_TIMEOUT = 9, /* reserved: no entry point returns it */
+    CRMSN_ERR_DEVICE_TIMEOUT = 9, /* attention_status: a wait inside a kernel ran out */
     CRMSN_ERR_ARG = 10,           /* eps / scale value out of range */
     CRMSN_ERR_SCRATCH_LIMIT = 11, /* rmsnorm_bwd_noalloc: problem needs more than its built-in scratch */
     CRMSN_ERR_NOT_DEBUG_BUILD = 12 /* crmsn_debug_status: the library has no bounds guard */
@@ -584,8 +584,10 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     token's, or one before its window; up to 256 rows share their keys) is
  *     worked out again key by key, about 11 us for each key of 32 such rows;
  *     over an E5M2 cache with infinities, a row that sees one as well.
- *   - The waits between the parts of a kernel are bounded (about 6 s); one that
- *     ran out leaves NaN.  Rows are worked out again where nothing waits.
+ *   - The waits between the parts of a kernel are bounded (about 6 s), and no
+ *     input keeps one that long: rows are worked out again where nothing waits.
+ *     Were one to run out all the same, all rows (and lse) of its thread block
+ *     would be NaN, and attention_status would say so.
  */
 typedef struct crmsn_attention {
     int64_t T, D, Hq, Hk, B;
@@ -621,6 +623,14 @@ typedef struct crmsn_paged_attention_call {
 
 /* Bytes of workspace for head size D on `device`; 0 for an invalid D or device. */
 size_t attention_workspace_bytes(int64_t D, int device);
+
+/*
+ * attention_status -- waits for the current device; CRMSN_ERR_DEVICE_TIMEOUT if
+ * a wait inside one of the attention functions' kernels has run out there since
+ * the last call of this function (*blocks, nullable: in how many thread
+ * blocks), else CRMSN_OK.  Not during a stream capture.
+ */
+crmsn_status attention_status(uint64_t *blocks);
 
 crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStream_t stream);
 

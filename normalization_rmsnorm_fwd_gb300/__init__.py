@@ -10,6 +10,7 @@ from .binding import (  # noqa: F401
     ada_rms_norm_style,
     as_heads,
     as_rows,
+    attention_status,
     attention_workspace_bytes,
     fused_add_rmsnorm_fp8_block_quant,
     fused_add_rmsnorm_quant,

@@ -43,6 +43,7 @@ SIGNATURES = {
     "prompt_attention": (_ST, [ctypes.c_char_p, _P]),
     "paged_attention": (_ST, [ctypes.c_char_p, _P]),
     "attention_workspace_bytes": (ctypes.c_size_t, [_I, _INT]),
+    "attention_status": (_ST, [ctypes.POINTER(ctypes.c_uint64)]),
     "crmsn_debug_status": (_ST, [ctypes.POINTER(ctypes.c_uint64)]),
 }
 

@@ -755,6 +755,14 @@ def attention_workspace_bytes(D: int, device=None) -> int:
     return n
 
 
+def attention_status(device=None) -> None:
+    """Waits for `device` (default: the current one); raises CrmsnError if a
+    wait inside an attention kernel has run out there since the last call of
+    this function (rows of NaN, which no input causes)."""
+    with torch.cuda.device(device):
+        check("attention_status", _lib().attention_status(None))
+
+
 _I32 = torch.int32
 
 

@@ -117,6 +117,20 @@ size_t attention_workspace_bytes(int64_t D, int device)
     return (size_t)(kAttnParts + parts * (int64_t)sizeof(float) + 255) / 256 * 256;
 }
 
+crmsn_status attention_status(uint64_t *blocks)
+{
+    if (blocks) *blocks = 0;
+    if (cudaError_t e = cudaDeviceSynchronize()) return launched(e);
+    uint64_t sum = 0;
+    for (const auto take : {take_given_up_bf16, take_given_up_e4m3, take_given_up_e5m2}) {
+        unsigned int n = 0;
+        if (cudaError_t e = take(n)) return launched(e);
+        sum += n;
+    }
+    if (blocks) *blocks = sum;
+    return sum ? CRMSN_ERR_DEVICE_TIMEOUT : CRMSN_OK;
+}
+
 crmsn_status prompt_attention(const crmsn_prompt_attention_call *call, cudaStream_t stream)
 {
     if (!call) return CRMSN_ERR_NULL;

@@ -102,6 +102,10 @@ inline int attn_tile_rows(int DP) { return DP > 192 ? 128 : 256; }
 cudaError_t launch_attn_tile_bf16(const AttnParams &p, int sms, cudaStream_t s);
 cudaError_t launch_attn_tile_e4m3(const AttnParams &p, int sms, cudaStream_t s);
 cudaError_t launch_attn_tile_e5m2(const AttnParams &p, int sms, cudaStream_t s);
+// CTAs of the current device whose waits ran out since the last call; waits for the device's legacy stream.
+cudaError_t take_given_up_bf16(unsigned int &n);
+cudaError_t take_given_up_e4m3(unsigned int &n);
+cudaError_t take_given_up_e5m2(unsigned int &n);
 
 // One warp for each row (attn_row.cu): any layout and head size.
 cudaError_t launch_attn_row(const AttnParams &p, int sms, cudaStream_t s);

@@ -184,6 +184,40 @@ struct __align__(16) Piece {
 enum { PIECE_BEGINS = 1, PIECE_ENDS = 2, PIECE_NONE = 4 };   // the tile's first block, its last; no piece: the end
 constexpr int kPieces = 8;
 
+// CTAs whose waits ran out since this was last read (by their element kind).
+static __device__ unsigned int g_given_up;
+static cudaError_t take_given_up(unsigned int &n)
+{
+    const unsigned int zero = 0;
+    if (cudaError_t e = cudaMemcpyFromSymbol(&n, g_given_up, sizeof n)) return e;
+    return n ? cudaMemcpyToSymbol(g_given_up, &zero, sizeof zero) : cudaSuccess;
+}
+
+// A wait ran out: some pieces were not worked out, or not told at all.  NaN for
+// all of the CTA's rows, sums of logarithms and parts.
+template <int KIND, int DP>
+__device__ __noinline__ void give_up(const AttnParams &p, const Walk &begin)
+{
+    using S = TileShape<KIND, DP>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.group.d, TT = S::ROWS / G, h = (int)blockIdx.x % p.Hk;
+    if (threadIdx.x == 0) atomicAdd(&g_given_up, 1u);
+    Walk c = begin;
+    do {
+        const int tok = c.s.first + c.t * TT, rows = min(TT, c.s.n - c.t * TT) * G;
+        for (int r = warp; r < rows; r += 8) {
+            if (c.k == c.k0 && c.end == c.k1) {
+                const int i = p.group.div(r), hq = h * G + r - i * G;
+                uint16_t *const out = const_cast<uint16_t *>(p.out.p) + (int64_t)(tok + i) * p.out.ld + hq * p.out.hs;
+                for (int d = 2 * lane; d < p.D; d += 64)
+                    if (dbg_global(out + d, 4, true)) *reinterpret_cast<uint32_t *>(out + d) = 0x7fff7fffu;
+                if (p.lse && lane == 0) st_f32(p.lse + (int64_t)(tok + i) * p.out.H + hq, NAN);
+            } else if (lane < 2) {
+                st_f32(part_of(p.ws, blockIdx.x, c.k == c.k0, S::ROWS, DP) + 2 * r + lane, NAN);
+            }
+        }
+    } while (walk_on<S::BN>(p, TT, c));
+}
+
 // The rows of the pieces that are whole tiles, once more where a result is not
 // finite: 32 rows a warp.
 template <int KIND, int DP>
@@ -200,6 +234,17 @@ __device__ __noinline__ void look_again(const AttnParams &p, const Walk &begin)
             if (__any_sync(0xffffffffu, suspect)) work_out_again<KIND, DP / 32>(p, c.b, h, tok, ntok, t, hq, suspect);
         }
     } while (walk_on<S::BN>(p, TT, c));
+}
+
+// What is left to do behind all pieces, by the warps of the weights (those that
+// have not given their registers away): state 2, 3: a wait ran out; 1: some
+// result is not finite.  (One call: with two the 16384-token prompt took 1637 us
+// instead of 1622, as the loops before are compiled differently.)
+template <int KIND, int DP>
+__device__ __noinline__ void last_look(const AttnParams &p, const Walk &begin, int state)
+{
+    if (state & 2) give_up<KIND, DP>(p, begin);
+    else look_again<KIND, DP>(p, begin);
 }
 
 template <int KIND, int DP>
@@ -710,6 +755,7 @@ struct TileKernel {
         return FP8 ? fmaf(M, scale, (float)(kLag - kWeightTop)) : M * scale;
     }
 
+    // Ends at once where a wait ran out (give_up follows).
     __device__ __forceinline__ void weight_loop(int half)
     {
         const uint32_t lanes = (uint32_t)((threadIdx.x >> 5) & 3) << 21;       // lane 32 (warp % 4), in bits 16 up
@@ -717,7 +763,7 @@ struct TileKernel {
         const float c_all = FP8 ? p.qk_scale * ld_f32_ro(p.scale[0]) : p.qk_scale;
         Place place{0, 0};
         Piece c, nx;
-        bool any = next(place, nx), have = false, copied = false, good = true;
+        bool any = next(place, nx), have = false, copied = false;
         Row row;
         int e = 0;
         float scale = 0.f, M = 0.f, L = 0.f;                  // M: the reference, a raw score
@@ -725,14 +771,14 @@ struct TileKernel {
         for (;;) {
             // The next tile's queries first (its scores are worked out meanwhile), then this one's results.
             while (any && !used(nx, half)) any = next(place, nx);
-            if (any && good) {
+            if (any) {
                 if (!copied) copy_queries(nx, half);
                 e = queries_here(half, FP8 ? score_sign(c_all) : 0u);
             }
             if (have) {
-                if (good) good = wait_all(&sm.o[half], (cnt - 1) & 1);
+                if (!wait_all(&sm.o[half], (cnt - 1) & 1)) return;
                 tc_fence_after();
-                finish(c, half, row, reference(M, scale), L, vs, lanes, good);
+                finish(c, half, row, reference(M, scale), L, vs, lanes);
             }
             if (!any) return;
             c = nx;
@@ -743,19 +789,17 @@ struct TileKernel {
             M = -INFINITY;
             L = 0.f;
             int hk = key_hi(p, c.s, row.tok) - c.k * BN, lk = key_lo(p, c.s, row.tok) - c.k * BN;    // seen: [lk, hk) of the block
-            bool begun = false, told = false;
-            for (int n = c.end - c.k; n > 0 && good; --n, ++cnt, hk -= BN, lk -= BN) {
+            bool begun = false;
+            for (int n = c.end - c.k; n > 0; --n, ++cnt, hk -= BN, lk -= BN) {
                 const int buf = NS == 2 ? cnt & 1 : 0;
                 const uint32_t sc = s_col(half, buf) + lanes;
                 const bool edge = __any_sync(0xffffffffu, hk < BN || lk > 0);
-                good = wait_all(&sm.s[half * NS + buf], NS == 2 ? (cnt >> 1) & 1 : cnt & 1);
-                if (!good) break;
+                if (!wait_all(&sm.s[half * NS + buf], NS == 2 ? (cnt >> 1) & 1 : cnt & 1)) return;
                 tc_fence_after();
                 // The last scores are here: the next tile's queries may take the place of these.
                 if (__builtin_expect(n == 1, 0)) {
                     // (One piece ahead and no further: later ones may wait for what this half still owes.)
                     any = next(place, nx);
-                    told = true;
                     copied = any && used(nx, half);
                     if (copied) copy_queries(nx, half);
                 }
@@ -791,8 +835,7 @@ struct TileKernel {
                 // A new reference changes O, the products of the block before done.  (One S: they were issued before
                 // its products, and are done with them.)
                 if (NS == 2 && cnt > 0) {
-                    good = wait_all(&sm.o[half], (cnt - 1) & 1);
-                    if (!good) break;
+                    if (!wait_all(&sm.o[half], (cnt - 1) & 1)) return;
                     tc_fence_after();
                 }
                 if (__builtin_expect(__any_sync(0xffffffffu, (most - M) * scale > kLag || M == -INFINITY), 0)) {
@@ -840,18 +883,14 @@ struct TileKernel {
                 L += sum.x + sum.y;
                 ready_tmem(&sm.w[half * NS + buf][1]);
             }
-            // A wait that ran out: this half's rows are NaN from here on, as far as pieces are still told.
-            if (!told) any = next(place, nx);
         }
     }
 
-    // A row's result, or part.  good = false: a wait ran out, and the row is NaN.
-    __device__ __forceinline__ void finish(const Piece &c, int half, const Row &row, float M, float L, float vs, uint32_t lanes,
-                                           bool good) const
+    // A row's result, or part.
+    __device__ __forceinline__ void finish(const Piece &c, int half, const Row &row, float M, float L, float vs, uint32_t lanes) const
     {
         const int64_t t = c.s.first + row.tok;
         const int r = threadIdx.x & 127;
-        if (!good) L = NAN;
         // This code runs once for each tile, from a cold instruction cache: a short loop is faster than a long one
         // unrolled.  16 columns at a time are two chunks of a result, four of a part.
         const bool whole = (c.flags & (PIECE_BEGINS | PIECE_ENDS)) == (PIECE_BEGINS | PIECE_ENDS);
@@ -866,7 +905,7 @@ struct TileKernel {
         } else {
             float *part = part_of(p.ws, blockIdx.x, c.flags & PIECE_BEGINS, S::ROWS, DP);
             if (row.valid) {
-                st_f32(part + 2 * (half * 128 + r), good ? M : 0.f);
+                st_f32(part + 2 * (half * 128 + r), M);
                 st_f32(part + 2 * (half * 128 + r) + 1, L);
             }
             to = reinterpret_cast<uint8_t *>(part + 2 * S::ROWS + (int64_t)(half * 128 + r) * DP);
@@ -1082,18 +1121,20 @@ struct TileKernel {
         if (warp < 8) {
             more_registers<S::REGS>();
             if (warp < 4 * NT) weight_loop(warp >> 2);
+            copy_wait_all();
             asm volatile("bar.sync 1, 256;" ::: "memory");    // all results are written
-            if (sm.odd) look_again<KIND, DP>(p, sm.begin);
+            if (const int state = sm.failed * 2 | sm.odd) last_look<KIND, DP>(p, sm.begin, state);
         } else {
             fewer_registers<S::OTHER_REGS>();
             if (warp < 12) {
                 if constexpr (FP8) convert_loop();
                 else copy_loop();
-                copy_wait<0>();
+                copy_wait_all();
             } else if (warp == 12) {
                 issue_loop();
                 __syncwarp();
-                if (sm.failed && lane == 0) {                 // products in flight end before their memory goes
+                // Products in flight end before their memory goes, whatever became of the waits.
+                if (elect_one()) {
                     products_done(at(&sm.last));
                     for (int i = 0; i < kWaitTries && !bar_try(at(&sm.last), 0); ++i) {}
                 }
@@ -1102,7 +1143,7 @@ struct TileKernel {
                 tell_loop(c);
             } else if (FP8) {
                 code_loop();
-                copy_wait<0>();
+                copy_wait_all();
             }
         }
     }

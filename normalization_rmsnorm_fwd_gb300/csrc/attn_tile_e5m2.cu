@@ -13,4 +13,6 @@ cudaError_t launch_attn_tile_e5m2(const AttnParams &p, int sms, cudaStream_t s)
     }
 }
 
+cudaError_t take_given_up_e5m2(unsigned int &n) { return take_given_up(n); }
+
 }  // namespace crmsn
