@@ -576,8 +576,12 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     paged_attention: table_pages * page_size).
  *   - The outputs may not overlap any input.
  *   - The order of the sums of a row depends on the lengths of all sequences
- *     of the call, the head counts, the form (the alignment rule above) and the
- *     SM count, and on nothing else.
+ *     of the call, the head counts, D, causal and window, the cache kind,
+ *     whether starts is given, whether no sequence can have more than
+ *     CRMSN_ATTENTION_SHORT keys (above: for paged_attention the width of the
+ *     page table says so), the form (the alignment rule above) and the SM
+ *     count.  Not on strides within a form, page numbers, page sizes, what the
+ *     workspace holds or whether lse is asked for.
  *   - Infinite and NaN values that a row sees reach its result as they are
  *     (times a weight that FP32 rounds to 0: NaN) and cost no time worth
  *     mentioning.  A row that does not see one which a neighbour does (a later

@@ -200,3 +200,113 @@ def test_a_cache_of_nan_costs_no_time(dtype, n):
     f = lambda c: crm.paged_attention(q, kc, c, table, int32(20000), k_scale=ks, v_scale=vs)
     assert f(bad).isnan().all() and f(vc).isfinite().all()
     assert microseconds(lambda: f(bad), 5) < 2 * microseconds(lambda: f(vc), 5) + 100
+
+
+# -------------------------------------------------------- calls as allowed --
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("page,capacity", [(16, 624), (16, 640), (16, 656), (1, 639), (1, 640), (1, 641)])
+def test_paged_calls_around_the_short_form(n, dtype, page, capacity):
+    # The table's width decides: up to 640 keys no workspace, whole tiles.
+    g = gen(page, capacity)
+    lens = [capacity, max(n, 7), capacity // 2]
+    kc, vc, table, ks, vs = cache(g, lens, page, 2, 128, dtype, junk=NAN)
+    table = table[:, :capacity // page].contiguous()
+    assert table.shape[1] * page == capacity
+    q = normal(g, 3 * n, 8, 128).to(BF16)
+    o, tol, l, ltol = attn_ref.paged(q, kc, vc, table, lens, [n] * 3, ks, vs)
+    for starts in (None, starts_of([n] * 3)):
+        lse = torch.full(q.shape[:2], NAN, device=DEV)
+        out = crm.paged_attention(q, kc, vc, table, int32(*lens), starts=starts, k_scale=ks, v_scale=vs, lse=lse)
+        attn_ref.check(out, o, tol)
+        attn_ref.check(lse, l, ltol, "lse")
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_page_tables_of_any_row_stride(n):
+    # One table for all sequences, and the first columns of a wider one.
+    g = gen(n)
+    kc, vc, table, _, _ = cache(g, [900], 16, 2, 128)
+    q = normal(g, 5 * n, 8, 128).to(BF16)
+    lens = [900, n, 333, 0, 512]
+    o, tol, _, _ = attn_ref.paged(q, kc, vc, table.expand(5, -1), lens, [n] * 5)
+    wide = torch.full((5, table.shape[1] + 9), -7, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    for t in (table.expand(5, -1), wide[:, :table.shape[1]]):
+        attn_ref.check(crm.paged_attention(q, kc, vc, t, int32(*lens)), o, tol)
+
+
+@pytest.mark.parametrize("T", [400, 1500])
+def test_graph_replays_follow_the_starts(T):
+    # A captured step over packed prompts whose borders change; tokens of none stay as they are.
+    g = gen(T)
+    q, k, v = heads(g, T, 8, 2, 128)
+    starts = starts_of([T // 2, T - T // 2, 0, 0])
+    out = torch.empty_like(q.contiguous())
+    crm.prompt_attention(q, k, v, starts=starts, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        crm.prompt_attention(q, k, v, starts=starts, out=out)
+    for ns in ([T // 2, T - T // 2, 0, 0], [1, 0, T - 41, 0], [0, 0, 0, 77], [0, 0, 0, 0]):
+        starts.copy_(starts_of(ns))
+        out.fill_(3.0)
+        graph.replay()
+        n = sum(ns)
+        if n:
+            o, tol, _, _ = attn_ref.prompt(q, k, v, ns)
+            attn_ref.check(out[:n], o, tol)
+        assert (out[n:] == 3).all()
+
+
+@pytest.mark.parametrize("D", [64, 100])
+def test_a_million_sequences(D):
+    # Nearly all of them empty, or of a token each.
+    B = 1 << 20
+    ns = torch.zeros(B, dtype=torch.int64)
+    ns[5], ns[B // 2], ns[B - 2] = 300, 1, 500
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), ns.cumsum(0)]).to(device=DEV, dtype=torch.int32)
+    q, k, v = heads(gen(D), 801, 4, 2, D)
+    o, tol, _, _ = attn_ref.prompt(q, k, v, [300, 1, 500])
+    attn_ref.check(crm.prompt_attention(q, k, v, starts=starts), o, tol)
+    q = normal(gen(D, 1), B, 2, D).to(BF16)
+    kc, vc = normal(gen(D, 2), 2, 1, 1, 1, D).to(BF16)
+    one = torch.ones(B, dtype=torch.int32, device=DEV)
+    out = crm.paged_attention(q, kc, vc, torch.zeros(B, 1, dtype=torch.int32, device=DEV), one)
+    assert torch.equal(out, vc[0].expand(B, 2, D))                            # one key: its value
+
+
+# ------------------------------------------------------- the order of sums --
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("ns", [[1, 1, 1], [20, 300, 1]])
+def test_bits_depend_on_what_the_contract_names(dtype, ns):
+    # Not on where pages lie, on their size, on the layout of a slot, on the workspace or on whether lse is asked for.
+    g = gen(len(ns), ns[0])
+    lens, Hk, D = [3000, 1024, 1999], 2, 128
+    kc, vc, table, ks, vs = cache(g, lens, 16, Hk, D, dtype)
+    table = table[:, :192].contiguous()
+    q = normal(g, sum(ns), 8, D).to(BF16)
+    starts = None if len(set(ns)) == 1 else starts_of(ns)
+    how = dict(starts=starts, k_scale=ks, v_scale=vs)
+    want = crm.paged_attention(q, kc, vc, table, int32(*lens), **how)
+    lse = torch.empty(q.shape[:2], device=DEV)
+    ws = torch.full((crm.attention_workspace_bytes(D),), 0x5a, dtype=torch.uint8, device=DEV)
+    assert torch.equal(want, crm.paged_attention(q, kc, vc, table, int32(*lens), lse=lse, workspace=ws, **how))
+    perm = torch.randperm(kc.shape[0], generator=g, device=DEV)
+    back = perm.argsort().to(torch.int32)
+    moved = torch.where((table >= 0) & (table < kc.shape[0]), back[table.clamp(0, kc.shape[0] - 1).long()], table)
+    swap = lambda t: t.view(torch.uint8)[perm].view(t.dtype) if dtype != BF16 else t[perm]
+    assert torch.equal(want, crm.paged_attention(q, swap(kc), swap(vc), moved, int32(*lens), **how))
+    lay = lambda t: t.transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(want, crm.paged_attention(q, lay(kc), lay(vc), table, int32(*lens), **how))
+    # The same keys in pages of 48.
+    wide = torch.zeros(3 * 64, 48, Hk, D, device=DEV)
+    big = [wide.to(dtype).clone() for _ in range(2)]
+    for b, m in enumerate(lens):
+        for t, c in zip(big, (kc, vc)):
+            rows = attn_ref.cached(c, table[b], m).to(F32).to(dtype)
+            t.view(3, 64 * 48, Hk, D)[b, :m] = rows
+    table48 = torch.arange(3 * 64, dtype=torch.int32, device=DEV).view(3, 64)
+    assert torch.equal(want, crm.paged_attention(q, big[0], big[1], table48, int32(*lens), **how))
