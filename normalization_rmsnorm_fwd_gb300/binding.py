@@ -838,7 +838,8 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, starts=None, scale=No
     names the first of each sequence, None: the tokens are shared out evenly
     (one each: a decode step).  The rest as in prompt_attention."""
     dev, shape, T, Hq, D = _first_head_tensor(q, "q")
-    if torch.is_grad_enabled() and q.requires_grad:
+    if torch.is_grad_enabled() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or
+                                    any(s is not None and s.requires_grad for s in (k_scale, v_scale))):
         raise RuntimeError("paged_attention has no gradient: call it under torch.no_grad()")
     ck = _CACHE.get(k_cache.dtype)
     if ck is None or v_cache.dtype is not k_cache.dtype or k_cache.get_device() != dev or v_cache.get_device() != dev:

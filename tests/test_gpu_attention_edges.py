@@ -310,3 +310,19 @@ def test_bits_depend_on_what_the_contract_names(dtype, ns):
             t.view(3, 64 * 48, Hk, D)[b, :m] = rows
     table48 = torch.arange(3 * 64, dtype=torch.int32, device=DEV).view(3, 64)
     assert torch.equal(want, crm.paged_attention(q, big[0], big[1], table48, int32(*lens), **how))
+
+
+def test_a_cache_that_records_gradients_is_refused():
+    g = gen(1)
+    kc, vc, table, _, _ = cache(g, [40], 16, 2, 128)
+    q = normal(g, 1, 4, 128).to(BF16)
+    for a, b in ((kc.clone().requires_grad_(), vc), (kc, vc.clone().requires_grad_())):
+        with pytest.raises(RuntimeError):
+            crm.paged_attention(q, a, b, table, int32(40))
+        with torch.no_grad():
+            crm.paged_attention(q, a, b, table, int32(40))
+    k8, v8 = kc.to(E4M3), vc.to(E4M3)
+    one = torch.ones(1, device=DEV)
+    for a, b in ((one.clone().requires_grad_(), one), (one, one.clone().requires_grad_())):
+        with pytest.raises(RuntimeError):
+            crm.paged_attention(q, k8, v8, table, int32(40), k_scale=a, v_scale=b)
