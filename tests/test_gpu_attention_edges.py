@@ -326,3 +326,18 @@ def test_a_cache_that_records_gradients_is_refused():
     for a, b in ((one.clone().requires_grad_(), one), (one, one.clone().requires_grad_())):
         with pytest.raises(RuntimeError):
             crm.paged_attention(q, k8, v8, table, int32(40), k_scale=a, v_scale=b)
+
+
+def test_empty_sequences_between_others_cost_no_time():
+    # A CTA whose work goes on behind thousands of sequences without tokens.
+    some = [3000] * 60 + [300], [1] * 64 + [200]
+    T = sum(some[0] + some[1])
+    q, k, v = heads(gen(1), T, 4, 2, 64)
+    apart, together = some[0] + [0] * 20000 + some[1] + [0] * 77, some[0] + some[1]
+    one, two = starts_of(apart), starts_of(together)
+    outs = [crm.prompt_attention(q, k, v, starts=s) for s in (one, two)]
+    o, tol, _, _ = attn_ref.prompt(q[-264:], k[-264:], v[-264:], some[1])
+    for out in outs:
+        attn_ref.check(out[-264:], o, tol)
+    assert torch.equal(*outs)
+    assert microseconds(lambda: crm.prompt_attention(q, k, v, starts=one), 5) < microseconds(lambda: crm.prompt_attention(q, k, v, starts=two), 5) + 300
