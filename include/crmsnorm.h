@@ -564,7 +564,7 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     starts[b + 1] - 1 (I32 [B + 1] on the device, not decreasing, in [0, T]);
  *     starts NULL: T / B tokens each.  Tokens of no sequence are neither read
  *     nor written.
- *   - window: 0: none.
+ *   - scale > 0, scale * log2(e) finite in FP32.  window: 0: none.
  *   - Any layout and D is accepted (D even, at most CRMSN_MAX_HEAD_DIM); the
  *     fast forms want D a multiple of 8 and at most 256, every stride a
  *     multiple of 8 elements (FP8 caches: 16) and every base 16-byte aligned.

@@ -14,6 +14,7 @@ using namespace crmsn;
 namespace {
 
 constexpr int64_t kMaxSequences = 1 << 20, kMaxGroup = 128;
+constexpr float kLog2e = 1.44269504f;
 
 // What both functions check first; on CRMSN_OK with no tokens there is nothing
 // to launch.
@@ -24,7 +25,7 @@ crmsn_status check_common(const crmsn_attention &a)
     if (a.D < 1) return CRMSN_ERR_SHAPE;
     if (a.D > CRMSN_MAX_HEAD_DIM || (a.D & 1)) return CRMSN_ERR_UNSUPPORTED_H;
     if (!a.starts && (a.B ? a.T % a.B : a.T)) return CRMSN_ERR_SHAPE;
-    if (!std::isfinite(a.scale) || a.scale <= 0.f || a.window < 0 || (a.window && !a.causal)) return CRMSN_ERR_ARG;
+    if (!std::isfinite(a.scale * kLog2e) || !(a.scale > 0.f) || a.window < 0 || (a.window && !a.causal)) return CRMSN_ERR_ARG;
     if (a.T == 0 || a.B == 0) return CRMSN_OK;
     const Heads q = heads(a.q, a.Hq), out = heads(a.out, a.Hq);
     if (crmsn_status s = check_heads(q, a.T, a.D)) return s;
@@ -74,7 +75,7 @@ void set_common(AttnParams &p, const crmsn_attention &a, int64_t keys)
     p.group = FastDiv((int)(a.Hq / a.Hk));
     p.causal = a.causal != 0;
     p.window = a.window < kMaxTokens ? (int)a.window : 0;      // no sequence is longer
-    p.qk_scale = a.scale * 1.44269504f;
+    p.qk_scale = a.scale * kLog2e;
     p.lse = a.lse;
     p.ws = static_cast<uint8_t *>(a.workspace);
 #ifdef CRMSN_DEBUG
