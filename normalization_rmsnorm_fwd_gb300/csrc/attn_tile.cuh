@@ -76,25 +76,25 @@ constexpr int kLag = 8;              // binary digits by which a row's reference
 constexpr int kTileThreads = 512;
 constexpr int kTileColumns = 512;
 
-// sum of floor((a i + b) / m) over 0 <= i < n (the classic Euclid-like
-// reduction of a count of lattice points under a line).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b)
+// Sum of floor((b + a i) / 2^lb) over 0 <= i < n; a > 0, b >= 0.  The terms
+// themselves add up to n b + a n (n - 1) / 2.  What the divisions leave over is
+// their remainders: these repeat after P = 2^lb / g terms, g the greatest power
+// of two in a and 2^lb, and are in some order the numbers below 2^lb that are b
+// modulo g; so whole periods are known, and the rest, at most 127 terms, are
+// added one by one.
+__device__ __forceinline__ int64_t quotient_sum(int64_t n, int lb, int a, int64_t b)
 {
-    int64_t sum = 0;
-    while (n > 0) {
-        const int64_t qa = quotient(a, m), qb = quotient(b, m);
-        sum += n * (n - 1) / 2 * qa + n * qb;
-        a -= qa * m;
-        b -= qb * m;
-        const int64_t y = a * n + b;
-        if (y < m) break;
-        n = quotient(y, m);
-        b = y - n * m;
-        const int64_t t = m;
-        m = a;
-        a = t;
+    if (n <= 0) return 0;
+    const int lg = min(__ffs(a) - 1, lb), mask = (1 << lb) - 1;
+    const int64_t P = 1 << (lb - lg);
+    int64_t over = (n >> (lb - lg)) * (P * (b & ((1 << lg) - 1)) + ((P * (P - 1) / 2) << lg));
+    int x = (int)(b & mask), some = 0;
+    for (int i = (int)(n & (P - 1)); i > 0; --i) {
+        some += x;
+        x = (x + a) & mask;
     }
-    return sum;
+    over += some;
+    return (n * b + a * (n * (n - 1) / 2) - over) >> lb;
 }
 
 // What a tile costs beside its blocks (its queries' and results' ways, the
@@ -113,13 +113,13 @@ __device__ __forceinline__ void tile_blocks(const AttnParams &p, const Seq &s, i
     k0 = key_lo(p, s, t * TT) / BN;
     k1 = max((key_hi(p, s, last) + BN - 1) / BN, k0 + 1);
 }
-// Blocks of BN keys of the first t of a sequence's nt tiles, in closed form.
+// Blocks of BN (a power of two) keys of the first t of a sequence's nt tiles, in closed form.
 // (Not inlined: it is called three times, and the start of a small call is
 // the time that its code takes to arrive.)
 static __device__ __noinline__ int64_t blocks_before(int BN, int n, int m, int causal, int window, int TT, int nt, int t)
 {
     if (t <= 0) return 0;
-    const int all = (m + BN - 1) / BN;
+    const int lb = __ffs(BN) - 1, all = (m + BN - 1) >> lb;
     if (!causal) return (int64_t)t * max(all, 1);
     const int64_t off = (int64_t)m - n;
     int64_t sum = 0;
@@ -127,14 +127,14 @@ static __device__ __noinline__ int64_t blocks_before(int BN, int n, int m, int c
     if (last) --t;
     // Tiles whose tokens all stand before the first key: one block each.
     const int64_t z = off < 0 ? min(quotient(-off, TT), (int64_t)t) : 0;
-    sum += z + floor_sum(t - z, BN, TT, off + (z + 1) * TT + BN - 1);
+    sum += z + quotient_sum(t - z, lb, TT, off + (z + 1) * TT + BN - 1);
     const int64_t gap = window - 1 - off;            // the first tiles' windows reach the first key
     if (window) {
         const int64_t y = max(z, gap > 0 ? quotient(gap + TT - 1, TT) : (int64_t)0);
-        if (y < t) sum -= floor_sum(t - y, BN, TT, off + 1 - window + y * TT);
+        if (y < t) sum -= quotient_sum(t - y, lb, TT, off + 1 - window + y * TT);
     }
     if (last) {
-        const int64_t lo = window ? max(off + (int64_t)t * TT + 1 - window, (int64_t)0) : 0, k0 = quotient(lo, BN);
+        const int64_t lo = window ? max(off + (int64_t)t * TT + 1 - window, (int64_t)0) : 0, k0 = lo >> lb;
         sum += max((int64_t)all, k0 + 1) - k0;
     }
     return sum;
