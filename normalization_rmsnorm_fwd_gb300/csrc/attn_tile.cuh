@@ -64,10 +64,12 @@ struct TileShape {
     static constexpr int SMEM = 1024 + NT * QBYTES + STAGES * STAGE + RAWS * RAW;
     static constexpr int OCOL = DP == 256 ? 256 : NT * NS * BN;   // columns of S, then of O
     // Registers of a thread: of the 128 at launch the copying and the issuing
-    // warps give up what the weights' warps need.  (BF16: 16384 tokens 1530 us at
-    // 152, 1450 at 168; FP8, whose copying warps convert: a chunk among single
-    // tokens 210 us at 168, 196 at 152.)
-    static constexpr int REGS = FP8 ? 152 : 168, OTHER_REGS = 256 - REGS;
+    // warps give up what the weights' warps need.  The loops that the compiler
+    // makes of it differ from step to step and not in one direction (BF16, by the
+    // call: 16384 tokens 1577, 1966, 1610, 1670 us at 144, 152, 160, 168, 24 packed
+    // prompts 460, 565, 476, 483; FP8, whose copying warps convert: a chunk among
+    // single tokens 200, 200, 221 at 144, 152, 160).
+    static constexpr int REGS = FP8 ? 152 : 144, OTHER_REGS = 256 - REGS;
     static_assert(OCOL + NT * DP <= 512, "tensor memory");
     static constexpr int STATIC = 2048;                      // for what is not dynamic
     static_assert(SMEM + STATIC <= 227 * 1024, "shared memory");
