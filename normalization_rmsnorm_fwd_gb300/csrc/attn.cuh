@@ -300,6 +300,7 @@ __device__ __noinline__ void work_out_again(const AttnParams &p, int b, int h, i
     const Seq s = sequence(p, b);
     const int i = t - s.first;
     const int lo = key_lo(p, s, i), hi = key_hi(p, s, i);
+    suspect = suspect && lo < hi;                 // (without keys: the scales are to blame)
     const int first_hi = __reduce_min_sync(0xffffffffu, suspect ? hi : kNone), last_lo = __reduce_max_sync(0xffffffffu, suspect ? lo : 0);
     const BadValues above = bad_values<KIND, V_BAD>(p, b, s, h, first_hi, key_hi(p, s, tok - s.first + ntok - 1), 0, 0);
     const BadValues below = bad_values<KIND, V_BAD>(p, b, s, h, key_lo(p, s, tok - s.first), last_lo, 0, 0);

@@ -8,7 +8,9 @@ import torch
 
 import attn_ref
 import normalization_rmsnorm_fwd_gb300 as crm
+from normalization_rmsnorm_fwd_gb300 import _abi, build
 from test_gpu_attention import BF16, DEV, E4M3, E5M2, F32, INF, NAN, cache, gen, heads, normal, starts_of
+from test_gpu_debug_guard import run_both
 
 pytestmark = pytest.mark.gpu
 
@@ -341,3 +343,25 @@ def test_empty_sequences_between_others_cost_no_time():
         attn_ref.check(out[-264:], o, tol)
     assert torch.equal(*outs)
     assert microseconds(lambda: crm.prompt_attention(q, k, v, starts=one), 5) < microseconds(lambda: crm.prompt_attention(q, k, v, starts=two), 5) + 300
+
+
+@pytest.mark.parametrize("n,m", [(60, 30), (4, 2), (300, 200)])
+@pytest.mark.parametrize("bad", ["k_scale", "v_scale"])
+def test_rows_without_keys_and_scales_of_nan(monkeypatch, n, m, bad):
+    # Rows before the first key are not finite here, and a value that they do not see is bad: none of it leads a look
+    # outside the cache (the debug build reports accesses).
+    dbg = _abi.load(build.build(debug=True))
+
+    def case():
+        g = gen(n)
+        kc, vc, table, ks, vs = cache(g, [m, m], 16, 2, 128, E4M3)
+        vc[int(table[0, (m - 1) // 16]), (m - 1) % 16] = NAN
+        if bad == "k_scale":
+            ks = torch.full_like(ks, NAN)
+        else:
+            vs = torch.full_like(vs, NAN)
+        q = normal(g, 2 * n, 8, 128).to(BF16)
+        return [crm.paged_attention(q, kc, vc, table, int32(m, m), k_scale=ks, v_scale=vs),
+                crm.paged_attention(q, kc, vc, table, int32(m, m), k_scale=ks, v_scale=vs, starts=starts_of([n, n]))]
+
+    run_both(dbg, monkeypatch, case)
