@@ -583,12 +583,14 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     count.  Not on strides within a form, page numbers, page sizes, what the
  *     workspace holds or whether lse is asked for.
  *   - Infinite and NaN values that a row sees reach its result as they are
- *     (times a weight that FP32 rounds to 0: NaN) and cost no time worth
- *     mentioning.  A row that does not see one which a neighbour does (a later
- *     token's, or one before its window; up to 256 rows share their keys) is
- *     worked out again key by key, about 11 us for each key of 32 such rows;
- *     over an E5M2 cache with infinities, a row that sees one as well.
- *   - The waits between the parts of a kernel are bounded (about 6 s), and no
+ *     (times a weight that FP32 rounds to 0: NaN) and cost a look at the values
+ *     beside the row (a prompt of 4096 tokens with 32 + 8 heads of 128 takes
+ *     0.33 to 0.40 ms instead of 0.14, of 16384 2.2 to 2.5 instead of 1.4).  A
+ *     row that does not see one which a neighbour does (a later token's, or one
+ *     before its window; up to 256 rows share their keys) is worked out again
+ *     key by key, about 16 us for each key of 32 such rows; over an E5M2 cache
+ *     with infinities, a row that sees one as well.
+ *   - The waits between the parts of a kernel are bounded (seconds), and no
  *     input keeps one that long: rows are worked out again where nothing waits.
  *     Were one to run out all the same, all rows (and lse) of its thread block
  *     would be NaN, and attention_status would say so.

@@ -83,9 +83,18 @@ inline int attn_groups(int sms, int Hk)
 inline int64_t attn_part_floats(int rows, int DP) { return (int64_t)rows * (2 + DP); }
 
 // Sequences of at most this many keys are dealt out by whole tiles, without a
-// count of their blocks and without a second kernel.  (A call of 77 tokens 9.0 us instead of 16.2; one token over 517 keys, 8
-// key heads, 9.8 instead of 7.2, but the host's 13.4 instead of 20.3 for one
-// launch and one allocation less.  Each further 128 keys cost 0.6 us.)
+// count of their blocks and without a second kernel.  Dealt whole against shared
+// out, device us, heads of 128 in BF16 (by the call a lone short sequence takes
+// 13.9 us against 19 to 20, for one launch and one allocation less):
+//                             128 keys     384        640       1024       2048
+//   1 token, 32 + 8 heads    4.6   6.2   7.3  7.7  10.0  7.9  13.8  8.5  24   10
+//   16 of them               4.9   6.7   7.7 12.3  10.4 15.1  14.4 17.8  28   32
+//   128 of them               23    24    49   53    69   72   100  100  184  179
+//   16 of them, 16 + 16      7.5   9.3    13   17    18   22    29   32   51   52
+//   a prompt, 32 + 8         9.4  14.4  12.5 19.2  16.0 26.8  20.9 34.0   62   58
+//   8 prompts               10.6  15.4    29   39    56   68   104  106  344  275
+// Only the lone token loses on the device from about 400 keys on, 2 us at the
+// threshold; all others gain to 1024 and lose by 2048.
 constexpr int kShortKeys = CRMSN_ATTENTION_SHORT;
 
 // Joins the parts of the tiles that several CTAs shared (attn_combine.cu).

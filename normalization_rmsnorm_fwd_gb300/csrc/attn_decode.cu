@@ -10,9 +10,9 @@
 // end of a tile (the keys of one sequence and head), whose parts are then
 // joined.  The ring runs on across the ends of tiles.  The keys are shared out
 // evenly over the CTAs (attn.cuh).  128 sequences of up to 8192 keys, 32 + 8
-// heads of 128 in BF16: 378 us, 6.5 TB/s, 96 % of the copy rate.  FP8: half the
-// bytes for the same instructions; 2 x 131071 keys in E4M3 take 100 us (79 %),
-// with the issue slots 45 % and the arithmetic pipe 40 % busy and two warps a
+// heads of 128 in BF16: 368 us, 6.7 TB/s, 98 % of the copy rate.  FP8: half the
+// bytes for the same instructions; 2 x 131071 keys in E4M3 take 102 us (78 %),
+// with the issue slots 44 % and the arithmetic pipe 40 % busy and two warps a
 // scheduler to hide it behind.
 //
 // Layouts.  Slots hold rows of DP elements with their 16-byte chunks permuted

@@ -30,16 +30,18 @@
 // Work is shared out by blocks (share_work): CTAs that meet inside a tile write
 // parts, which attn_combine.cu joins.
 //
-// What it takes (GB300, 32 + 8 heads of 128): 16384 tokens 1501 us, 1465
-// TFLOP/s, 75 % of the measured rate of a large BF16 product; 2048 tokens over
-// 32768 keys in pages of 64, 759 us.  What bounds it: a block of 128 keys takes
-// about 3000 cycles for two halves, whose products alone take 2048.  A half's
-// round (scores, 270 for their maximum, 1200 for the weights, products) is
-// longer than the other half's products; with nothing to load the prompt takes
-// 1389 us, and without a single power of two as long as with them.  A piece's
-// end costs some 4000 cycles, mostly instructions that arrive from the L2 cache:
-// this kernel's code is larger than the SM keeps, and shorter loops at a tile's
-// end were faster than unrolled ones.  Tried and left: the halves of a tile of
+// What it takes (GB300, 32 + 8 heads of 128), call after call: 16384 tokens
+// 1556 us, 1413 TFLOP/s, 72 % of the rate of a large BF16 product alone and 82 %
+// of its rate under the power cap, which holds here too (1750 to 1900 MHz; after
+// a pause, at 2070 MHz, 1430 us); 2048 tokens over 32768 keys in pages of 64,
+// 806 us (736).  What bounds it: the products of two halves over 128 keys take
+// 2048 cycles, their round longer: a half's scores, 270 cycles for their maximum,
+// 1200 for the weights and its products do not fit behind the other half's
+// products (an earlier form took 3000, and 1389 of 1501 us with nothing to load).
+// A piece's end costs some 4000 cycles, mostly instructions that arrive from the
+// L2 cache: this kernel's code is larger than the SM keeps, and shorter loops at
+// a tile's end were faster than unrolled ones.  Halves in turn and a reference
+// that may lag are published techniques for these tensor cores.  Tried and left: the halves of a tile of
 // 128 rows taking every other block (no faster: 222 against 215 us for one chunk
 // among single tokens), results staged in shared memory (a stage of keys less).
 #pragma once
