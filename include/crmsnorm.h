@@ -588,8 +588,10 @@ crmsn_status qk_rmsnorm_rope_append(const crmsn_qk_append_call *call, cudaStream
  *     0.33 to 0.40 ms instead of 0.14, of 16384 2.2 to 2.5 instead of 1.4).  A
  *     row that does not see one which a neighbour does (a later token's, or one
  *     before its window; up to 256 rows share their keys) is worked out again
- *     key by key, about 16 us for each key of 32 such rows; over an E5M2 cache
- *     with infinities, a row that sees one as well.
+ *     key by key, about 16 us for each key of 32 such rows.  Over an E5M2 cache
+ *     the look goes through all the values that the row sees, up to one of
+ *     nothing but NaN (about 0.1 us a key), and a row that sees an infinite one
+ *     is worked out again too.
  *   - The waits between the parts of a kernel are bounded (seconds), and no
  *     input keeps one that long: rows are worked out again where nothing waits.
  *     Were one to run out all the same, all rows (and lse) of its thread block
